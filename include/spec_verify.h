@@ -83,6 +83,12 @@ enum { SV_MODE_SAMPLE = 0, SV_MODE_GREEDY = 1 };
 #define SV_DATA_EMPTY_ROW 0x4u     /* a sampled row without any finite logit */
 #define SV_DATA_BAD_MODE 0x8u      /* mode[b] not SAMPLE or GREEDY (treated as SAMPLE) */
 #define SV_DATA_DEGENERATE_RESIDUAL 0x10u /* informational: residual mass 0 after a reject; drew from p */
+#define SV_DATA_BAD_LOGIT 0x40u    /* a NaN or +inf logit in a row (sv_token_logprobs) */
+#define SV_DATA_BAD_PAGE 0x80u     /* a page id outside the cache, a window beyond its page table, or a
+                                      reference count that does not fit the tables (cache calls) */
+#define SV_DATA_NO_PAGES 0x100u    /* the cache has too few free pages (sv_cache_reserve) */
+#define SV_DATA_BAD_SEQ 0x200u     /* a sequence index out of range, taken twice or not empty, or a
+                                      length out of range (cache calls) */
 #define SV_DEV_COPY_TIMEOUT 0x20u  /* a bounded wait for an asynchronous copy gave up (never expected);
                                       the call's outputs are invalid and the workspace must be
                                       zero-filled again before reuse */
@@ -389,6 +395,51 @@ sv_status sv_vshard_draw(const void* target, const void* draft, sv_dtype dtype, 
 sv_status sv_vshard_finish(const void* jobs, int32_t B, int32_t R_t, const int32_t* draw_tok,
                            const float* draw_prob, int32_t* out_tokens, float* out_probs, uint32_t* status,
                            void* cuda_stream);
+
+/*
+ * Log probabilities of given tokens, with rank, entropy and the top
+ * alternatives, of rows of logits: what an answer carries beside its tokens.
+ * Per row, with p = softmax(z / T):
+ *   out_logprob   ln p(token);
+ *   out_rank      1 + the number of tokens with a larger logit, or with an
+ *                 equal logit and a lower index;
+ *   out_entropy   -sum p ln p;
+ *   out_top_ids, out_top_logprobs   the n_top largest logits in order (equal
+ *                 logits: the lowest index first) and their ln p. Tokens at
+ *                 -inf are no alternatives: where fewer are left the rest
+ *                 is -1 and -inf.
+ * One pass reads each row once; the sums are fp32 per thread, joined in
+ * double.
+ *
+ *   logits       [R, V] dtype with row stride ld >= V elements; R >= 0. Finite
+ *                or -inf; any V >= 1 of int32 range.
+ *   tokens       [R] int32, or NULL (then out_logprob and out_rank are NULL).
+ *   B, cu_draft, out_len   NULL, NULL and B = 0: every row. Otherwise the
+ *                packed layout above, with the out_len of the verify call: of
+ *                request b only the rows of its out_len[b] committed tokens
+ *                (the tokens being out_tokens) are read; the other rows'
+ *                outputs, and those past cu_draft[B] + B, are left as they
+ *                were. out_len[b] = 0 takes no row of request b.
+ *   temperature  T > 0.
+ *   n_top        0 .. SV_LOGPROBS_MAX_TOP; out_top_* are [R, n_top] (may be
+ *                NULL when n_top is 0, or each by itself when not wanted).
+ *   out_*        each may be NULL. float32 and int32.
+ *   status       device uint32 that collects SV_DATA_* bits (the caller
+ *                clears it), or NULL.
+ * Data errors, per row: a token outside [0, V) gives logprob NaN and rank 0
+ * (SV_DATA_BAD_TOKEN); a row without a finite logit, or with a NaN or +inf,
+ * gives NaN, rank 0, and -1 / NaN alternatives (SV_DATA_EMPTY_ROW,
+ * SV_DATA_BAD_LOGIT); offsets that decrease, or an out_len outside
+ * [0, K_b + 1], leave the rows concerned as they were (SV_DATA_BAD_OFFSETS).
+ * No workspace; safe in any number of streams and graphs at once.
+ */
+#define SV_LOGPROBS_MAX_TOP 32
+sv_status sv_token_logprobs(const void* logits, sv_dtype dtype, int32_t V, int64_t ld, int32_t R,
+                            const int32_t* tokens, int32_t B, const int32_t* cu_draft,
+                            const int32_t* out_len, float temperature, int32_t n_top,
+                            float* out_logprob, int32_t* out_rank, float* out_entropy,
+                            int32_t* out_top_ids, float* out_top_logprobs, uint32_t* status,
+                            void* cuda_stream);
 
 /*
  * N-gram / prompt-lookup proposer ("5.2 Draft 模型与无模型方案", §4.1 and §6):

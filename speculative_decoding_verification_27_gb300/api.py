@@ -9,7 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -24,6 +24,10 @@ SV_DATA_EMPTY_ROW = 0x4
 SV_DATA_BAD_MODE = 0x8
 SV_DATA_DEGENERATE_RESIDUAL = 0x10
 SV_DEV_COPY_TIMEOUT = 0x20
+SV_DATA_BAD_LOGIT = 0x40
+SV_DATA_BAD_PAGE = 0x80
+SV_DATA_NO_PAGES = 0x100
+SV_DATA_BAD_SEQ = 0x200
 SV_ONEHOT_ROW_BYTES_DEFAULT = 128 * 1024  # sv_set_onehot_row_bytes' initial limit
 
 HEADER = os.path.join(ROOT, "include", "spec_verify.h")
@@ -58,6 +62,8 @@ def load() -> ctypes.CDLL:
     lib.ngram_propose.restype = ctypes.c_int
     lib.sv_pack_drafts.argtypes = [P, P, i32, i32, P, P, P]
     lib.sv_pack_drafts.restype = ctypes.c_int
+    lib.sv_token_logprobs.argtypes = [P, ctypes.c_int, i32, i64, i32, P, i32, P, P, f32, i32, P, P, P, P, P, P, P]
+    lib.sv_token_logprobs.restype = ctypes.c_int
     lib.sv_check_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_uint32)]
     lib.sv_check_status.restype = ctypes.c_int
     lib.sv_status_string.argtypes = [ctypes.c_int]
@@ -465,3 +471,91 @@ def sv_select_candidates(cu_cand: torch.Tensor, out_len: torch.Tensor, policy: i
     _check("sv_select_candidates", fn(_ptr(cu_cand), _ptr(out_len), int(B), int(policy), _ptr(u_select),
                                       _ptr(best), _ptr(best_len), _stream(stream)))
     return best, best_len
+
+
+# ---------------------------------------------------------------------------
+# Log probabilities of given tokens
+# ---------------------------------------------------------------------------
+SV_LOGPROBS_MAX_TOP = 32
+
+
+class TokenLogprobs(NamedTuple):
+    logprob: Optional[torch.Tensor]       # [R] float32, ln p(token)
+    rank: Optional[torch.Tensor]          # [R] int32, 1 = the largest logit
+    entropy: Optional[torch.Tensor]       # [R] float32
+    top_ids: Optional[torch.Tensor]       # [R, n_top] int32, -1 where fewer are left
+    top_logprobs: Optional[torch.Tensor]  # [R, n_top] float32
+
+
+def _place(t: torch.Tensor, stream):
+    """(device guard, stream pointer) of a call on t's device: the guard is
+    None when that device is the current one."""
+    idx = t.device.index
+    s = torch.cuda.current_stream(idx) if stream is None else stream
+    return (None if idx == torch.cuda.current_device() else torch.cuda.device(idx)), ctypes.c_void_p(s.cuda_stream)
+
+
+def _launch(name: str, t: torch.Tensor, stream, *args):
+    """Calls the library on t's device and stream (the current one if None)."""
+    guard, s = _place(t, stream)
+    if guard is None:
+        st = getattr(load(), name)(*args, s)
+    else:
+        with guard:
+            st = getattr(load(), name)(*args, s)
+    _check(name, st)
+
+
+def _new(make, shape, dtype, like: torch.Tensor, stream):
+    """An output tensor beside `like`, owned by the stream that writes it."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=like.device)
+
+
+def _vec(t: Optional[torch.Tensor], name: str, dtype, *shape):
+    """Pointer of a contiguous tensor of that type and shape (None in the
+    shape: any length); None stays None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {list(shape)}")
+    return _ptr(t)
+
+
+def sv_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *, cu_draft=None, out_len=None,
+                      temperature: float = 1.0, n_top: int = 0, out_logprob=None, out_rank=None, out_entropy=None,
+                      out_top_ids=None, out_top_logprobs=None, status=None, stream=None) -> TokenLogprobs:
+    """Log probability, rank, entropy and top alternatives of every row, or,
+    with the cu_draft and out_len of a verify call (and its out_tokens as
+    `tokens`), of the committed rows only: the other rows of given outputs
+    keep their values, those of outputs made here are zero. `logits` may have
+    a row stride. `status`: a one-element int32 CUDA tensor that collects the
+    data-error bits."""
+    if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a CUDA matrix with contiguous rows")
+    R, V = logits.shape
+    ld = logits.stride(0) if R > 1 else max(V, 1)
+    n_top = int(n_top)
+    f32, i32 = torch.float32, torch.int32
+    if (cu_draft is None) != (out_len is None):
+        raise ValueError("cu_draft and out_len come together")
+    B = 0 if out_len is None else out_len.shape[0]
+    make = torch.empty if out_len is None else torch.zeros
+    if tokens is not None and out_logprob is None:
+        out_logprob = _new(make, R, f32, logits, stream)
+    if tokens is not None and out_rank is None:
+        out_rank = _new(make, R, i32, logits, stream)
+    if out_entropy is None:
+        out_entropy = _new(make, R, f32, logits, stream)
+    if n_top > 0 and out_top_ids is None:
+        out_top_ids = _new(make, (R, n_top), i32, logits, stream)
+    if n_top > 0 and out_top_logprobs is None:
+        out_top_logprobs = _new(make, (R, n_top), f32, logits, stream)
+    _launch("sv_token_logprobs", logits, stream, ctypes.c_void_p(logits.data_ptr()), _dtype(logits), V, ld, R,
+            _vec(tokens, "tokens", i32, R), B, _vec(cu_draft, "cu_draft", i32, B + 1), _vec(out_len, "out_len", i32, B),
+            float(temperature), n_top, _vec(out_logprob, "out_logprob", f32, R), _vec(out_rank, "out_rank", i32, R),
+            _vec(out_entropy, "out_entropy", f32, R), _vec(out_top_ids, "out_top_ids", i32, R, n_top),
+            _vec(out_top_logprobs, "out_top_logprobs", f32, R, n_top), _vec(status, "status", i32, 1))
+    return TokenLogprobs(out_logprob, out_rank, out_entropy, out_top_ids, out_top_logprobs)
