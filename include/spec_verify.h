@@ -442,6 +442,172 @@ sv_status sv_token_logprobs(const void* logits, sv_dtype dtype, int32_t V, int64
                             void* cuda_stream);
 
 /*
+ * A paged key-value cache around the verify step ("Draft Model（草稿模型）" §2
+ * runs one target pass over the prefix and the K draft tokens; the Chain of
+ * Draft page, "共享 prefix KV", shares the prefix's keys and values and keeps
+ * those of the accepted branch only). All calls below share these
+ * descriptions; their pointers are device pointers, the structs themselves
+ * are read on the host during the call.
+ *
+ * sv_kv_cache: the pages of every layer. Element (layer, page, token, head,
+ * d) of K is at k[layer * layer_stride + page * page_stride + token *
+ * token_stride + head * head_stride + d], of V alike. k and v are 16-byte
+ * aligned; head_dim and the strides are multiples of 16 bytes. page_ref
+ * counts the sequences that hold a page; bit p % 32 of free_bits[p / 32] is
+ * set exactly where page_ref[p] is 0 (bits past n_pages are 0). A new cache
+ * has page_ref 0 everywhere and those bits set.
+ *
+ * sv_sequences: n sequences, sequence b with ctx_len[b] tokens in the cache.
+ * Token t is in page table[b * table_stride + t / page_size], place
+ * t % page_size. Entries behind the pages that a sequence holds are -1 (a new
+ * sequence: all -1, ctx_len 0).
+ *
+ * Windows. Sequence b is request b of the step. Its window is the rows that
+ * the target scores, with their keys and values at tokens ctx_len[b],
+ * ctx_len[b] + 1, ... : the K_b + 1 target rows (the last committed token and
+ * the K_b drafts) in the packed layout above. With several candidates a
+ * request (the flattened call of sv_select_candidates) cu_draft has n_cand + 1
+ * offsets, request b owns candidates cu_cand[b] .. cu_cand[b+1]-1, and its
+ * window is their rows one after another. Without candidates cu_cand is NULL
+ * and n_cand is n. cu_draft NULL (n_cand = n, cu_cand NULL) stands for one
+ * row a sequence: plain decoding, a draft model's step.
+ *
+ * Order of one step: sv_cache_reserve; per layer sv_cache_append and
+ * sv_window_attention; spec_verify (and sv_select_candidates);
+ * sv_cache_commit. The token drawn at the stop row has no keys yet: it is the
+ * next window's first row.
+ *
+ * Every call checks each index that it reads from the device and stays in
+ * bounds: sequences it cannot serve are left as they were and set a bit in
+ * `status` (a device uint32 that the caller clears, or NULL): offsets out of
+ * order SV_DATA_BAD_OFFSETS, pages out of range SV_DATA_BAD_PAGE, sequence
+ * indices and lengths SV_DATA_BAD_SEQ. Calls that change a cache or its
+ * sequences must not overlap others on the same cache. Results do not depend
+ * on timing: pages are taken lowest index first, in the order of the
+ * sequences.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  sv_dtype dtype;
+  int32_t n_layers, n_pages, page_size, n_kv_heads, head_dim;
+  int64_t layer_stride, page_stride, token_stride, head_stride;
+  int32_t* page_ref;   /* [n_pages] */
+  uint32_t* free_bits; /* [ceil(n_pages / 32)] */
+} sv_kv_cache;
+
+typedef struct {
+  int32_t* table;       /* [n, table_pages] with row stride table_stride */
+  int64_t table_stride;
+  int32_t table_pages;
+  int32_t n;
+  int32_t* ctx_len;     /* [n] */
+} sv_sequences;
+
+/*
+ * Forks sequences: dst[i] becomes a copy of src[i] that shares its pages
+ * (their counts grow by one); no keys or values are copied until a fork
+ * writes (sv_cache_reserve). dst[i] must hold nothing (ctx_len 0). The same
+ * src may stand more than once. A dst that stands more than once is taken
+ * by its first entry; an entry whose src is also a dst is refused. Both set
+ * SV_DATA_BAD_SEQ, as do lengths or indices out of range.
+ */
+sv_status sv_cache_fork(const sv_kv_cache* cache, const sv_sequences* seqs, int32_t N,
+                        const int32_t* src, const int32_t* dst, uint32_t* status, void* cuda_stream);
+
+/*
+ * Ends sequences: every page of seqs[which[i]] is released (a page that no
+ * sequence holds any more is free), its entries become -1, its length 0. An
+ * index that stands twice counts once.
+ */
+sv_status sv_cache_free(const sv_kv_cache* cache, const sv_sequences* seqs, int32_t N,
+                        const int32_t* which, uint32_t* status, void* cuda_stream);
+
+/*
+ * Pages for every request's window, before its keys and values are written.
+ * A sequence whose last page is partly filled and shared gets a page of its
+ * own with the tokens it holds there copied, in every layer (of several
+ * requests of this call that share it, the last keeps it when nobody else
+ * holds it). Then its table grows to ctx_len + window tokens with the lowest
+ * free pages. Requests are served in order. When pages run out, the first
+ * request that does not fit and every later one that needs a page, or whose
+ * partly filled page was shared, is left as it was (SV_DATA_NO_PAGES). A
+ * window beyond the table's width is refused (SV_DATA_BAD_PAGE). Pages that
+ * an earlier call reserved beyond ctx_len are used first. n <= SV_CACHE_MAX_SEQS.
+ *   granted    [n] int32 or NULL: the window's rows, or 0 if it got no room.
+ *   workspace  sv_cache_reserve_workspace_size(n) bytes, 16-byte aligned, of
+ *              any contents.
+ */
+#define SV_CACHE_MAX_SEQS 16384
+size_t sv_cache_reserve_workspace_size(int32_t n);
+sv_status sv_cache_reserve(const sv_kv_cache* cache, const sv_sequences* seqs, int32_t n_cand,
+                           const int32_t* cu_draft, const int32_t* cu_cand, int32_t* granted,
+                           void* workspace, size_t workspace_bytes, uint32_t* status,
+                           void* cuda_stream);
+
+/*
+ * Writes the windows' keys and values to their pages, for the layers layer
+ * .. layer + n_layers - 1. k_new, v_new: [n_layers, R, n_kv_heads, head_dim]
+ * of the cache's dtype with strides new_layer_stride and new_row_stride
+ * (elements; multiples of 16 bytes, heads contiguous), 16-byte aligned. Rows
+ * without a page, or whose page another sequence holds too (a window that
+ * sv_cache_reserve refused), are skipped (SV_DATA_BAD_PAGE); rows that
+ * belong to no window are not read.
+ */
+sv_status sv_cache_append(const sv_kv_cache* cache, int32_t layer, int32_t n_layers,
+                          const void* k_new, const void* v_new, int64_t new_layer_stride,
+                          int64_t new_row_stride, int32_t R, const sv_sequences* seqs,
+                          int32_t n_cand, const int32_t* cu_draft, const int32_t* cu_cand,
+                          uint32_t* status, void* cuda_stream);
+
+/*
+ * After the verify call: keeps the keys and values of the committed rows.
+ * Request b keeps the first out_len[c] rows of candidate c = best[b] (without
+ * candidates c = b; best[b] = -1 keeps none): they are moved to the front of
+ * the window in every layer, ctx_len[b] grows by out_len[c], and the pages
+ * behind the new length are released. out_len is the verify call's, [n_cand].
+ * out_len = 0 releases the window. A request whose kept rows lack a page of
+ * its own is left as it was (SV_DATA_BAD_PAGE). best is NULL exactly where cu_cand is.
+ */
+sv_status sv_cache_commit(const sv_kv_cache* cache, const sv_sequences* seqs, int32_t n_cand,
+                          const int32_t* cu_draft, const int32_t* cu_cand, const int32_t* best,
+                          const int32_t* out_len, uint32_t* status, void* cuda_stream);
+
+/*
+ * Attention of every request's window over its history and itself, for one
+ * layer whose window rows are in their pages. Window row w of request b, in a
+ * candidate whose rows begin at w0 of the window, sees tokens 0 ..
+ * ctx_len[b] - 1 and ctx_len[b] + w0 .. ctx_len[b] + w (block-diagonal and
+ * causal inside the window). With n_kv_heads key-value heads, query head h
+ * reads head h / (n_q_heads / n_kv_heads). Over the tokens t it sees,
+ *   out = sum_t softmax_t(scale * q . k_t) v_t,  lse = ln sum_t e^(scale * q . k_t).
+ *
+ *   q, out      [R, n_q_heads, head_dim] of the cache's dtype, row strides
+ *               q_stride and out_stride (elements, multiples of 16 bytes,
+ *               heads contiguous), 16-byte aligned. Rows of no window are
+ *               neither read nor written.
+ *   out_lse     [R, n_q_heads] float32, or NULL.
+ *   scale       finite; usually 1 / sqrt(head_dim).
+ *   head_dim    64 or 128; n_q_heads a multiple of n_kv_heads, at most 64
+ *               query heads to a key-value head.
+ *   workspace   sv_window_attention_workspace_size(cache, n_q_heads, R)
+ *               bytes, 16-byte aligned, of any contents.
+ * Scores, the softmax statistics and the sums are fp32. With a bf16 cache the
+ * weights are rounded to bf16 for the product with V (as V is), their sum is
+ * not. Keys and values of the tokens a window holds must be finite; what lies
+ * in the pages behind it may be anything. A page out of range in a
+ * sequence's table hides its tokens (SV_DATA_BAD_PAGE); a row that sees no
+ * token gives out = 0 and lse = -inf.
+ */
+size_t sv_window_attention_workspace_size(const sv_kv_cache* cache, int32_t n_q_heads, int32_t R);
+sv_status sv_window_attention(const void* q, int64_t q_stride, int32_t n_q_heads, int32_t R,
+                              const sv_kv_cache* cache, int32_t layer, const sv_sequences* seqs,
+                              int32_t n_cand, const int32_t* cu_draft, const int32_t* cu_cand,
+                              float scale, void* out, int64_t out_stride, float* out_lse,
+                              void* workspace, size_t workspace_bytes, uint32_t* status,
+                              void* cuda_stream);
+
+/*
  * N-gram / prompt-lookup proposer ("5.2 Draft 模型与无模型方案", §4.1 and §6):
  * for n = min(max_n, L) down to min_n, take the tail h[L-n, L) of the
  * history and find the most recent earlier start s, 0 <= s <= L-2n-1, with

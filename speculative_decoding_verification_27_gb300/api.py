@@ -64,6 +64,19 @@ def load() -> ctypes.CDLL:
     lib.sv_pack_drafts.restype = ctypes.c_int
     lib.sv_token_logprobs.argtypes = [P, ctypes.c_int, i32, i64, i32, P, i32, P, P, f32, i32, P, P, P, P, P, P, P]
     lib.sv_token_logprobs.restype = ctypes.c_int
+    lib.sv_cache_fork.argtypes = [P, P, i32, P, P, P, P]
+    lib.sv_cache_free.argtypes = [P, P, i32, P, P, P]
+    lib.sv_cache_reserve_workspace_size.argtypes = [i32]
+    lib.sv_cache_reserve_workspace_size.restype = sz
+    lib.sv_cache_reserve.argtypes = [P, P, i32, P, P, P, P, sz, P, P]
+    lib.sv_cache_append.argtypes = [P, i32, i32, P, P, i64, i64, i32, P, i32, P, P, P, P]
+    lib.sv_cache_commit.argtypes = [P, P, i32, P, P, P, P, P, P]
+    lib.sv_window_attention_workspace_size.argtypes = [P, i32, i32]
+    lib.sv_window_attention_workspace_size.restype = sz
+    lib.sv_window_attention.argtypes = [P, i64, i32, i32, P, i32, P, i32, P, P, f32, P, i64, P, P, sz, P, P]
+    for name in ("sv_cache_fork", "sv_cache_free", "sv_cache_reserve", "sv_cache_append", "sv_cache_commit",
+                 "sv_window_attention"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.sv_check_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_uint32)]
     lib.sv_check_status.restype = ctypes.c_int
     lib.sv_status_string.argtypes = [ctypes.c_int]
@@ -559,3 +572,167 @@ def sv_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = Non
             _vec(out_entropy, "out_entropy", f32, R), _vec(out_top_ids, "out_top_ids", i32, R, n_top),
             _vec(out_top_logprobs, "out_top_logprobs", f32, R, n_top), _vec(status, "status", i32, 1))
     return TokenLogprobs(out_logprob, out_rank, out_entropy, out_top_ids, out_top_logprobs)
+
+
+# ---------------------------------------------------------------------------
+# The paged key-value cache around the verify step
+# ---------------------------------------------------------------------------
+SV_CACHE_MAX_SEQS = 16384
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int), ("n_layers", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("layer_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("page_ref", ctypes.c_void_p),
+                ("free_bits", ctypes.c_void_p)]
+
+
+class _Sequences(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("table_pages", ctypes.c_int32),
+                ("n", ctypes.c_int32), ("ctx_len", ctypes.c_void_p)]
+
+
+class KVCache:
+    """The pages of a key-value cache: `k` and `v` are [n_layers, n_pages,
+    page_size, n_kv_heads, head_dim] views with equal strides (any order of
+    the first four dimensions in memory, the last contiguous). page_ref
+    [n_pages] int32 counts a page's holders, free_bits [ceil(n_pages / 32)]
+    int32 has a bit set per free page; without them the cache starts empty."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, page_ref=None, free_bits=None):
+        if k.dim() != 5 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must be [layers, pages, page_size, kv_heads, head_dim] with equal strides")
+        if not k.is_cuda or (k.shape[4] > 1 and k.stride(4) != 1):
+            raise ValueError("k and v must be CUDA tensors with a contiguous last dimension")
+        if (page_ref is None) != (free_bits is None):
+            raise ValueError("page_ref and free_bits come together")
+        n, words = k.shape[1], -(-k.shape[1] // 32)
+        if page_ref is None:
+            page_ref = torch.zeros(n, dtype=torch.int32, device=k.device)
+            free_bits = torch.full((words,), -1, dtype=torch.int32, device=k.device)
+            if n % 32:
+                free_bits[-1] = (1 << n % 32) - 1
+        self.k, self.v, self.page_ref, self.free_bits = k, v, page_ref, free_bits
+        self.n_layers, self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = k.shape
+        # A dimension of one element takes no step; its stride may be anything.
+        steps = [s if m > 1 else 0 for s, m in zip(k.stride(), k.shape)]
+        self._c = _Cache(k.data_ptr(), v.data_ptr(), _dtype(k), *k.shape, *steps[:4],
+                         _vec(page_ref, "page_ref", torch.int32, n), _vec(free_bits, "free_bits", torch.int32, words))
+        self._ref = ctypes.byref(self._c)
+
+
+def _seqs(page_table: torch.Tensor, ctx_len: torch.Tensor):
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or not page_table.is_cuda or \
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be an int32 CUDA matrix with contiguous rows")
+    n, width = page_table.shape
+    return ctypes.byref(_Sequences(page_table.data_ptr(), page_table.stride(0) if n > 1 else max(width, 1), width, n,
+                                   _vec(ctx_len, "ctx_len", torch.int32, n)))
+
+
+def _windows(n: int, cu_draft, cu_cand):
+    """(n_cand, cu_draft, cu_cand) as the library takes them."""
+    if cu_draft is None:
+        if cu_cand is not None:
+            raise ValueError("cu_cand needs cu_draft")
+        return n, None, None
+    n_cand = cu_draft.shape[0] - 1
+    if cu_cand is None and n_cand != n:
+        raise ValueError("cu_draft has an offset per sequence and one more")
+    return n_cand, _vec(cu_draft, "cu_draft", torch.int32, n_cand + 1), _vec(cu_cand, "cu_cand", torch.int32, n + 1)
+
+
+def _scratch(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
+    return _new(torch.empty, max(nbytes, 16), torch.uint8, like, stream)
+
+
+def sv_cache_fork(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, *,
+                  status=None, stream=None) -> None:
+    """Sequences dst[i] (empty) become copies of src[i] that share its pages."""
+    N = src.shape[0]
+    _launch("sv_cache_fork", cache.k, stream, cache._ref, _seqs(page_table, ctx_len), N, _vec(src, "src", torch.int32, N),
+            _vec(dst, "dst", torch.int32, N), _vec(status, "status", torch.int32, 1))
+
+
+def sv_cache_free(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Tensor, which: torch.Tensor, *, status=None,
+                  stream=None) -> None:
+    """Ends the sequences `which`: their pages are released."""
+    N = which.shape[0]
+    _launch("sv_cache_free", cache.k, stream, cache._ref, _seqs(page_table, ctx_len), N,
+            _vec(which, "which", torch.int32, N), _vec(status, "status", torch.int32, 1))
+
+
+def sv_cache_reserve(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Tensor, cu_draft=None, cu_cand=None, *,
+                     granted=None, workspace=None, status=None, stream=None) -> torch.Tensor:
+    """Pages for every sequence's window. Returns `granted` [n]: the window's
+    rows, or 0 for a sequence that got no room."""
+    n = page_table.shape[0]
+    if granted is None:
+        granted = _new(torch.empty, n, torch.int32, page_table, stream)
+    if workspace is None:
+        workspace = _scratch(load().sv_cache_reserve_workspace_size(n), page_table, stream)
+    _launch("sv_cache_reserve", cache.k, stream, cache._ref, _seqs(page_table, ctx_len), *_windows(n, cu_draft, cu_cand),
+            _vec(granted, "granted", torch.int32, n), _ptr(workspace), workspace.numel(),
+            _vec(status, "status", torch.int32, 1))
+    return granted
+
+
+def sv_cache_append(cache: KVCache, layer: int, k_new: torch.Tensor, v_new: torch.Tensor, page_table: torch.Tensor,
+                    ctx_len: torch.Tensor, cu_draft=None, cu_cand=None, *, status=None, stream=None) -> None:
+    """Writes the windows' keys and values to their pages: [R, kv_heads,
+    head_dim] for one layer, or [n_layers, R, kv_heads, head_dim] for the
+    layers from `layer` on."""
+    if k_new.dim() == 3:
+        k_new, v_new = k_new[None], v_new[None]
+    L, R = k_new.shape[:2]
+    heads = (cache.n_kv_heads, cache.head_dim)
+    for x in (k_new, v_new):
+        if x.dim() != 4 or tuple(x.shape) != (L, R, *heads) or x.dtype != cache.k.dtype or not x.is_cuda or \
+                x.stride() != k_new.stride() or (R and L and not x[0, 0].is_contiguous()):
+            raise ValueError("k_new and v_new must be [n_layers, R, kv_heads, head_dim] of the cache's dtype, alike in "
+                             "strides, with contiguous heads")
+    _launch("sv_cache_append", cache.k, stream, cache._ref, int(layer), L, k_new.data_ptr(), v_new.data_ptr(),
+            k_new.stride(0) if L > 1 else 0, k_new.stride(1) if R > 1 else 0, R, _seqs(page_table, ctx_len),
+            *_windows(page_table.shape[0], cu_draft, cu_cand), _vec(status, "status", torch.int32, 1))
+
+
+def sv_cache_commit(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Tensor, cu_draft, out_len: torch.Tensor,
+                    cu_cand=None, best=None, *, status=None, stream=None) -> None:
+    """Keeps the committed rows of every window (candidate best[b]'s first
+    out_len rows, moved to the window's front) and releases the pages behind
+    them; ctx_len grows by the rows kept."""
+    n = page_table.shape[0]
+    if (cu_cand is None) != (best is None):
+        raise ValueError("cu_cand and best come together")
+    win = _windows(n, cu_draft, cu_cand)
+    _launch("sv_cache_commit", cache.k, stream, cache._ref, _seqs(page_table, ctx_len), *win,
+            _vec(best, "best", torch.int32, n), _vec(out_len, "out_len", torch.int32, win[0]),
+            _vec(status, "status", torch.int32, 1))
+
+
+def sv_window_attention(q: torch.Tensor, cache: KVCache, layer: int, page_table: torch.Tensor, ctx_len: torch.Tensor,
+                        cu_draft=None, cu_cand=None, *, scale: Optional[float] = None, out=None, out_lse=None,
+                        want_lse: bool = False, workspace=None, status=None, stream=None):
+    """Attention of every window (q [R, q_heads, head_dim]) over its history
+    and itself, whose keys and values are in their pages. Returns (out, lse);
+    rows of no window keep the values of a given `out`, and are zero in one
+    made here. scale: 1 / sqrt(head_dim) if None."""
+    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.dtype != cache.k.dtype or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor [R, q_heads, head_dim] of the cache's dtype")
+    R, heads, D = q.shape
+    if out is None:
+        out = _new(torch.zeros, (R, heads, D), q.dtype, q, stream)
+    for x in (q, out):
+        if tuple(x.shape) != (R, heads, D) or x.dtype != q.dtype or not x.is_cuda or (R and not x[0].is_contiguous()):
+            raise ValueError("q and out must be [R, q_heads, head_dim] with contiguous heads")
+    if out_lse is None and want_lse:
+        out_lse = _new(torch.zeros, (R, heads), torch.float32, q, stream)
+    if workspace is None:
+        workspace = _scratch(load().sv_window_attention_workspace_size(cache._ref, heads, R), q, stream)
+    _launch("sv_window_attention", q, stream, q.data_ptr(), q.stride(0) if R > 1 else heads * D, heads, R, cache._ref,
+            int(layer), _seqs(page_table, ctx_len), *_windows(page_table.shape[0], cu_draft, cu_cand),
+            D ** -0.5 if scale is None else float(scale), out.data_ptr(), out.stride(0) if R > 1 else heads * D,
+            _vec(out_lse, "out_lse", torch.float32, R, heads), _ptr(workspace), workspace.numel(),
+            _vec(status, "status", torch.int32, 1))
+    return out, out_lse
