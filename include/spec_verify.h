@@ -412,7 +412,7 @@ sv_status sv_vshard_finish(const void* jobs, int32_t B, int32_t R_t, const int32
  * double.
  *
  *   logits       [R, V] dtype with row stride ld >= V elements; R >= 0. Finite
- *                or -inf; any V >= 1 of int32 range.
+ *                or -inf; 1 <= V <= 2^30.
  *   tokens       [R] int32, or NULL (then out_logprob and out_rank are NULL).
  *   B, cu_draft, out_len   NULL, NULL and B = 0: every row. Otherwise the
  *                packed layout above, with the out_len of the verify call: of
@@ -420,7 +420,7 @@ sv_status sv_vshard_finish(const void* jobs, int32_t B, int32_t R_t, const int32
  *                (the tokens being out_tokens) are read; the other rows'
  *                outputs, and those past cu_draft[B] + B, are left as they
  *                were. out_len[b] = 0 takes no row of request b.
- *   temperature  T > 0.
+ *   temperature  2^-100 <= T <= 2^100.
  *   n_top        0 .. SV_LOGPROBS_MAX_TOP; out_top_* are [R, n_top] (may be
  *                NULL when n_top is 0, or each by itself when not wanted).
  *   out_*        each may be NULL. float32 and int32.

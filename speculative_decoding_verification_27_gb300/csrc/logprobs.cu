@@ -5,13 +5,24 @@
 //   S = sum e^t, ln p(x) = t_x - ln S, H = ln S - (1 / S) sum e^t t,
 //   rank = 1 + #{z_x > z_tok} + #{z_x = z_tok, x < tok},
 //   the top n in the order (z descending, index ascending).
+// One pass: every thread keeps the sums relative to its own running maximum
+// m; moving the reference from m to m' with d = (m - m') / T multiplies S by
+// e^d and turns S1 = sum e^t t into e^d (S1 + d S). The threads' sums are
+// joined in double-float.
 //
-// One CTA per row: a pass for M, a pass for S, the entropy sum and the rank,
-// and one pass per alternative (the largest pair below the last one in that
-// order).
+// The alternatives come from the same pass. A floor that n elements of the
+// row are known to reach (each warp publishes the ceil(n / warps)-th largest
+// of its lanes' maxima, the floor is the least of those) lets almost every
+// batch pass with one comparison; elements at or above it go to a buffer, and
+// the row's end sorts what reached the last floor. Rows that overflow the
+// buffer (long ties at the top) take n passes for the n alternatives.
+//
+// The rows are bound by their bytes; the exponentials are next (one a logit,
+// about 70% of the special-function rate at the copy rate for bf16).
 #include "../../include/spec_verify.h"
 #include "sv_device.cuh"
 
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -27,8 +38,8 @@ struct Params {
   const int32_t* tokens;
   const int32_t* cu;
   const int32_t* out_len;
-  float c;       // log2(e) / T
-  double inv_T;
+  float c_hi, c_lo;          // log2(e) / T in two parts
+  float inv_T_hi, inv_T_lo;  // 1 / T
   float* logprob;
   int32_t* rank;
   float* entropy;
@@ -41,21 +52,11 @@ __device__ __forceinline__ void flag(const Params& P, uint32_t bit) {
   if (P.status) atomicOr(P.status, bit);
 }
 
-// Whether row r is asked for: with offsets, only a request's committed rows.
-// The search ends for any contents of cu, and what it finds is checked.
-__device__ __forceinline__ bool row_wanted(const Params& P, int r) {
-  if (!P.cu) return true;
-  int lo = 0, hi = P.B;  // the request is in [lo, hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((long long)P.cu[mid] + mid <= r)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  const long long i = (long long)r - P.cu[lo] - lo;
-  const long long K = (long long)P.cu[lo + 1] - P.cu[lo];
-  const int n = P.out_len[lo];
+// Whether row r is asked for, b being the request that the offsets put it in.
+__device__ __forceinline__ bool row_wanted(const Params& P, int r, int b) {
+  const long long i = (long long)r - P.cu[b] - b;
+  const long long K = (long long)P.cu[b + 1] - P.cu[b];
+  const int n = P.out_len[b];
   return K >= 0 && n <= K + 1 && i >= 0 && i < n;
 }
 
@@ -70,115 +71,467 @@ __device__ __forceinline__ void check_offsets(const Params& P, int tid) {
   if (bad) flag(P, SV_DATA_BAD_OFFSETS);
 }
 
+constexpr int kU = 4;            // 16-byte loads of a batch, per thread; the next batch's are in flight meanwhile
+constexpr int kCap = 2048;       // buffered candidates of a CTA
+constexpr int kMaxCluster = 8;   // CTAs to a row, at most
+constexpr float kFar = 200.f;    // 2^-kFar is zero in fp32: exponents are cut off there
+
+// The 16-byte vector at aligned-down place v of a row that begins `off`
+// elements behind it; elements outside the row read as -inf.
 template <int DT>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(Params P) {
-  __shared__ float s_f[kWarps];
-  __shared__ int s_i[kWarps];
-  __shared__ double s_d[2][kWarps];
+__device__ __forceinline__ uint4 load_vec(const char* row, const char* base, int v, int off, int V) {
+  constexpr int EPV = Elem<DT>::kEPV;
+  const int x0 = v * EPV - off;
+  if (x0 >= 0 && x0 + EPV <= V) return ld_stream16(base + (long long)v * 16);
+  float f[EPV];
+#pragma unroll
+  for (int j = 0; j < EPV; ++j) f[j] = x0 + j >= 0 && x0 + j < V ? Elem<DT>::scalar(row, x0 + j) : -INFINITY;
+  uint4 r;
+  uint32_t* w = &r.x;
+  if constexpr (DT == 1) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = (__float_as_uint(f[2 * j]) >> 16) | (__float_as_uint(f[2 * j + 1]) & 0xffff0000u);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(f[j]);
+  }
+  return r;
+}
+
+// Maxima that keep a NaN, so that a row with one is found out.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_nan_bf2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+template <int DT>
+__device__ __forceinline__ float batch_max(const uint4 (&v)[kU]) {
+  if constexpr (DT == 1) {
+    uint32_t m = max_nan_bf2(max_nan_bf2(v[0].x, v[0].y), max_nan_bf2(v[0].z, v[0].w));
+#pragma unroll
+    for (int u = 1; u < kU; ++u) m = max_nan_bf2(m, max_nan_bf2(max_nan_bf2(v[u].x, v[u].y), max_nan_bf2(v[u].z, v[u].w)));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  } else {
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      m = max_nan(m, max_nan(max_nan(__uint_as_float(v[u].x), __uint_as_float(v[u].y)),
+                             max_nan(__uint_as_float(v[u].z), __uint_as_float(v[u].w))));
+    return m;
+  }
+}
+
+__device__ __forceinline__ int order_key(float f) {  // whole numbers in the order of the floats
+  const int b = __float_as_int(f);
+  return b < 0 ? b ^ 0x7fffffff : b;
+}
+__device__ __forceinline__ float key_value(int k) { return __int_as_float(k < 0 ? k ^ 0x7fffffff : k); }
+
+// Where logits are cut off below a maximum m: kFar in the exponent, rounded
+// down, and below m itself where that is less than a step. -inf where m is
+// the type's lowest value (then the terms are counted, add_lowest).
+template <int DT>
+__device__ __forceinline__ uint32_t cut_off(float m, float far) {
+  if constexpr (DT == 1) {
+    const int k = min(order_key(m - far) >> 16, (order_key(m) >> 16) - 1);
+    const uint32_t b = __float_as_uint(key_value((int)((uint32_t)k << 16 | (k < 0 ? 0xffffu : 0u)))) & 0xffff0000u;
+    return b | b >> 16;
+  } else {
+    return __float_as_uint(key_value(min(order_key(m - far), order_key(m) - 1)));
+  }
+}
+
+// Adds one vector's terms 2^((z - m) c) and their first moments, in pairs.
+// The reference's negative and the two parts of c come as pairs; `lowest`
+// cuts off logits so far below m that their term is zero (-inf among them,
+// whose product 0 * inf would not be a number).
+// A maximum that is the type's lowest value: what is not -inf counts one.
+template <int DT>
+__device__ __forceinline__ void add_lowest(const uint4& v, f2_t& S) {
+  float f[Elem<DT>::kEPV], n = 0.f;
+  Elem<DT>::unpack(v, f);
+#pragma unroll
+  for (int j = 0; j < Elem<DT>::kEPV; ++j) n += f[j] > -INFINITY ? 1.f : 0.f;
+  S = f2_add(S, f2_pack(n, 0.f));
+}
+
+template <int DT>
+__device__ __forceinline__ void add_terms(const uint4& v, uint32_t lowest, f2_t neg_m, f2_t c_hi, f2_t c_lo, f2_t& S, f2_t& S1) {
+  const uint32_t* w = &v.x;
+  if constexpr (DT == 1) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t x = max_nan_bf2(w[j], lowest);
+      const f2_t d = f2_add(f2_pack(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), neg_m);
+      const f2_t t = f2_fma(d, c_lo, f2_mul(d, c_hi));
+      const f2_t e = f2_ex2(t);
+      S = f2_add(S, e);
+      S1 = f2_fma(e, t, S1);
+    }
+  } else {
+    const float lo = __uint_as_float(lowest);
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      const f2_t d = f2_add(f2_pack(max_nan(__uint_as_float(w[j]), lo), max_nan(__uint_as_float(w[j + 1]), lo)), neg_m);
+      const f2_t t = f2_fma(d, c_lo, f2_mul(d, c_hi));
+      const f2_t e = f2_ex2(t);
+      S = f2_add(S, e);
+      S1 = f2_fma(e, t, S1);
+    }
+  }
+}
+
+// The q-th largest of the lanes' values (1 <= q <= 32).
+__device__ __forceinline__ float warp_nth_largest(float v, int q) {
+  const int lane = threadIdx.x & 31;
+  int key = order_key(v + 0.f), top = key;
+  for (int i = 0; i < q; ++i) {
+    top = __reduce_max_sync(kFull, key);
+    const unsigned who = __ballot_sync(kFull, key == top);
+    if (lane == __ffs(who) - 1) key = INT_MIN;
+  }
+  return key_value(top);
+}
+
+struct Smem {
+  float2 cand[kCap];               // (logit, index as bits)
+  float2 best[kMaxCluster * SV_LOGPROBS_MAX_TOP];  // the CTAs' sorted alternatives, in the leader
+  float rec[kMaxCluster][6];       // the CTAs' (M, S.hi, S.lo, S1.hi, S1.lo, rank count), in the leader
+  float2 mine[SV_LOGPROBS_MAX_TOP];
+  float floor_w[kWarps];
+  float red[kWarps][5];
+  int cnt[kWarps];
+  int n, n2, kept;
+};
+
+__device__ __forceinline__ bool ahead(float2 a, float2 b) {  // a comes before b among the alternatives
+  return a.x > b.x || (a.x == b.x && __float_as_int(a.y) < __float_as_int(b.y));
+}
+
+// The first n of c candidates in order, to out[0 .. n): each thread counts who is ahead of its own. Places that stay free are
+// (-inf, -1). Every thread of the CTA calls it.
+__device__ __forceinline__ void sort_top(const float2* from, int c, int n, float2* out) {
+  for (int j = threadIdx.x; j < n; j += kThreads)
+    if (j >= c) out[j] = make_float2(-INFINITY, __int_as_float(-1));
+  for (int i = threadIdx.x; i < c; i += kThreads) {
+    const float2 x = from[i];
+    int k = 0;
+    for (int j = 0; j < c; ++j) k += ahead(from[j], x) || (j < i && !ahead(x, from[j]));
+    if (k < n) out[k] = x;
+  }
+}
+
+// Largest b in [0, B) with cu[b] + b <= t, by every thread of the CTA (as the verify kernels look a row up). Ends for any
+// contents of cu.
+__device__ __forceinline__ int find_request(const int32_t* cu, int B, int t) {
+  int lo = 0, n = B;
+  while (n > 1) {
+    const int step = (n + kThreads - 1) / kThreads;
+    const int c = lo + (int)threadIdx.x * step;
+    const bool pass = c < lo + n && (long long)cu[c] + c <= t;
+    const int cnt = max(__syncthreads_count(pass), 1);
+    const int end = lo + n;
+    lo += (cnt - 1) * step;
+    n = min(step, end - lo);
+  }
+  return lo;
+}
+
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// Writes a word into the leader's shared memory.
+__device__ __forceinline__ void to_leader(void* p, float v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_addr(p)));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+
+// A cluster of `cl` CTAs takes a row, each a contiguous slice of its vectors.
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl) {
+  constexpr int EPV = Elem<DT>::kEPV;
+  __shared__ Smem sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int r = blockIdx.x;
-  if (r == 0) check_offsets(P, tid);
-  if (!row_wanted(P, r)) return;
+  const int rank = cl > 1 ? (int)cluster_rank() : 0;
+  const int r = cl > 1 ? blockIdx.x / cl : blockIdx.x;
+  if (blockIdx.x == 0) check_offsets(P, tid);
+  if (P.cu && !row_wanted(P, r, find_request(P.cu, P.B, r))) return;  // all CTAs of the row alike
+  const int V = P.V, n_top = P.n_top;
   const char* row = P.logits + (long long)r * P.ld_bytes;
-  const int V = P.V;
+  const int off = (int)((uintptr_t)row & 15) / Elem<DT>::kBytes;
+  const char* base = row - off * Elem<DT>::kBytes;
+  const int n_vec = (off + V + EPV - 1) / EPV;
+  const int per = (n_vec + cl - 1) / cl;
+  const int v0 = min(rank * per, n_vec), v1 = min(v0 + per, n_vec);
+
+  uint4 nxt[kU];
+  auto fetch = [&](int at) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int v = at + u * kThreads + tid;
+      nxt[u] = v < v1 ? load_vec<DT>(row, base, v, off, V) : (DT == 1 ? make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u)
+                                                                    : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u));
+    }
+  };
+  fetch(v0);
   const int tok = P.tokens ? P.tokens[r] : -1;
   const bool tok_ok = tok >= 0 && tok < V;
+  const float zt = tok_ok ? Elem<DT>::scalar(row, tok) : INFINITY;
+  if (tid < kWarps) sm.floor_w[tid] = -INFINITY;
+  if (tid == 0) sm.n = sm.n2 = 0;
+  __syncthreads();
 
-  float m = -INFINITY;
-  bool bad = false;
-  for (int x = tid; x < V; x += kThreads) {
-    const float z = Elem<DT>::scalar(row, x);
-    bad |= !(z < INFINITY);
-    m = fmaxf(m, z);
-  }
-  bad = __syncthreads_or(bad);
-  m = warp_max(m);
-  if (lane == 0) s_f[warp] = m;
-  __syncthreads();
-  m = s_f[0];
-  for (int w = 1; w < kWarps; ++w) m = fmaxf(m, s_f[w]);
-  if (bad || m == -INFINITY || (P.tokens && !tok_ok)) {
-    if (tid == 0) {
-      if (bad) flag(P, SV_DATA_BAD_LOGIT);
-      if (!bad && m == -INFINITY) flag(P, SV_DATA_EMPTY_ROW);
-      if (P.tokens && !tok_ok) flag(P, SV_DATA_BAD_TOKEN);
-      if (P.logprob) P.logprob[r] = NAN;
-      if (P.rank) P.rank[r] = 0;
-    }
-    if (bad || m == -INFINITY) {
-      if (tid == 0 && P.entropy) P.entropy[r] = NAN;
-      for (int j = tid; j < P.n_top; j += kThreads) {
-        if (P.top_ids) P.top_ids[(long long)r * P.n_top + j] = -1;
-        if (P.top_lp) P.top_lp[(long long)r * P.n_top + j] = NAN;
-      }
-      return;
-    }
-  }
-  const float zt = tok_ok ? Elem<DT>::scalar(row, tok) : 0.f;
-  float S = 0.f, S1 = 0.f;
+  const int q = (n_top + kWarps - 1) / kWarps;
+  const float far = kFar / P.c_hi;
+  const f2_t c_hi = f2_splat(P.c_hi), c_lo = f2_splat(P.c_lo);
+  const float lowest_value = DT == 1 ? __uint_as_float(0xff7f0000u) : -FLT_MAX;
+  float m = -INFINITY;  // this thread's maximum
+  uint32_t lowest = 0;
+  f2_t neg_m = 0ull;
+  f2_t S = 0ull, S1 = 0ull;
   int above = 0;
-  for (int x = tid; x < V; x += kThreads) {
-    const float z = Elem<DT>::scalar(row, x);
-    const float t = (z - m) * P.c;
-    const float e = ex2(t);
-    S += e;
-    if (e > 0.f) S1 = fmaf(e, t, S1);
-    above += z > zt || (z == zt && x < tok);
+  bool first = true;
+  for (int at = v0; at < v1; at += kThreads * kU) {
+    uint4 cur[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) cur[u] = nxt[u];
+    fetch(at + kThreads * kU);
+    const float bm = batch_max<DT>(cur);
+    if (!(bm <= m)) {  // a new maximum (or a NaN): move the sums to it
+      if (m > -INFINITY) {
+        const float d = (m - bm) * P.c_hi, f = d < -kFar ? 0.f : ex2(d);
+        S1 = f2_mul(f2_splat(f), f2_fma(f2_splat(d < -kFar ? 0.f : d), S, S1));
+        S = f2_mul(f2_splat(f), S);
+      }
+      m = bm;
+      neg_m = f2_splat(-m);
+      lowest = cut_off<DT>(m, far);
+    }
+    if (n_top) {
+      if (first) {  // no floor yet: the whole CTA's first maxima make one
+        const float w = warp_nth_largest(m, q);
+        if (lane == 0) sm.floor_w[warp] = w;
+        __syncthreads();
+      }
+      float floor = sm.floor_w[0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) floor = fminf(floor, sm.floor_w[w]);
+      // A warp that would keep much (values that rise along the row, a mask's end) raises its own floor first.
+      if (__popc(__ballot_sync(kFull, bm >= floor && bm > -INFINITY)) > 16) floor = fmaxf(floor, warp_nth_largest(m, n_top));
+      if (bm >= floor && bm > -INFINITY) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          float f[EPV];
+          Elem<DT>::unpack(cur[u], f);
+          const int x0 = (at + u * kThreads + tid) * EPV - off;
+#pragma unroll
+          for (int j = 0; j < EPV; ++j)
+            if (f[j] >= floor && f[j] > -INFINITY) {
+              const int k = atomicAdd(&sm.n, 1);
+              if (k < kCap) sm.cand[k] = make_float2(f[j] + 0.f, __int_as_float(x0 + j));
+            }
+        }
+      }
+      __syncwarp();
+      if (!first) {
+        const float w = warp_nth_largest(m, q);
+        if (lane == 0) sm.floor_w[warp] = w;
+      }
+      first = false;
+    }
+    if (bm >= zt) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        float f[EPV];
+        Elem<DT>::unpack(cur[u], f);
+        const int v = at + u * kThreads + tid, x0 = v * EPV - off;
+        if (v >= v1) continue;  // what is read behind the slice is -inf, as the token may be
+#pragma unroll
+        for (int j = 0; j < EPV; ++j) above += f[j] > zt || (f[j] == zt && (unsigned)(x0 + j) < (unsigned)tok);
+      }
+    }
+    if (m == lowest_value) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) add_lowest<DT>(cur[u], S);
+    } else if (bm != -INFINITY) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) add_terms<DT>(cur[u], lowest, neg_m, c_hi, c_lo, S, S1);
+    }
   }
-  double dS = S, dS1 = S1;
-  for (int o = 16; o > 0; o >>= 1) {
-    dS += __shfl_xor_sync(kFull, dS, o);
-    dS1 += __shfl_xor_sync(kFull, dS1, o);
-    above += __shfl_xor_sync(kFull, above, o);
+
+  // The CTA's sums: every thread's, moved to the common maximum.
+  float M = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(kFull, M, o));
+  float s0, s1, a0, a1;
+  f2_unpack(S, s0, s1);
+  f2_unpack(S1, a0, a1);
+  DF dS{0.f, 0.f}, dS1{0.f, 0.f};
+  if (!(m == -INFINITY)) {
+    const float d = (m - M) * P.c_hi, f = d < -kFar ? 0.f : ex2(d);
+    dS = df_mul_f(df_add_f(DF{s0, 0.f}, s1), f);
+    dS1 = df_mul_f(df_add(df_add_f(DF{a0, 0.f}, a1), df_mul_f(df_add_f(DF{s0, 0.f}, s1), d < -kFar ? 0.f : d)), f);
   }
+  dS = warp_sum_df(dS);
+  dS1 = warp_sum_df(dS1);
+  above = __reduce_add_sync(kFull, above);
   if (lane == 0) {
-    s_d[0][warp] = dS;
-    s_d[1][warp] = dS1;
-    s_i[warp] = above;
+    sm.red[warp][0] = M;
+    sm.red[warp][1] = dS.hi;
+    sm.red[warp][2] = dS.lo;
+    sm.red[warp][3] = dS1.hi;
+    sm.red[warp][4] = dS1.lo;
+    sm.cnt[warp] = above;
   }
   __syncthreads();
-  dS = dS1 = 0.0;
-  above = 0;
+
+  // The CTA's alternatives, in order.
+  if (n_top) {
+    float2* out = cl > 1 ? sm.mine : sm.best;
+    if (sm.n <= kCap) {
+      float floor = sm.floor_w[0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) floor = fminf(floor, sm.floor_w[w]);
+      const int c = sm.n;
+      // What reached the last floor, moved to the front in any order (the sort below does not depend on it).
+      float2 keep[kCap / kThreads];
+      int nk = 0;
+      for (int i = tid; i < c; i += kThreads) {
+        const float2 x = sm.cand[i];
+        if (x.x >= floor) keep[nk++] = x;
+      }
+      __syncthreads();
+      int at = nk ? atomicAdd(&sm.n2, nk) : 0;
+      for (int i = 0; i < nk; ++i) sm.cand[at + i] = keep[i];
+      __syncthreads();
+      sort_top(sm.cand, sm.n2, n_top, out);
+    } else {
+      // One pass an alternative: the largest pair behind the last one.
+      float2 last = make_float2(INFINITY, __int_as_float(-1));
+      for (int j = 0; j < n_top; ++j) {
+        float bv = -INFINITY;
+        int bi = INT_MAX;
+        for (int v = v0 + tid; v < v1; v += kThreads) {
+          float f[EPV];
+          Elem<DT>::unpack(load_vec<DT>(row, base, v, off, V), f);
+#pragma unroll
+          for (int e = 0; e < EPV; ++e) {
+            const int x = v * EPV - off + e;
+            if (f[e] < last.x || (f[e] == last.x && x > __float_as_int(last.y))) argmax_merge(bv, bi, f[e], x);
+          }
+        }
+        warp_argmax(bv, bi);
+        if (lane == 0) sm.cand[j % 2 * kWarps + warp] = make_float2(bv, __int_as_float(bi));
+        __syncthreads();
+        last = sm.cand[j % 2 * kWarps];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+          const float2 x = sm.cand[j % 2 * kWarps + w];
+          if (ahead(x, last)) last = x;
+        }
+        if (tid == 0) out[j] = last.x > -INFINITY ? make_float2(last.x + 0.f, last.y) : make_float2(-INFINITY, __int_as_float(-1));
+      }
+    }
+    __syncthreads();
+  }
+
+  // The row's: in its only CTA, or in the leader of the cluster.
+  float rM = -INFINITY;
+  DF rS{0.f, 0.f}, rS1{0.f, 0.f};
+  int rank_count = 0;
+  auto join = [&](float jM, DF jS, DF jS1) {
+    if (jM == -INFINITY) return;
+    const float top = max_nan(rM, jM);
+    const float d0 = (rM - top) * P.c_hi, d1 = (jM - top) * P.c_hi;
+    if (rM > -INFINITY) {
+      const float f = d0 < -kFar ? 0.f : ex2(d0);
+      rS1 = df_mul_f(df_add(rS1, df_mul_f(rS, d0 < -kFar ? 0.f : d0)), f);
+      rS = df_mul_f(rS, f);
+    }
+    const float f = d1 < -kFar ? 0.f : ex2(d1);
+    rS1 = df_add(rS1, df_mul_f(df_add(jS1, df_mul_f(jS, d1 < -kFar ? 0.f : d1)), f));
+    rS = df_add(rS, df_mul_f(jS, f));
+    rM = top;
+  };
+#pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    dS += s_d[0][w];
-    dS1 += s_d[1][w];
-    above += s_i[w];
+    join(sm.red[w][0], DF{sm.red[w][1], sm.red[w][2]}, DF{sm.red[w][3], sm.red[w][4]});
+    rank_count += sm.cnt[w];
   }
-  const double lnS = log(dS);
-  if (tid == 0) {
-    if (tok_ok) {
-      if (P.logprob) P.logprob[r] = (float)(((double)zt - (double)m) * P.inv_T - lnS);
-      if (P.rank) P.rank[r] = 1 + above;
-    }
-    if (P.entropy) P.entropy[r] = (float)(lnS - dS1 / dS * 0.6931471805599453);
-  }
-  // Alternatives: each pass finds the largest (value, lowest index) below the last.
-  float lv = INFINITY;
-  int li = -1;
-  for (int j = 0; j < P.n_top; ++j) {
-    float bv = -INFINITY;
-    int bi = INT_MAX;
-    for (int x = tid; x < V; x += kThreads) {
-      const float z = Elem<DT>::scalar(row, x);
-      if (z < lv || (z == lv && x > li)) argmax_merge(bv, bi, z, x);
-    }
-    warp_argmax(bv, bi);
-    __syncthreads();
-    if (lane == 0) {
-      s_f[warp] = bv;
-      s_i[warp] = bi;
-    }
-    __syncthreads();
-    lv = s_f[0];
-    li = s_i[0];
-    for (int w = 1; w < kWarps; ++w) argmax_merge(lv, li, s_f[w], s_i[w]);
+  if (cl > 1) {
+    cluster_sync();  // the leader has started
     if (tid == 0) {
-      const bool any = lv > -INFINITY;
-      if (P.top_ids) P.top_ids[(long long)r * P.n_top + j] = any ? li : -1;
-      if (P.top_lp)
-        P.top_lp[(long long)r * P.n_top + j] = any ? (float)(((double)lv - (double)m) * P.inv_T - lnS) : -INFINITY;
+      to_leader(&sm.rec[rank][0], rM);
+      to_leader(&sm.rec[rank][1], rS.hi);
+      to_leader(&sm.rec[rank][2], rS.lo);
+      to_leader(&sm.rec[rank][3], rS1.hi);
+      to_leader(&sm.rec[rank][4], rS1.lo);
+      to_leader(&sm.rec[rank][5], __int_as_float(rank_count));
+    }
+    for (int j = tid; j < n_top; j += kThreads) {
+      to_leader(&sm.best[rank * n_top + j].x, sm.mine[j].x);
+      to_leader(&sm.best[rank * n_top + j].y, sm.mine[j].y);
+    }
+    cluster_sync();
+    if (rank != 0) return;
+    rM = -INFINITY;
+    rS = rS1 = DF{0.f, 0.f};
+    rank_count = 0;
+    for (int k = 0; k < cl; ++k) {
+      join(sm.rec[k][0], DF{sm.rec[k][1], sm.rec[k][2]}, DF{sm.rec[k][3], sm.rec[k][4]});
+      rank_count += __float_as_int(sm.rec[k][5]);
+    }
+    if (n_top) {
+      sort_top(sm.best, cl * n_top, n_top, sm.cand);
+      __syncthreads();
     }
   }
+  const float2* top = cl > 1 ? sm.cand : sm.best;
+
+  const bool empty = rM == -INFINITY, bad = !empty && !(rS.hi < INFINITY);
+  const float lnS = logf(rS.hi) + rS.lo / rS.hi;
+  // (z - M) / T - ln S, the quotient with its rounding error.
+  auto logprob = [&](float z) {
+    const float d = z - rM, p = d * P.inv_T_hi, e = fmaf(d, P.inv_T_hi, -p) + d * P.inv_T_lo;
+    return isinf(p) ? p : (p - lnS) + e;
+  };
+  for (int j = tid; j < n_top; j += kThreads) {
+    const float2 x = top[j];
+    const bool any = x.x > -INFINITY;
+    const long long o = (long long)r * n_top + j;
+    if (P.top_ids) P.top_ids[o] = any && !bad && !empty ? __float_as_int(x.y) : -1;
+    if (P.top_lp) P.top_lp[o] = bad || empty ? NAN : any ? logprob(x.x) : -INFINITY;
+  }
+  if (tid == 0) {
+    if (bad) flag(P, SV_DATA_BAD_LOGIT);
+    if (empty) flag(P, SV_DATA_EMPTY_ROW);
+    if (P.tokens && !tok_ok) flag(P, SV_DATA_BAD_TOKEN);
+    const bool ok = !bad && !empty;
+    if (P.logprob) P.logprob[r] = ok && tok_ok ? logprob(zt) : NAN;
+    if (P.rank) P.rank[r] = ok && tok_ok ? 1 + rank_count : 0;
+    if (P.entropy) P.entropy[r] = ok ? lnS - (rS1.hi / rS.hi) * 0.69314718056f : NAN;
+  }
+}
+
+// CTAs to a row: enough for every processor to have work, but slices of a
+// few batches at least.
+inline int cluster_size(int R, long long row_bytes) {
+  int cl = 1;
+  while (cl < kMaxCluster && (long long)R * cl < 2 * 152 && row_bytes / (2 * cl) >= 8192) cl *= 2;
+  return cl;
 }
 
 }  // namespace lp
@@ -191,10 +544,10 @@ extern "C" sv_status sv_token_logprobs(const void* logits, sv_dtype dtype, int32
                                        int32_t* out_top_ids, float* out_top_logprobs, uint32_t* status,
                                        void* cuda_stream) {
   using namespace sv;
-  if ((dtype != SV_FP32 && dtype != SV_BF16) || V < 1 || ld < V || R < 0 || B < 0) return SV_ERR_INVALID_ARG;
+  if ((dtype != SV_FP32 && dtype != SV_BF16) || V < 1 || V > (1 << 30) || ld < V || R < 0 || B < 0) return SV_ERR_INVALID_ARG;
   const int es = dtype == SV_BF16 ? 2 : 4;
   if (ld > INT64_MAX / 4) return SV_ERR_INVALID_ARG;
-  if (!(temperature > 0.f) || std::isinf(temperature)) return SV_ERR_INVALID_ARG;
+  if (!(temperature >= 0x1p-100f && temperature <= 0x1p100f)) return SV_ERR_INVALID_ARG;
   if (n_top < 0 || n_top > SV_LOGPROBS_MAX_TOP) return SV_ERR_INVALID_ARG;
   if (!tokens && (out_logprob || out_rank)) return SV_ERR_INVALID_ARG;
   if ((cu_draft == nullptr) != (out_len == nullptr) || (!cu_draft && B != 0)) return SV_ERR_INVALID_ARG;
@@ -213,8 +566,11 @@ extern "C" sv_status sv_token_logprobs(const void* logits, sv_dtype dtype, int32
   P.tokens = tokens;
   P.cu = cu_draft;
   P.out_len = out_len;
-  P.c = (float)(1.4426950408889634 / (double)temperature);
-  P.inv_T = 1.0 / (double)temperature;
+  const double c = 1.4426950408889634 / (double)temperature, inv_T = 1.0 / (double)temperature;
+  P.c_hi = (float)c;
+  P.c_lo = std::isinf(P.c_hi) ? 0.f : (float)(c - (double)P.c_hi);
+  P.inv_T_hi = (float)inv_T;
+  P.inv_T_lo = std::isinf(P.inv_T_hi) ? 0.f : (float)(inv_T - (double)P.inv_T_hi);
   P.logprob = out_logprob;
   P.rank = out_rank;
   P.entropy = out_entropy;
@@ -222,9 +578,19 @@ extern "C" sv_status sv_token_logprobs(const void* logits, sv_dtype dtype, int32
   P.top_lp = out_top_logprobs;
   P.status = status;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  if (dtype == SV_BF16)
-    lp::logprobs_kernel<1><<<R, kThreads, 0, st>>>(P);
-  else
-    lp::logprobs_kernel<0><<<R, kThreads, 0, st>>>(P);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  const int cl = lp::cluster_size(R, (long long)V * es);
+  if ((long long)R * cl > INT32_MAX) return SV_ERR_INVALID_ARG;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(R * cl));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cl;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cl > 1 ? 1 : 0;
+  const cudaError_t e = dtype == SV_BF16 ? cudaLaunchKernelEx(&cfg, lp::logprobs_kernel<1>, P, cl)
+                                         : cudaLaunchKernelEx(&cfg, lp::logprobs_kernel<0>, P, cl);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }

@@ -32,7 +32,7 @@ def test_host_validation(lib):
     E = api.SV_ERR_INVALID_ARG
     assert _call(lib, R=0) == api.SV_OK
     assert _call(lib, B=0, cu=FAKE, ln=FAKE) == api.SV_OK  # a batch without requests: nothing to do
-    for bad in (dict(V=0), dict(ld=99), dict(ld=1 << 62), dict(R=-1), dict(dt=2), dict(T=0.0), dict(T=-1.0), dict(T=INF),
+    for bad in (dict(V=0), dict(ld=99), dict(ld=1 << 62), dict(R=-1), dict(dt=2), dict(T=0.0), dict(T=-1.0), dict(T=INF), dict(T=1e-31), dict(T=1e31),
                 dict(T=math.nan), dict(n=-1), dict(n=33), dict(tok=None), dict(B=1), dict(B=2, cu=FAKE), dict(B=2, ln=FAKE),
                 dict(B=-1, cu=FAKE, ln=FAKE), dict(z=None), dict(z=MISALIGNED), dict(tok=MISALIGNED), dict(lp=MISALIGNED),
                 dict(rank=MISALIGNED), dict(ent=MISALIGNED), dict(ids=MISALIGNED), dict(tlp=MISALIGNED), dict(st=MISALIGNED)):
@@ -148,7 +148,12 @@ def _shapes(V, dtype):
     block[: V // 2] = -INF                                      # half the vocabulary is masked
     far = torch.full((V,), -80.0)
     far[V // 3] = 90.0
-    return torch.stack(rows + [saw, zero, low, two, block, far]).to(dtype)
+    least = torch.full((V,), torch.finfo(dtype).min)            # nothing above the lowest value, and a padded tail
+    least[V // 2:] = -INF
+    huge = -1.0e6 - 8192.0 * (torch.arange(V) % 5)              # values whose next one is further off than any exponent reaches
+    up = torch.full((V,), 2.0e38)
+    up[V // 2:] = 1.0e38
+    return torch.stack(rows + [saw, zero, low, two, block, far, least, huge, up]).to(dtype)
 
 
 @pytest.mark.gpu
@@ -160,6 +165,17 @@ def test_ties_masks_and_orders(cuda_lib, dtype, V, copies):
     tok = torch.tensor([V - 1, 0, V // 2, V // 3] * z.shape[0])[: z.shape[0]].to(torch.int32)
     got = api.sv_token_logprobs(z.cuda(), tok.cuda(), n_top=32)
     _check(z, tok, 1.0, 32, got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [1e-8, 1e-3, 50.0, 1e9])
+def test_extreme_temperatures(cuda_lib, dtype, T):
+    z, tok = _logits(5, 9000, dtype, 21)
+    z[1, 100:8000] = -INF
+    z[2, : 4000] = -INF
+    tok[1], tok[2] = 3, 8999
+    _check(z, tok, T, 9, api.sv_token_logprobs(z.cuda(), tok.cuda(), temperature=T, n_top=9))
 
 
 @pytest.mark.gpu
