@@ -72,7 +72,8 @@ __device__ __forceinline__ void check_offsets(const Params& P, int tid) {
 }
 
 constexpr int kU = 4;            // 16-byte loads of a batch, per thread; the next batch's are in flight meanwhile
-constexpr int kCap = 2048;       // buffered candidates of a CTA
+constexpr int kVecs = 1024;      // vectors that a CTA buffers because one of their elements may be an alternative
+constexpr int kCap = 1024;       // elements that reached the last floor
 constexpr int kMaxCluster = 8;   // CTAs to a row, at most
 constexpr float kFar = 200.f;    // 2^-kFar is zero in fp32: exponents are cut off there
 
@@ -110,21 +111,26 @@ __device__ __forceinline__ uint32_t max_nan_bf2(uint32_t a, uint32_t b) {
   return d;
 }
 
+// The maxima of a batch's vectors (a bf16 pair of them, or one), and of the whole batch.
 template <int DT>
-__device__ __forceinline__ float batch_max(const uint4 (&v)[kU]) {
-  if constexpr (DT == 1) {
-    uint32_t m = max_nan_bf2(max_nan_bf2(v[0].x, v[0].y), max_nan_bf2(v[0].z, v[0].w));
+__device__ __forceinline__ uint32_t vec_max(const uint4& v) {
+  if constexpr (DT == 1)
+    return max_nan_bf2(max_nan_bf2(v.x, v.y), max_nan_bf2(v.z, v.w));
+  else
+    return __float_as_uint(max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                                   max_nan(__uint_as_float(v.z), __uint_as_float(v.w))));
+}
+template <int DT>
+__device__ __forceinline__ float max_value(uint32_t m) {
+  return DT == 1 ? max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u)) : __uint_as_float(m);
+}
+template <int DT>
+__device__ __forceinline__ float batch_max(const uint32_t (&vm)[kU]) {
+  uint32_t m = vm[0];
 #pragma unroll
-    for (int u = 1; u < kU; ++u) m = max_nan_bf2(m, max_nan_bf2(max_nan_bf2(v[u].x, v[u].y), max_nan_bf2(v[u].z, v[u].w)));
-    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
-  } else {
-    float m = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-      m = max_nan(m, max_nan(max_nan(__uint_as_float(v[u].x), __uint_as_float(v[u].y)),
-                             max_nan(__uint_as_float(v[u].z), __uint_as_float(v[u].w))));
-    return m;
-  }
+  for (int u = 1; u < kU; ++u)
+    m = DT == 1 ? max_nan_bf2(m, vm[u]) : __float_as_uint(max_nan(__uint_as_float(m), __uint_as_float(vm[u])));
+  return max_value<DT>(m);
 }
 
 __device__ __forceinline__ int order_key(float f) {  // whole numbers in the order of the floats
@@ -132,6 +138,15 @@ __device__ __forceinline__ int order_key(float f) {  // whole numbers in the ord
   return b < 0 ? b ^ 0x7fffffff : b;
 }
 __device__ __forceinline__ float key_value(int k) { return __int_as_float(k < 0 ? k ^ 0x7fffffff : k); }
+
+// The next value of the type below f; -inf stays. Zeros count as one.
+template <int DT>
+__device__ __forceinline__ float value_below(float f) {
+  if (f == -INFINITY) return f;
+  const int k = (f == 0.f ? -1 : order_key(f)) - (DT == 1 ? 0x10000 : 1);  // -1: the key of -0
+  if (DT == 1) return __uint_as_float(__float_as_uint(key_value(k)) & 0xffff0000u);
+  return key_value(k);
+}
 
 // Where logits are cut off below a maximum m: kFar in the exponent, rounded
 // down, and below m itself where that is less than a step. -inf where m is
@@ -199,15 +214,86 @@ __device__ __forceinline__ float warp_nth_largest(float v, int q) {
   return key_value(top);
 }
 
+// Sums of 2^((z - m) c) and their first moments about a maximum m.
+struct Sums {
+  float m;
+  DF S, S1;
+};
+
+// The sums of the warp's first `lanes` lanes (a power of two; the others
+// hold none: m = -inf, 0, 0), moved to their common maximum. The order of
+// the additions is fixed.
+__device__ __forceinline__ Sums join_lanes(Sums x, int lanes, float c) {
+  float m = x.m;
+  for (int o = lanes / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, o));
+  if (x.m == -INFINITY) {
+    x.S = x.S1 = DF{0.f, 0.f};
+  } else {
+    const float d = fmaxf((x.m - m) * c, -kFar), f = ex2(d);
+    x.S1 = df_mul_f(df_add(x.S1, df_mul_f(x.S, d)), f);
+    x.S = df_mul_f(x.S, f);
+  }
+  for (int o = lanes / 2; o > 0; o >>= 1) {
+    x.S = df_add(x.S, DF{__shfl_xor_sync(kFull, x.S.hi, o), __shfl_xor_sync(kFull, x.S.lo, o)});
+    x.S1 = df_add(x.S1, DF{__shfl_xor_sync(kFull, x.S1.hi, o), __shfl_xor_sync(kFull, x.S1.lo, o)});
+  }
+  // To every lane of the warp.
+  return Sums{__shfl_sync(kFull, m, 0), DF{__shfl_sync(kFull, x.S.hi, 0), __shfl_sync(kFull, x.S.lo, 0)},
+              DF{__shfl_sync(kFull, x.S1.hi, 0), __shfl_sync(kFull, x.S1.lo, 0)}};
+}
+
+// Adds the batch's elements that rank above the token: larger ones, and
+// equal ones of a lower index. Vectors before the token's count what is above
+// the value below zt, those behind it what is above zt.
+template <int DT>
+__device__ __forceinline__ void count_above(const uint4 (&cur)[kU], int at, int v1, int off, int tok, float zt, float zt_below,
+                                            int& above) {
+  constexpr int EPV = Elem<DT>::kEPV;
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    const int v = at + u * kThreads, x0 = v * EPV - off;
+    if (v >= v1) continue;  // what is read behind the slice is -inf, as the token may be
+    if (tok - x0 >= 0 && tok - x0 < EPV) {
+      float f[EPV];
+      Elem<DT>::unpack(cur[u], f);
+#pragma unroll
+      for (int j = 0; j < EPV; ++j) above += f[j] > zt || (f[j] == zt && x0 + j >= 0 && x0 + j < tok);
+      continue;
+    }
+    if (x0 < tok && zt == -INFINITY) {  // nothing is below: every element before the token counts
+      above += min(EPV, x0 + EPV);
+      continue;
+    }
+    const float z = x0 < tok ? zt_below : zt;
+    const uint32_t* w = &cur[u].x;
+    if constexpr (DT == 1) {
+      const uint32_t zz = (__float_as_uint(z) >> 16) * 0x10001u;
+      uint32_t n = 0;  // two counts to a word, as bf16 numbers
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t g;
+        asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(g) : "r"(w[j]), "r"(zz));
+        asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(n) : "r"(g));
+      }
+      above += (int)(__uint_as_float(n << 16) + __uint_as_float(n & 0xffff0000u));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) above += __uint_as_float(w[j]) > z;
+    }
+  }
+}
+
 struct Smem {
+  uint4 vec[kVecs];                // buffered vectors, and their places
+  int vec_at[kVecs];
   float2 cand[kCap];               // (logit, index as bits)
   float2 best[kMaxCluster * SV_LOGPROBS_MAX_TOP];  // the CTAs' sorted alternatives, in the leader
-  float rec[kMaxCluster][6];       // the CTAs' (M, S.hi, S.lo, S1.hi, S1.lo, rank count), in the leader
+  float rec[kMaxCluster][6];       // the CTAs' sums (m, S, S1) and rank counts, in the leader
   float2 mine[SV_LOGPROBS_MAX_TOP];
   float floor_w[kWarps];
-  float red[kWarps][5];
+  Sums sums[kWarps];
   int cnt[kWarps];
-  int n, n2, kept;
+  int n, n2;
 };
 
 __device__ __forceinline__ bool ahead(float2 a, float2 b) {  // a comes before b among the alternatives
@@ -279,6 +365,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
 
   uint4 nxt[kU];
   auto fetch = [&](int at) {
+    // Inside the row every vector of the CTA's batch is whole: no tests.
+    if (at > 0 && at + kThreads * kU <= v1 && at + kThreads * kU < n_vec) {
+      const char* p = base + (long long)(at + tid) * 16;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) nxt[u] = ld_stream16(p + u * kThreads * 16);
+      return;
+    }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int v = at + u * kThreads + tid;
@@ -289,7 +382,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
   fetch(v0);
   const int tok = P.tokens ? P.tokens[r] : -1;
   const bool tok_ok = tok >= 0 && tok < V;
-  const float zt = tok_ok ? Elem<DT>::scalar(row, tok) : INFINITY;
+  const float zt = tok_ok ? Elem<DT>::scalar(row, tok) + 0.f : INFINITY;
+  const float zt_below = value_below<DT>(zt);
   if (tid < kWarps) sm.floor_w[tid] = -INFINITY;
   if (tid == 0) sm.n = sm.n2 = 0;
   __syncthreads();
@@ -309,16 +403,20 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
 #pragma unroll
     for (int u = 0; u < kU; ++u) cur[u] = nxt[u];
     fetch(at + kThreads * kU);
-    const float bm = batch_max<DT>(cur);
+    uint32_t vm[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) vm[u] = vec_max<DT>(cur[u]);
+    const float bm = batch_max<DT>(vm);
     if (!(bm <= m)) {  // a new maximum (or a NaN): move the sums to it
       if (m > -INFINITY) {
-        const float d = (m - bm) * P.c_hi, f = d < -kFar ? 0.f : ex2(d);
-        S1 = f2_mul(f2_splat(f), f2_fma(f2_splat(d < -kFar ? 0.f : d), S, S1));
-        S = f2_mul(f2_splat(f), S);
+        const float d = fmaxf((m - bm) * P.c_hi, -kFar);
+        const f2_t f = f2_splat(ex2(d));
+        S1 = f2_mul(f, f2_fma(f2_splat(d), S, S1));
+        S = f2_mul(f, S);
       }
+      if (!(m > lowest_value)) lowest = cut_off<DT>(bm, far);  // then it stays: a higher maximum only makes its term smaller
       m = bm;
       neg_m = f2_splat(-m);
-      lowest = cut_off<DT>(m, far);
     }
     if (n_top) {
       if (first) {  // no floor yet: the whole CTA's first maxima make one
@@ -329,40 +427,34 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
       float floor = sm.floor_w[0];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) floor = fminf(floor, sm.floor_w[w]);
-      // A warp that would keep much (values that rise along the row, a mask's end) raises its own floor first.
-      if (__popc(__ballot_sync(kFull, bm >= floor && bm > -INFINITY)) > 16) floor = fmaxf(floor, warp_nth_largest(m, n_top));
-      if (bm >= floor && bm > -INFINITY) {
+      bool hit = bm >= floor && bm > -INFINITY;
+      const unsigned hits = __ballot_sync(kFull, hit);
+      if (hits) {
+        // A warp that would keep much (values that rise along the row, a mask's end) raises its own floor first.
+        if (__popc(hits) > 16) {
+          floor = fmaxf(floor, warp_nth_largest(m, n_top));
+          hit = bm >= floor && bm > -INFINITY;
+        }
+        if (hit) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          float f[EPV];
-          Elem<DT>::unpack(cur[u], f);
-          const int x0 = (at + u * kThreads + tid) * EPV - off;
-#pragma unroll
-          for (int j = 0; j < EPV; ++j)
-            if (f[j] >= floor && f[j] > -INFINITY) {
+          for (int u = 0; u < kU; ++u)
+            if (max_value<DT>(vm[u]) >= floor) {
               const int k = atomicAdd(&sm.n, 1);
-              if (k < kCap) sm.cand[k] = make_float2(f[j] + 0.f, __int_as_float(x0 + j));
+              if (k < kVecs) {
+                sm.vec[k] = cur[u];
+                sm.vec_at[k] = at + u * kThreads + tid;
+              }
             }
         }
-      }
-      __syncwarp();
-      if (!first) {
-        const float w = warp_nth_largest(m, q);
-        if (lane == 0) sm.floor_w[warp] = w;
+        __syncwarp();
+        if (!first) {
+          const float w = warp_nth_largest(m, q);
+          if (lane == 0) sm.floor_w[warp] = w;
+        }
       }
       first = false;
     }
-    if (bm >= zt) {
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        float f[EPV];
-        Elem<DT>::unpack(cur[u], f);
-        const int v = at + u * kThreads + tid, x0 = v * EPV - off;
-        if (v >= v1) continue;  // what is read behind the slice is -inf, as the token may be
-#pragma unroll
-        for (int j = 0; j < EPV; ++j) above += f[j] > zt || (f[j] == zt && (unsigned)(x0 + j) < (unsigned)tok);
-      }
-    }
+    if (bm >= zt) count_above<DT>(cur, at + tid, v1, off, tok, zt, zt_below, above);
     if (m == lowest_value) {
 #pragma unroll
       for (int u = 0; u < kU; ++u) add_lowest<DT>(cur[u], S);
@@ -372,53 +464,55 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
     }
   }
 
-  // The CTA's sums: every thread's, moved to the common maximum.
-  float M = m;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(kFull, M, o));
-  float s0, s1, a0, a1;
-  f2_unpack(S, s0, s1);
-  f2_unpack(S1, a0, a1);
-  DF dS{0.f, 0.f}, dS1{0.f, 0.f};
-  if (!(m == -INFINITY)) {
-    const float d = (m - M) * P.c_hi, f = d < -kFar ? 0.f : ex2(d);
-    dS = df_mul_f(df_add_f(DF{s0, 0.f}, s1), f);
-    dS1 = df_mul_f(df_add(df_add_f(DF{a0, 0.f}, a1), df_mul_f(df_add_f(DF{s0, 0.f}, s1), d < -kFar ? 0.f : d)), f);
-  }
-  dS = warp_sum_df(dS);
-  dS1 = warp_sum_df(dS1);
-  above = __reduce_add_sync(kFull, above);
-  if (lane == 0) {
-    sm.red[warp][0] = M;
-    sm.red[warp][1] = dS.hi;
-    sm.red[warp][2] = dS.lo;
-    sm.red[warp][3] = dS1.hi;
-    sm.red[warp][4] = dS1.lo;
-    sm.cnt[warp] = above;
+  // Every warp's sums, moved to its maximum.
+  {
+    float s0, s1, a0, a1;
+    f2_unpack(S, s0, s1);
+    f2_unpack(S1, a0, a1);
+    Sums x{m, df_add_f(DF{s0, 0.f}, s1), df_add_f(DF{a0, 0.f}, a1)};
+    x = join_lanes(x, 32, P.c_hi);
+    above = __reduce_add_sync(kFull, above);
+    if (lane == 0) {
+      sm.sums[warp] = x;
+      sm.cnt[warp] = above;
+    }
   }
   __syncthreads();
 
   // The CTA's alternatives, in order.
   if (n_top) {
     float2* out = cl > 1 ? sm.mine : sm.best;
-    if (sm.n <= kCap) {
-      float floor = sm.floor_w[0];
+    float floor = sm.floor_w[0];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) floor = fminf(floor, sm.floor_w[w]);
-      const int c = sm.n;
-      // What reached the last floor, moved to the front in any order (the sort below does not depend on it).
-      float2 keep[kCap / kThreads];
-      int nk = 0;
+    for (int w = 1; w < kWarps; ++w) floor = fminf(floor, sm.floor_w[w]);
+    if (floor == -INFINITY) {  // short or masked slices: one warp's n elements may still make a floor
+      __syncthreads();
+      const float w = warp_nth_largest(m, n_top);
+      if (lane == 0) sm.floor_w[warp] = w;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) floor = fmaxf(floor, sm.floor_w[k]);
+    }
+    const int c = sm.n;
+    if (c <= kVecs) {
+      // What reached the last floor, in any order: the sort below does not depend on it.
       for (int i = tid; i < c; i += kThreads) {
-        const float2 x = sm.cand[i];
-        if (x.x >= floor) keep[nk++] = x;
+        float f[EPV];
+        Elem<DT>::unpack(sm.vec[i], f);
+        const int x0 = sm.vec_at[i] * EPV - off;
+#pragma unroll
+        for (int j = 0; j < EPV; ++j)
+          if (f[j] >= floor && f[j] > -INFINITY) {
+            const int k = atomicAdd(&sm.n2, 1);
+            if (k < kCap) sm.cand[k] = make_float2(f[j] + 0.f, __int_as_float(x0 + j));
+          }
       }
       __syncthreads();
-      int at = nk ? atomicAdd(&sm.n2, nk) : 0;
-      for (int i = 0; i < nk; ++i) sm.cand[at + i] = keep[i];
-      __syncthreads();
+    }
+    if (c <= kVecs && sm.n2 <= kCap) {
       sort_top(sm.cand, sm.n2, n_top, out);
     } else {
+      __syncthreads();
       // One pass an alternative: the largest pair behind the last one.
       float2 last = make_float2(INFINITY, __int_as_float(-1));
       for (int j = 0; j < n_top; ++j) {
@@ -448,38 +542,23 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
     __syncthreads();
   }
 
-  // The row's: in its only CTA, or in the leader of the cluster.
-  float rM = -INFINITY;
-  DF rS{0.f, 0.f}, rS1{0.f, 0.f};
-  int rank_count = 0;
-  auto join = [&](float jM, DF jS, DF jS1) {
-    if (jM == -INFINITY) return;
-    const float top = max_nan(rM, jM);
-    const float d0 = (rM - top) * P.c_hi, d1 = (jM - top) * P.c_hi;
-    if (rM > -INFINITY) {
-      const float f = d0 < -kFar ? 0.f : ex2(d0);
-      rS1 = df_mul_f(df_add(rS1, df_mul_f(rS, d0 < -kFar ? 0.f : d0)), f);
-      rS = df_mul_f(rS, f);
+  // The CTA's sums by its first warp; in a cluster the leader's joins the CTAs'.
+  Sums row_sums{-INFINITY, DF{0.f, 0.f}, DF{0.f, 0.f}};
+  int count = 0;
+  if (warp == 0) {
+    if (lane < kWarps) {
+      row_sums = sm.sums[lane];
+      count = sm.cnt[lane];
     }
-    const float f = d1 < -kFar ? 0.f : ex2(d1);
-    rS1 = df_add(rS1, df_mul_f(df_add(jS1, df_mul_f(jS, d1 < -kFar ? 0.f : d1)), f));
-    rS = df_add(rS, df_mul_f(jS, f));
-    rM = top;
-  };
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    join(sm.red[w][0], DF{sm.red[w][1], sm.red[w][2]}, DF{sm.red[w][3], sm.red[w][4]});
-    rank_count += sm.cnt[w];
+    row_sums = join_lanes(row_sums, kWarps, P.c_hi);
+    count = __reduce_add_sync(kFull, count);
   }
   if (cl > 1) {
     cluster_sync();  // the leader has started
     if (tid == 0) {
-      to_leader(&sm.rec[rank][0], rM);
-      to_leader(&sm.rec[rank][1], rS.hi);
-      to_leader(&sm.rec[rank][2], rS.lo);
-      to_leader(&sm.rec[rank][3], rS1.hi);
-      to_leader(&sm.rec[rank][4], rS1.lo);
-      to_leader(&sm.rec[rank][5], __int_as_float(rank_count));
+      const float word[6] = {row_sums.m, row_sums.S.hi, row_sums.S.lo, row_sums.S1.hi, row_sums.S1.lo, __int_as_float(count)};
+#pragma unroll
+      for (int k = 0; k < 6; ++k) to_leader(&sm.rec[rank][k], word[k]);
     }
     for (int j = tid; j < n_top; j += kThreads) {
       to_leader(&sm.best[rank * n_top + j].x, sm.mine[j].x);
@@ -487,42 +566,47 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
     }
     cluster_sync();
     if (rank != 0) return;
-    rM = -INFINITY;
-    rS = rS1 = DF{0.f, 0.f};
-    rank_count = 0;
-    for (int k = 0; k < cl; ++k) {
-      join(sm.rec[k][0], DF{sm.rec[k][1], sm.rec[k][2]}, DF{sm.rec[k][3], sm.rec[k][4]});
-      rank_count += __float_as_int(sm.rec[k][5]);
-    }
     if (n_top) {
       sort_top(sm.best, cl * n_top, n_top, sm.cand);
       __syncthreads();
     }
+    if (warp == 0) {
+      row_sums = Sums{-INFINITY, DF{0.f, 0.f}, DF{0.f, 0.f}};
+      count = 0;
+      if (lane < cl) {
+        const float* w = sm.rec[lane];
+        row_sums = Sums{w[0], DF{w[1], w[2]}, DF{w[3], w[4]}};
+        count = __float_as_int(w[5]);
+      }
+      row_sums = join_lanes(row_sums, kMaxCluster, P.c_hi);
+      count = __reduce_add_sync(kFull, count);
+    }
   }
+  if (warp != 0) return;
   const float2* top = cl > 1 ? sm.cand : sm.best;
-
-  const bool empty = rM == -INFINITY, bad = !empty && !(rS.hi < INFINITY);
+  const float M = row_sums.m;
+  const DF rS = row_sums.S;
+  const bool empty = M == -INFINITY, bad = !empty && !(rS.hi < INFINITY), ok = !empty && !bad;
   const float lnS = logf(rS.hi) + rS.lo / rS.hi;
   // (z - M) / T - ln S, the quotient with its rounding error.
   auto logprob = [&](float z) {
-    const float d = z - rM, p = d * P.inv_T_hi, e = fmaf(d, P.inv_T_hi, -p) + d * P.inv_T_lo;
+    const float d = z - M, p = d * P.inv_T_hi, e = fmaf(d, P.inv_T_hi, -p) + d * P.inv_T_lo;
     return isinf(p) ? p : (p - lnS) + e;
   };
-  for (int j = tid; j < n_top; j += kThreads) {
-    const float2 x = top[j];
+  if (lane < n_top) {  // n_top <= 32
+    const float2 x = top[lane];
     const bool any = x.x > -INFINITY;
-    const long long o = (long long)r * n_top + j;
-    if (P.top_ids) P.top_ids[o] = any && !bad && !empty ? __float_as_int(x.y) : -1;
-    if (P.top_lp) P.top_lp[o] = bad || empty ? NAN : any ? logprob(x.x) : -INFINITY;
+    const long long o = (long long)r * n_top + lane;
+    if (P.top_ids) P.top_ids[o] = any && ok ? __float_as_int(x.y) : -1;
+    if (P.top_lp) P.top_lp[o] = !ok ? NAN : any ? logprob(x.x) : -INFINITY;
   }
-  if (tid == 0) {
+  if (lane == 0) {
     if (bad) flag(P, SV_DATA_BAD_LOGIT);
     if (empty) flag(P, SV_DATA_EMPTY_ROW);
     if (P.tokens && !tok_ok) flag(P, SV_DATA_BAD_TOKEN);
-    const bool ok = !bad && !empty;
     if (P.logprob) P.logprob[r] = ok && tok_ok ? logprob(zt) : NAN;
-    if (P.rank) P.rank[r] = ok && tok_ok ? 1 + rank_count : 0;
-    if (P.entropy) P.entropy[r] = ok ? lnS - (rS1.hi / rS.hi) * 0.69314718056f : NAN;
+    if (P.rank) P.rank[r] = ok && tok_ok ? 1 + count : 0;
+    if (P.entropy) P.entropy[r] = ok ? lnS - (row_sums.S1.hi / rS.hi) * 0.69314718056f : NAN;
   }
 }
 
