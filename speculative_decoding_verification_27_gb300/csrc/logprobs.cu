@@ -242,73 +242,103 @@ __device__ __forceinline__ Sums join_lanes(Sums x, int lanes, float c) {
               DF{__shfl_sync(kFull, x.S1.hi, 0), __shfl_sync(kFull, x.S1.lo, 0)}};
 }
 
-// Adds the batch's elements that rank above the token: larger ones, and
-// equal ones of a lower index. Vectors before the token's count what is above
-// the value below zt, those behind it what is above zt.
+// The batch's elements that rank above the token: larger ones, and equal
+// ones of a lower index. `at` is the thread's first vector.
 template <int DT>
-__device__ __forceinline__ void count_above(const uint4 (&cur)[kU], int at, int v1, int off, int tok, float zt, float zt_below,
-                                            int& above) {
+__device__ __forceinline__ int count_above_near(const uint4 (&cur)[kU], int at, int v1, int off, int tok, float zt) {
   constexpr int EPV = Elem<DT>::kEPV;
+  int n = 0;
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
     const int v = at + u * kThreads, x0 = v * EPV - off;
-    if (v >= v1) continue;  // what is read behind the slice is -inf, as the token may be
-    if (tok - x0 >= 0 && tok - x0 < EPV) {
-      float f[EPV];
-      Elem<DT>::unpack(cur[u], f);
+    float f[EPV];
+    Elem<DT>::unpack(cur[u], f);
+    if (v < v1) {  // what is read behind the slice is -inf, as the token may be
 #pragma unroll
-      for (int j = 0; j < EPV; ++j) above += f[j] > zt || (f[j] == zt && x0 + j >= 0 && x0 + j < tok);
-      continue;
+      for (int j = 0; j < EPV; ++j) n += f[j] > zt || (f[j] == zt && x0 + j >= 0 && x0 + j < tok);
     }
-    if (x0 < tok && zt == -INFINITY) {  // nothing is below: every element before the token counts
-      above += min(EPV, x0 + EPV);
-      continue;
-    }
-    const float z = x0 < tok ? zt_below : zt;
-    const uint32_t* w = &cur[u].x;
-    if constexpr (DT == 1) {
-      const uint32_t zz = (__float_as_uint(z) >> 16) * 0x10001u;
-      uint32_t n = 0;  // two counts to a word, as bf16 numbers
+  }
+  return n;
+}
+// The same for a batch that lies before the token or behind it as a whole:
+// how many are above z, which is the token's logit, or the value below it.
+template <int DT>
+__device__ __forceinline__ int count_above(const uint4 (&cur)[kU], float z) {
+  if constexpr (DT == 1) {
+    const uint32_t zz = (__float_as_uint(z) >> 16) * 0x10001u;
+    uint32_t n = 0;  // two counts to a word, as bf16 numbers (of 4 * kU at most)
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const uint32_t* w = &cur[u].x;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t g;
         asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(g) : "r"(w[j]), "r"(zz));
         asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(n) : "r"(g));
       }
-      above += (int)(__uint_as_float(n << 16) + __uint_as_float(n & 0xffff0000u));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) above += __uint_as_float(w[j]) > z;
     }
+    return (int)(__uint_as_float(n << 16) + __uint_as_float(n & 0xffff0000u));
+  } else {
+    int n = 0;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const uint32_t* w = &cur[u].x;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) n += __uint_as_float(w[j]) > z;
+    }
+    return n;
   }
 }
+
+// An alternative as one number: larger logits first, then lower indices.
+typedef unsigned long long u64;
+__device__ __forceinline__ u64 make_key(float z, int x) {
+  return (u64)((uint32_t)order_key(z + 0.f) ^ 0x80000000u) << 32 | (uint32_t)~x;
+}
+__device__ __forceinline__ float key_logit(u64 k) { return key_value((int)((uint32_t)(k >> 32) ^ 0x80000000u)); }
+__device__ __forceinline__ int key_index(u64 k) { return (int)~(uint32_t)k; }
+// None: below every finite logit's key, and different for every j.
+__device__ __forceinline__ u64 no_key(int j) { return (u64)j; }
+__device__ __forceinline__ bool is_key(u64 k) { return (k >> 32) > 0x007fffffull; }
 
 struct Smem {
   uint4 vec[kVecs];                // buffered vectors, and their places
   int vec_at[kVecs];
-  float2 cand[kCap];               // (logit, index as bits)
-  float2 best[kMaxCluster * SV_LOGPROBS_MAX_TOP];  // the CTAs' sorted alternatives, in the leader
+  alignas(16) u64 cand[kCap];      // alternatives as keys
+  alignas(16) u64 best[kMaxCluster * SV_LOGPROBS_MAX_TOP];  // the CTAs' sorted alternatives, in the leader
   float rec[kMaxCluster][6];       // the CTAs' sums (m, S, S1) and rank counts, in the leader
-  float2 mine[SV_LOGPROBS_MAX_TOP];
-  float floor_w[kWarps];
+  u64 mine[SV_LOGPROBS_MAX_TOP];
+  alignas(16) float floor_w[kWarps];
   Sums sums[kWarps];
   int cnt[kWarps];
   int n, n2;
 };
 
-__device__ __forceinline__ bool ahead(float2 a, float2 b) {  // a comes before b among the alternatives
-  return a.x > b.x || (a.x == b.x && __float_as_int(a.y) < __float_as_int(b.y));
+// n elements of the row reach the least of the warps' floors.
+__device__ __forceinline__ float shared_floor(const Smem& sm) {
+  float f = sm.floor_w[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) f = fminf(f, sm.floor_w[w]);
+  return f;
 }
 
-// The first n of c candidates in order, to out[0 .. n): each thread counts who is ahead of its own. Places that stay free are
-// (-inf, -1). Every thread of the CTA calls it.
-__device__ __forceinline__ void sort_top(const float2* from, int c, int n, float2* out) {
-  for (int j = threadIdx.x; j < n; j += kThreads)
-    if (j >= c) out[j] = make_float2(-INFINITY, __int_as_float(-1));
+// The first n of c keys in descending order, to out[0 .. n); places that
+// stay free get keys that stand for none. Each thread counts the keys above
+// its own (they are all different); `from` has room for one more.
+__device__ __forceinline__ void sort_top(u64* from, int c, int n, u64* out) {
+  for (int j = c + threadIdx.x; j < n; j += kThreads) out[j] = no_key(j);
+  if (c & 1) {
+    if (threadIdx.x == 0) from[c] = 0;
+    __syncthreads();
+  }
   for (int i = threadIdx.x; i < c; i += kThreads) {
-    const float2 x = from[i];
+    const u64 x = from[i];
     int k = 0;
-    for (int j = 0; j < c; ++j) k += ahead(from[j], x) || (j < i && !ahead(x, from[j]));
+#pragma unroll 8
+    for (int j = 0; j < c; j += 2) {
+      const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(from + j);
+      k += (y.x > x) + (y.y > x);
+    }
     if (k < n) out[k] = x;
   }
 }
@@ -343,6 +373,11 @@ __device__ __forceinline__ void to_leader(void* p, float v) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_addr(p)));
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ void to_leader(u64* p, u64 v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_addr(p)));
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 
 // A cluster of `cl` CTAs takes a row, each a contiguous slice of its vectors.
@@ -384,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
   const bool tok_ok = tok >= 0 && tok < V;
   const float zt = tok_ok ? Elem<DT>::scalar(row, tok) + 0.f : INFINITY;
   const float zt_below = value_below<DT>(zt);
+  const int tok_v = (tok + off) / EPV;  // the token's vector
   if (tid < kWarps) sm.floor_w[tid] = -INFINITY;
   if (tid == 0) sm.n = sm.n2 = 0;
   __syncthreads();
@@ -398,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
   f2_t S = 0ull, S1 = 0ull;
   int above = 0;
   bool first = true;
+  float floor = -INFINITY;
   for (int at = v0; at < v1; at += kThreads * kU) {
     uint4 cur[kU];
 #pragma unroll
@@ -423,17 +460,17 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
         const float w = warp_nth_largest(m, q);
         if (lane == 0) sm.floor_w[warp] = w;
         __syncthreads();
+        floor = shared_floor(sm);
       }
-      float floor = sm.floor_w[0];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) floor = fminf(floor, sm.floor_w[w]);
       bool hit = bm >= floor && bm > -INFINITY;
-      const unsigned hits = __ballot_sync(kFull, hit);
-      if (hits) {
+      if (__any_sync(kFull, hit)) {
+        floor = shared_floor(sm);
+        hit = hit && bm >= floor;
+        const unsigned hits = __ballot_sync(kFull, hit);
         // A warp that would keep much (values that rise along the row, a mask's end) raises its own floor first.
         if (__popc(hits) > 16) {
           floor = fmaxf(floor, warp_nth_largest(m, n_top));
-          hit = bm >= floor && bm > -INFINITY;
+          hit = hit && bm >= floor;
         }
         if (hit) {
 #pragma unroll
@@ -454,7 +491,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
       }
       first = false;
     }
-    if (bm >= zt) count_above<DT>(cur, at + tid, v1, off, tok, zt, zt_below, above);
+    if (__any_sync(kFull, bm >= zt)) {
+      // Nothing is below -inf: there, and around the token itself, element by element.
+      const bool near = zt == -INFINITY || (tok_v >= at && tok_v < at + kThreads * kU);
+      above += near ? count_above_near<DT>(cur, at + tid, v1, off, tok, zt) : count_above<DT>(cur, at < tok_v ? zt_below : zt);
+    }
     if (m == lowest_value) {
 #pragma unroll
       for (int u = 0; u < kU; ++u) add_lowest<DT>(cur[u], S);
@@ -481,10 +522,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
 
   // The CTA's alternatives, in order.
   if (n_top) {
-    float2* out = cl > 1 ? sm.mine : sm.best;
-    float floor = sm.floor_w[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) floor = fminf(floor, sm.floor_w[w]);
+    u64* out = cl > 1 ? sm.mine : sm.best;
+    floor = shared_floor(sm);
     if (floor == -INFINITY) {  // short or masked slices: one warp's n elements may still make a floor
       __syncthreads();
       const float w = warp_nth_largest(m, n_top);
@@ -504,39 +543,42 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
         for (int j = 0; j < EPV; ++j)
           if (f[j] >= floor && f[j] > -INFINITY) {
             const int k = atomicAdd(&sm.n2, 1);
-            if (k < kCap) sm.cand[k] = make_float2(f[j] + 0.f, __int_as_float(x0 + j));
+            if (k < kCap - 1) sm.cand[k] = make_key(f[j], x0 + j);
           }
       }
       __syncthreads();
     }
-    if (c <= kVecs && sm.n2 <= kCap) {
+    if (c <= kVecs && sm.n2 < kCap) {
       sort_top(sm.cand, sm.n2, n_top, out);
     } else {
       __syncthreads();
-      // One pass an alternative: the largest pair behind the last one.
-      float2 last = make_float2(INFINITY, __int_as_float(-1));
+      // One pass an alternative: the largest key below the last one.
+      u64 last = ~0ull;
       for (int j = 0; j < n_top; ++j) {
-        float bv = -INFINITY;
-        int bi = INT_MAX;
+        u64 best = 0;
         for (int v = v0 + tid; v < v1; v += kThreads) {
           float f[EPV];
           Elem<DT>::unpack(load_vec<DT>(row, base, v, off, V), f);
 #pragma unroll
           for (int e = 0; e < EPV; ++e) {
-            const int x = v * EPV - off + e;
-            if (f[e] < last.x || (f[e] == last.x && x > __float_as_int(last.y))) argmax_merge(bv, bi, f[e], x);
+            const u64 k = make_key(f[e], v * EPV - off + e);
+            if (f[e] > -INFINITY && k < last && k > best) best = k;
           }
         }
-        warp_argmax(bv, bi);
-        if (lane == 0) sm.cand[j % 2 * kWarps + warp] = make_float2(bv, __int_as_float(bi));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const u64 k = __shfl_xor_sync(kFull, best, o);
+          best = k > best ? k : best;
+        }
+        if (lane == 0) sm.cand[j % 2 * kWarps + warp] = best;
         __syncthreads();
         last = sm.cand[j % 2 * kWarps];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) {
-          const float2 x = sm.cand[j % 2 * kWarps + w];
-          if (ahead(x, last)) last = x;
+          const u64 k = sm.cand[j % 2 * kWarps + w];
+          last = k > last ? k : last;
         }
-        if (tid == 0) out[j] = last.x > -INFINITY ? make_float2(last.x + 0.f, last.y) : make_float2(-INFINITY, __int_as_float(-1));
+        if (tid == 0) out[j] = is_key(last) ? last : no_key(j);
       }
     }
     __syncthreads();
@@ -561,8 +603,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
       for (int k = 0; k < 6; ++k) to_leader(&sm.rec[rank][k], word[k]);
     }
     for (int j = tid; j < n_top; j += kThreads) {
-      to_leader(&sm.best[rank * n_top + j].x, sm.mine[j].x);
-      to_leader(&sm.best[rank * n_top + j].y, sm.mine[j].y);
+      const u64 k = sm.mine[j];
+      to_leader(&sm.best[rank * n_top + j], is_key(k) ? k : no_key(rank * n_top + j));
     }
     cluster_sync();
     if (rank != 0) return;
@@ -583,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
     }
   }
   if (warp != 0) return;
-  const float2* top = cl > 1 ? sm.cand : sm.best;
+  const u64* top = cl > 1 ? sm.cand : sm.best;
   const float M = row_sums.m;
   const DF rS = row_sums.S;
   const bool empty = M == -INFINITY, bad = !empty && !(rS.hi < INFINITY), ok = !empty && !bad;
@@ -594,11 +636,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
     return isinf(p) ? p : (p - lnS) + e;
   };
   if (lane < n_top) {  // n_top <= 32
-    const float2 x = top[lane];
-    const bool any = x.x > -INFINITY;
+    const u64 x = top[lane];
+    const bool any = is_key(x);
     const long long o = (long long)r * n_top + lane;
-    if (P.top_ids) P.top_ids[o] = any && ok ? __float_as_int(x.y) : -1;
-    if (P.top_lp) P.top_lp[o] = !ok ? NAN : any ? logprob(x.x) : -INFINITY;
+    if (P.top_ids) P.top_ids[o] = any && ok ? key_index(x) : -1;
+    if (P.top_lp) P.top_lp[o] = !ok ? NAN : any ? logprob(key_logit(x)) : -INFINITY;
   }
   if (lane == 0) {
     if (bad) flag(P, SV_DATA_BAD_LOGIT);
