@@ -27,7 +27,8 @@ struct Params {
   long long q_row_b, out_row_b;
   float* lse;
   float scale_log2;  // scale * log2(e); for the tensor core kernel its absolute value, and
-  uint32_t q_sign;   // the bits that turn q's sign
+  uint32_t q_sign;   // the bits that turn q's sign; with a scale of zero q is
+  uint32_t q_mask;   // masked to zero and scaled by one
   int group;         // query heads to a key-value head
   uint32_t* status;
 };
@@ -111,7 +112,6 @@ __global__ void __launch_bounds__(kT) window_kernel(Params P) {
 // ---------------------------------------------------------------------------
 // bf16: tensor cores over a paged pipeline
 // ---------------------------------------------------------------------------
-constexpr int kTW = 128;   // threads: four warps
 constexpr int kTK = 64;    // tokens of a key tile
 
 // How the work is cut. A unit is a (request, key-value head, tile of MT
@@ -205,9 +205,12 @@ constexpr size_t part_bytes() {
 template <int D, int WM>
 struct Shape {
   static constexpr int MT = 16 * WM;            // stacked rows of a unit
-  static constexpr int WK = 4 / WM;             // warps that split a key tile
+  static constexpr int WK = WM < 4 ? 4 / WM : 1;  // warps that split a key tile
+  static constexpr int kT = 32 * WM * WK;       // threads
   static constexpr int KW = kTK / WK;           // tokens of a tile for one warp
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int KS = KW < 32 ? KW : 32;  // tokens that go through the softmax at once
+  static constexpr int kCtas = D == 64 && WM == 4 ? 3 : D == 128 && WM == 8 ? 1 : 2;  // an SM
+  static constexpr int kStages = D == 128 ? (WM == 8 ? 5 : 3) : (WM == 4 ? 4 : 6);
   static constexpr int kTile = kTK * D * 2;     // bytes of K (or V) of a tile
   static constexpr size_t smem = (size_t)kStages * 2 * kTile + (kStages + 1) * (kTK * 8 + 16);
   // The warps that split the keys join in the stage that they have just used.
@@ -222,8 +225,9 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 }
 
 template <int D, int WM>
-__global__ void __launch_bounds__(kTW, 2) window_mma_kernel(Params P, Plan L) {
+__global__ void __launch_bounds__(Shape<D, WM>::kT, Shape<D, WM>::kCtas) window_mma_kernel(Params P, Plan L) {
   using Sh = Shape<D, WM>;
+  constexpr int kTW = Sh::kT, KS = Sh::KS;
   constexpr int MT = Sh::MT, WK = Sh::WK, KW = Sh::KW, S = Sh::kStages;
   constexpr int ND = D / 8;    // n-tiles of the output
   constexpr int KD = D / 16;   // k-steps of a score
@@ -233,7 +237,7 @@ __global__ void __launch_bounds__(kTW, 2) window_mma_kernel(Params P, Plan L) {
   char* s_kv = smem;
   long long* s_off = reinterpret_cast<long long*>(smem + S * 2 * Sh::kTile);  // [S + 1][kTK]
   uint32_t* s_valid = reinterpret_cast<uint32_t*>(s_off + (S + 1) * kTK);                  // [S + 1][4]
-  __shared__ long long s_scan[4];
+  __shared__ long long s_scan[kTW / 32];
   __shared__ int s_start[2];
   __shared__ long long s_first;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -257,7 +261,7 @@ __global__ void __launch_bounds__(kTW, 2) window_mma_kernel(Params P, Plan L) {
   if (lane == 31) s_scan[warp] = incl;
   __syncthreads();
   long long total = 0;
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < kTW / 32; ++w) {
     if (w < warp) incl += s_scan[w];
     total += s_scan[w];
   }
@@ -347,14 +351,21 @@ __global__ void __launch_bounds__(kTW, 2) window_mma_kernel(Params P, Plan L) {
     }
   };
 
-  // The first S - 1 tiles, and the lookup behind them.
+  // The first S - 1 tiles, and the lookup behind them: all S table loads before the first is used.
   int page, place;
-  for (int i = 0; i < S; ++i) {
-    if (i < n_tiles) {
-      lookup(ld, page, place);
-      store_lookup(i, ld.u.head, page, place);
-      if (i + 1 < n_tiles && ++ld.tile == ld.u.tiles) next_unit(ld);
+  {
+    int pages[S], places[S], heads[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      if (i < n_tiles) {
+        lookup(ld, pages[i], places[i]);
+        heads[i] = ld.u.head;
+        if (i + 1 < n_tiles && ++ld.tile == ld.u.tiles) next_unit(ld);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+      if (i < n_tiles) store_lookup(i, heads[i], pages[i], places[i]);
   }
   __syncthreads();
 #pragma unroll
@@ -400,8 +411,8 @@ __global__ void __launch_bounds__(kTW, 2) window_mma_kernel(Params P, Plan L) {
                                                                 (long long)(cp.u.head * P.group + h) * (D * 2)) + (lane & 3);
 #pragma unroll
         for (int k = 0; k < KD; ++k) {
-          q[k][e] = ok ? __ldg(src + k * 8) ^ P.q_sign : 0u;
-          q[k][e + 2] = ok ? __ldg(src + k * 8 + 4) ^ P.q_sign : 0u;
+          q[k][e] = ok ? (__ldg(src + k * 8) & P.q_mask) ^ P.q_sign : 0u;
+          q[k][e + 2] = ok ? (__ldg(src + k * 8 + 4) & P.q_mask) ^ P.q_sign : 0u;
         }
         m_run[e] = -INFINITY;
         l_run[e] = 0.f;
@@ -418,93 +429,87 @@ __global__ void __launch_bounds__(kTW, 2) window_mma_kernel(Params P, Plan L) {
     cp_commit();
 
     const uint32_t kb = smem_addr(s_kv) + (i % S) * 2 * Sh::kTile, vb = kb + Sh::kTile;
-    const int key0 = wk * KW;
-    float s[KW / 8][4];
-#pragma unroll
-    for (int n = 0; n < KW / 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
-#pragma unroll
-    for (int k = 0; k < KD; ++k) {
-#pragma unroll
-      for (int n = 0; n < KW / 8; n += 2) {
-        uint32_t b[4];  // tokens n*8 .. +7 at d k*16 and +8, then tokens +8 .. +15
-        const int r = key0 + n * 8 + (lane & 7) + ((lane >> 4) << 3), c = k * 2 + ((lane >> 3) & 1);
-        ldsm4(b, kb + swz<D>(r, c));
-        mma_bf16(s[n], q[k], b[0], b[1]);
-        mma_bf16(s[n + 1], q[k], b[2], b[3]);
-      }
-    }
-    // Hidden tokens: behind the history all but the row's part of the window, and those without a page.
     const int ring = i % (S + 1);
-    const uint32_t valid = s_valid[ring * 4 + (key0 >> 5)];
-    const int t_end = (cp.tile + 1) * kTK;
-    const bool whole = (s_valid[ring * 4] & s_valid[ring * 4 + 1]) == 0xffffffffu;
-    if (t_end > cp.u.ctx || !whole) {
+    const bool masked = (cp.tile + 1) * kTK > cp.u.ctx || (s_valid[ring * 4] & s_valid[ring * 4 + 1]) != 0xffffffffu;
 #pragma unroll
-      for (int n = 0; n < KW / 8; ++n)
+    for (int key0 = wk * KW; key0 < (wk + 1) * KW; key0 += KS) {
+      float s[KS / 8][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int kk = key0 + n * 8 + (lane & 3) * 2 + (e & 1);
-          const int place_w = cp.tile * kTK + kk - cp.u.ctx;
-          const uint32_t word = KW > 32 ? s_valid[ring * 4 + (kk >> 5)] : valid;
-          const bool see = (place_w < 0 ? hi[e >> 1] >= -cp.u.ctx : place_w >= lo[e >> 1] && place_w <= hi[e >> 1]) && (word >> (kk & 31) & 1u);
-          if (!see) s[n][e] = -INFINITY;
+      for (int n = 0; n < KS / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KD; ++k) {
+#pragma unroll
+        for (int n = 0; n < KS / 8; n += 2) {
+          uint32_t b[4];  // tokens n*8 .. +7 at d k*16 and +8, then tokens +8 .. +15
+          const int r = key0 + n * 8 + (lane & 7) + ((lane >> 4) << 3), c = k * 2 + ((lane >> 3) & 1);
+          ldsm4(b, kb + swz<D>(r, c));
+          mma_bf16(s[n], q[k], b[0], b[1]);
+          mma_bf16(s[n + 1], q[k], b[2], b[3]);
         }
-    }
-    float m_new[2] = {m_run[0], m_run[1]};
-#pragma unroll
-    for (int n = 0; n < KW / 8; ++n) {
-      m_new[0] = fmaxf(m_new[0], fmaxf(s[n][0], s[n][1]));
-      m_new[1] = fmaxf(m_new[1], fmaxf(s[n][2], s[n][3]));
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      m_new[e] = fmaxf(m_new[e], __shfl_xor_sync(kFull, m_new[e], 1));
-      m_new[e] = fmaxf(m_new[e], __shfl_xor_sync(kFull, m_new[e], 2));
-    }
-    float f[2], off[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      off[e] = m_new[e] == -INFINITY ? 0.f : __fmul_rn(m_new[e], P.scale_log2);
-      f[e] = factor(m_run[e], m_new[e], P.scale_log2);
-    }
-    if (__any_sync(kFull, m_new[0] != m_run[0] || m_new[1] != m_run[1])) {
-#pragma unroll
-      for (int n = 0; n < ND; ++n) {
-        o[n][0] *= f[0];
-        o[n][1] *= f[0];
-        o[n][2] *= f[1];
-        o[n][3] *= f[1];
       }
-      l_run[0] *= f[0];
-      l_run[1] *= f[1];
-      m_run[0] = m_new[0];
-      m_run[1] = m_new[1];
-    }
-    float sum[2] = {0.f, 0.f};
-    uint32_t pa[KW / 16][4];
+      // Hidden tokens: behind the history all but the row's part of the window, and those without a page.
+      if (masked) {
+        const uint32_t word = s_valid[ring * 4 + (key0 >> 5)];
 #pragma unroll
-    for (int n = 0; n < KW / 8; ++n) {
-      float p[4];
+        for (int n = 0; n < KS / 8; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p[e] = s[n][e] == -INFINITY ? 0.f : ex2(fmaf(s[n][e], P.scale_log2, -off[e >> 1]));
-      sum[0] += p[0] + p[1];
-      sum[1] += p[2] + p[3];
-      pa[n / 2][(n & 1) * 2] = pack_bf16(p[0], p[1]);
-      pa[n / 2][(n & 1) * 2 + 1] = pack_bf16(p[2], p[3]);
-    }
-    l_run[0] += sum[0];
-    l_run[1] += sum[1];
+          for (int e = 0; e < 4; ++e) {
+            const int kk = key0 + n * 8 + (lane & 3) * 2 + (e & 1);
+            const int at = cp.tile * kTK + kk - cp.u.ctx;
+            const bool see = (at < 0 ? hi[e >> 1] >= -cp.u.ctx : at >= lo[e >> 1] && at <= hi[e >> 1]) && (word >> (kk & 31) & 1u);
+            if (!see) s[n][e] = -INFINITY;
+          }
+      }
+      float m_new[2] = {m_run[0], m_run[1]};
 #pragma unroll
-    for (int k = 0; k < KW / 16; ++k) {
+      for (int n = 0; n < KS / 8; ++n) {
+        m_new[0] = fmaxf(m_new[0], fmaxf(s[n][0], s[n][1]));
+        m_new[1] = fmaxf(m_new[1], fmaxf(s[n][2], s[n][3]));
+      }
 #pragma unroll
-      for (int n = 0; n < ND; n += 2) {
-        uint32_t b[4];  // tokens k*16 .. +7 and +8 .. +15 at d n*8, then at d n*8 + 8
-        const int r = key0 + k * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), c = n + (lane >> 4);
-        ldsm4t(b, vb + swz<D>(r, c));
-        mma_bf16(o[n], pa[k], b[0], b[1]);
-        mma_bf16(o[n + 1], pa[k], b[2], b[3]);
+      for (int e = 0; e < 2; ++e) {
+        m_new[e] = fmaxf(m_new[e], __shfl_xor_sync(kFull, m_new[e], 1));
+        m_new[e] = fmaxf(m_new[e], __shfl_xor_sync(kFull, m_new[e], 2));
+      }
+      if (__any_sync(kFull, m_new[0] != m_run[0] || m_new[1] != m_run[1])) {
+        const float f0 = factor(m_run[0], m_new[0], P.scale_log2), f1 = factor(m_run[1], m_new[1], P.scale_log2);
+#pragma unroll
+        for (int n = 0; n < ND; ++n) {
+          o[n][0] *= f0;
+          o[n][1] *= f0;
+          o[n][2] *= f1;
+          o[n][3] *= f1;
+        }
+        l_run[0] *= f0;
+        l_run[1] *= f1;
+        m_run[0] = m_new[0];
+        m_run[1] = m_new[1];
+      }
+      // A row that has seen nothing yet keeps -inf scores: with an offset of 0 their weights are 0.
+      const float off0 = m_run[0] == -INFINITY ? 0.f : __fmul_rn(m_run[0], P.scale_log2);
+      const float off1 = m_run[1] == -INFINITY ? 0.f : __fmul_rn(m_run[1], P.scale_log2);
+      uint32_t pa[KS / 16][4];
+#pragma unroll
+      for (int n = 0; n < KS / 8; ++n) {
+        const float p0 = ex2(fmaf(s[n][0], P.scale_log2, -off0)), p1 = ex2(fmaf(s[n][1], P.scale_log2, -off0));
+        const float p2 = ex2(fmaf(s[n][2], P.scale_log2, -off1)), p3 = ex2(fmaf(s[n][3], P.scale_log2, -off1));
+        l_run[0] += p0 + p1;
+        l_run[1] += p2 + p3;
+        pa[n / 2][(n & 1) * 2] = pack_bf16(p0, p1);
+        pa[n / 2][(n & 1) * 2 + 1] = pack_bf16(p2, p3);
+      }
+#pragma unroll
+      for (int k = 0; k < KS / 16; ++k) {
+#pragma unroll
+        for (int n = 0; n < ND; n += 2) {
+          uint32_t b[4];  // tokens k*16 .. +7 and +8 .. +15 at d n*8, then at d n*8 + 8
+          const int r = key0 + k * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), c = n + (lane >> 4);
+          ldsm4t(b, vb + swz<D>(r, c));
+          mma_bf16(o[n], pa[k], b[0], b[1]);
+          mma_bf16(o[n + 1], pa[k], b[2], b[3]);
+        }
       }
     }
 
@@ -649,17 +654,18 @@ __global__ void __launch_bounds__(128) join_kernel(Params P, Plan L, int grid) {
   }
 }
 
-constexpr int kGrid = 152 * 2;  // CTAs of the pipeline: two an SM
+constexpr int kGrid = 152 * 3;  // CTAs of the pipeline, at most
 
 template <int D, int WM>
 cudaError_t launch_mma(const Params& P, Plan L, cudaStream_t st) {
   using Sh = Shape<D, WM>;
   cudaError_t e = cudaFuncSetAttribute(window_mma_kernel<D, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::smem);
   if (e != cudaSuccess) return e;
-  window_mma_kernel<D, WM><<<kGrid, kTW, Sh::smem, st>>>(P, L);
+  constexpr int grid = 152 * Sh::kCtas;
+  window_mma_kernel<D, WM><<<grid, Sh::kT, Sh::smem, st>>>(P, L);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  join_kernel<1, D, Sh::MT><<<dim3(kGrid, Sh::MT / 16), 128, 0, st>>>(P, L, kGrid);
+  join_kernel<1, D, Sh::MT><<<dim3(grid, Sh::MT / 16), 128, 0, st>>>(P, L, grid);
   return cudaGetLastError();
 }
 
@@ -670,8 +676,8 @@ extern "C" {
 
 size_t sv_window_attention_workspace_size(const sv_kv_cache* cache, int32_t n_q_heads, int32_t R) {
   if (!cache || n_q_heads < 1 || R < 0) return 0;
-  // The cuts, then two partial results of at most 64 rows a CTA.
-  return (size_t)sv::att::kGrid * 16 + (size_t)sv::att::kGrid * 2 * 64 * ((size_t)128 + 2) * 4;
+  // The cuts, then two partial results of at most 128 rows a CTA.
+  return (size_t)sv::att::kGrid * 16 + (size_t)sv::att::kGrid * 2 * 128 * ((size_t)128 + 2) * 4;
 }
 
 sv_status sv_window_attention(const void* q, int64_t q_stride, int32_t n_q_heads, int32_t R, const sv_kv_cache* cache,
@@ -715,6 +721,11 @@ sv_status sv_window_attention(const void* q, int64_t q_stride, int32_t n_q_heads
     while ((1ll << s) < P.C.page_size) ++s;
     L.div_shift = 31 + s;
     L.div_mul = (uint32_t)(((1ull << (31 + s)) + P.C.page_size - 1) / P.C.page_size);
+    P.q_mask = 0xffffffffu;
+    if (P.scale_log2 == 0.f) {
+      P.scale_log2 = 1.f;
+      P.q_mask = 0u;
+    }
     if (P.scale_log2 < 0.f) {
       P.scale_log2 = -P.scale_log2;
       P.q_sign = 0x80008000u;
@@ -723,9 +734,11 @@ sv_status sv_window_attention(const void* q, int64_t q_stride, int32_t n_q_heads
     const long long rows = ((long long)R + P.S.n - 1) / P.S.n * P.group;
     cudaError_t e;
     if (D == 128)
-      e = rows <= 16 ? att::launch_mma<128, 1>(P, L, st) : rows <= 32 ? att::launch_mma<128, 2>(P, L, st) : att::launch_mma<128, 4>(P, L, st);
+      e = rows <= 16 ? att::launch_mma<128, 1>(P, L, st) : rows <= 32 ? att::launch_mma<128, 2>(P, L, st)
+          : rows <= 64 ? att::launch_mma<128, 4>(P, L, st) : att::launch_mma<128, 8>(P, L, st);
     else
-      e = rows <= 16 ? att::launch_mma<64, 1>(P, L, st) : rows <= 32 ? att::launch_mma<64, 2>(P, L, st) : att::launch_mma<64, 4>(P, L, st);
+      e = rows <= 16 ? att::launch_mma<64, 1>(P, L, st) : rows <= 32 ? att::launch_mma<64, 2>(P, L, st)
+          : rows <= 64 ? att::launch_mma<64, 4>(P, L, st) : att::launch_mma<64, 8>(P, L, st);
     return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
   }
   const int gy = P.S.n > 32768 ? 32768 : P.S.n;
