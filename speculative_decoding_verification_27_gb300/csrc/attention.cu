@@ -16,8 +16,6 @@
 namespace sv {
 namespace att {
 
-constexpr int kT = 256;
-
 struct Params {
   CacheView C;
   SeqView S;
@@ -32,82 +30,6 @@ struct Params {
   int group;         // query heads to a key-value head
   uint32_t* status;
 };
-
-template <int DT, int D>
-__global__ void __launch_bounds__(kT) window_kernel(Params P) {
-  constexpr int EPL = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int heads = P.C.n_heads * P.group;
-  for (int b = blockIdx.y; b < P.S.n; b += gridDim.y) {
-    const Window w = find_window(P.W, b);
-    const long long ctx = P.S.ctx[b];
-    if (w.rows < 0 || !length_ok(P.C, P.S, ctx) || !length_ok(P.C, P.S, ctx + w.rows)) {
-      if (blockIdx.x == 0 && threadIdx.x == 0)
-        set_status(P.status, w.rows < 0 ? SV_DATA_BAD_OFFSETS
-                                        : length_ok(P.C, P.S, ctx) ? SV_DATA_BAD_PAGE : SV_DATA_BAD_SEQ);
-      continue;
-    }
-    const int32_t* row = P.S.table + (long long)b * P.S.stride;
-    const long long n = (long long)w.rows * heads;
-    for (long long u = blockIdx.x * (kT / 32) + (threadIdx.x >> 5); u < n; u += gridDim.x * (kT / 32)) {
-      const int r = (int)(u / heads), h = (int)(u % heads);
-      int begin = r;  // the candidate's first row
-      if (P.W.cu) {
-        int lo = w.c0, hi = w.c1;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if ((long long)P.W.cu[mid] + mid - w.r0 <= r)
-            lo = mid;
-          else
-            hi = mid;
-        }
-        const long long at = (long long)P.W.cu[lo] + lo - w.r0;
-        begin = at < 0 || at > r ? r : (int)at;
-      }
-      const char* qp = P.q + (w.r0 + r) * P.q_row_b + (long long)h * P.C.head_bytes;
-      float q[EPL], o[EPL];
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) {
-        q[e] = Elem<DT>::scalar(qp, e * 32 + lane) * P.scale_log2;
-        o[e] = 0.f;
-      }
-      float m = -INFINITY, l = 0.f;
-      const long long head_at = (long long)(h / P.group) * P.C.head_b;
-      for (long long t = 0; t <= ctx + r; ++t) {
-        if (t >= ctx && t < ctx + begin) continue;
-        const int page = row[t / P.C.page_size];
-        if (page < 0 || page >= P.C.n_pages) {
-          if (lane == 0) set_status(P.status, SV_DATA_BAD_PAGE);
-          continue;
-        }
-        const long long at = page * P.C.page_b + (t % P.C.page_size) * P.C.token_b + head_at;
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) s = fmaf(q[e], Elem<DT>::scalar(P.C.k + at, e * 32 + lane), s);
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(kFull, s, x);
-        const float m2 = fmaxf(m, s), f = ex2(m - m2), p = ex2(s - m2);
-        m = m2;
-        l = l * f + p;
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) o[e] = fmaf(p, Elem<DT>::scalar(P.C.v + at, e * 32 + lane), o[e] * f);
-      }
-      char* op = P.out + (w.r0 + r) * P.out_row_b + (long long)h * P.C.head_bytes;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) {
-        const float x = o[e] * inv;
-        if (DT == 1)
-          reinterpret_cast<__nv_bfloat16*>(op)[e * 32 + lane] = __float2bfloat16_rn(x);
-        else
-          reinterpret_cast<float*>(op)[e * 32 + lane] = x;
-      }
-      if (P.lse && lane == 0)
-        P.lse[(long long)(w.r0 + r) * heads + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-    }
-  }
-}
-
 
 // ---------------------------------------------------------------------------
 // bf16: tensor cores over a paged pipeline
@@ -157,6 +79,109 @@ __device__ __forceinline__ void load_request(const Params& P, int b, Unit& u, bo
   u.keys = u.ctx + u.w.rows;
   u.tiles = (u.keys + kTK - 1) / kTK;
   u.n_mt = (int)(((long long)u.w.rows * P.group + MT - 1) / MT);
+}
+
+struct Share {
+  long long t0, t1, total;  // this CTA's tiles of the list
+  int grid;                 // CTAs that have a share
+};
+struct Cursor {
+  Unit u;
+  int tile;
+};
+
+// This CTA's share, and a cursor on its first tile; false for a CTA without
+// one. Thread i sums the tiles of its run of requests; a scan over the threads
+// gives the list's length, and the thread whose run holds the share's first
+// tile walks it.
+template <int MT, int kThr>
+__device__ __forceinline__ bool take_share(const Params& P, const Plan& L, Share& sh, Cursor& c) {
+  __shared__ long long s_scan[kThr / 32];
+  __shared__ int s_start;
+  __shared__ long long s_first;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (P.S.n + kThr - 1) / kThr;
+  long long mine = 0;
+  for (int b = tid * per; b < min((tid + 1) * per, P.S.n); ++b) {
+    load_request<MT>(P, b, c.u, blockIdx.x == 0);
+    mine += (long long)c.u.tiles * c.u.n_mt * P.C.n_heads;
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  sh.total = 0;
+  for (int w = 0; w < kThr / 32; ++w) {
+    if (w < warp) incl += s_scan[w];
+    sh.total += s_scan[w];
+  }
+  sh.grid = (int)min((long long)gridDim.x, sh.total);  // shares of a tile at least
+  if (blockIdx.x >= sh.grid) {
+    if (tid == 0) L.cut[blockIdx.x * 4] = -1;
+    return false;
+  }
+  sh.t0 = sh.total * blockIdx.x / sh.grid;
+  sh.t1 = sh.total * (blockIdx.x + 1) / sh.grid;
+  if (sh.t0 >= incl - mine && sh.t0 < incl) {
+    long long at = incl - mine;
+    int b = tid * per;
+    for (;; ++b) {
+      load_request<MT>(P, b, c.u, false);
+      const long long n = (long long)c.u.tiles * c.u.n_mt * P.C.n_heads;
+      if (sh.t0 < at + n) break;
+      at += n;
+    }
+    s_start = b;
+    s_first = sh.t0 - at;  // first tile of the share within its request
+  }
+  __syncthreads();
+  load_request<MT>(P, s_start, c.u, false);
+  const long long unit = s_first / c.u.tiles;
+  c.tile = (int)(s_first - unit * c.u.tiles);
+  c.u.head = (int)(unit / c.u.n_mt);
+  c.u.mt = (int)(unit - (long long)c.u.head * c.u.n_mt);
+  return true;
+}
+
+// On to the next unit's first tile (the share holds one).
+template <int MT>
+__device__ __forceinline__ void next_unit(const Params& P, Cursor& c) {
+  c.tile = 0;
+  if (++c.u.mt < c.u.n_mt) return;
+  c.u.mt = 0;
+  if (++c.u.head < P.C.n_heads) return;
+  c.u.head = 0;
+  for (int b = c.u.b + 1; b < P.S.n; ++b) {
+    load_request<MT>(P, b, c.u, false);
+    if (c.u.tiles) return;
+  }
+}
+
+// By one thread on the share's last tile: the unit that the share cuts at its
+// end, if it began here, and the last CTA that has a part of it.
+__device__ __forceinline__ void tell_cut(const Plan& L, const Share& sh, const Cursor& c, bool cuts) {
+  const long long last = sh.t1 - 1 + (c.u.tiles - 1 - c.tile);  // the unit's last tile in the list
+  *reinterpret_cast<int4*>(L.cut + blockIdx.x * 4) =
+      make_int4(cuts ? c.u.b : -1, c.u.head, c.u.mt, (int)(((last + 1) * sh.grid - 1) / sh.total));  // the largest share that begins by then
+}
+
+// The first row of the candidate that window row w lies in.
+__device__ __forceinline__ int candidate_start(const Params& P, const Window& win, int w) {
+  if (!P.W.cand) return 0;
+  int a = win.c0, z = win.c1;
+  while (z - a > 1) {
+    const int mid = (a + z) >> 1;
+    if ((long long)P.W.cu[mid] + mid - win.r0 <= w)
+      a = mid;
+    else
+      z = mid;
+  }
+  const long long at = (long long)P.W.cu[a] + a - win.r0;
+  return at < 0 || at > w ? w : (int)at;
 }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
@@ -209,8 +234,8 @@ struct Shape {
   static constexpr int kT = 32 * WM * WK;       // threads
   static constexpr int KW = kTK / WK;           // tokens of a tile for one warp
   static constexpr int KS = KW < 32 ? KW : 32;  // tokens that go through the softmax at once
-  static constexpr int kCtas = D == 64 && WM == 4 ? 3 : D == 128 && WM == 8 ? 1 : 2;  // an SM
-  static constexpr int kStages = D == 128 ? (WM == 8 ? 5 : 3) : (WM == 4 ? 4 : 6);
+  static constexpr int kCtas = D == 64 ? (WM <= 2 ? 4 : WM == 4 ? 3 : 2) : (WM <= 4 ? 2 : 1);  // an SM
+  static constexpr int kStages = D == 64 ? (WM <= 2 ? 3 : WM == 4 ? 4 : 6) : (WM <= 4 ? 3 : 5);
   static constexpr int kTile = kTK * D * 2;     // bytes of K (or V) of a tile
   static constexpr size_t smem = (size_t)kStages * 2 * kTile + (kStages + 1) * (kTK * 8 + 16);
   // The warps that split the keys join in the stage that they have just used.
@@ -237,84 +262,14 @@ __global__ void __launch_bounds__(Shape<D, WM>::kT, Shape<D, WM>::kCtas) window_
   char* s_kv = smem;
   long long* s_off = reinterpret_cast<long long*>(smem + S * 2 * Sh::kTile);  // [S + 1][kTK]
   uint32_t* s_valid = reinterpret_cast<uint32_t*>(s_off + (S + 1) * kTK);                  // [S + 1][4]
-  __shared__ long long s_scan[kTW / 32];
-  __shared__ int s_start[2];
-  __shared__ long long s_first;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wm = warp % WM, wk = warp / WM;
 
-  // This CTA's share. Thread i sums the tiles of its run of requests; a scan over the threads, and the thread whose run holds
-  // the first tile of the share walks it.
-  const int per = (P.S.n + kTW - 1) / kTW;
-  long long mine = 0;
-  for (int b = tid * per; b < min((tid + 1) * per, P.S.n); ++b) {
-    Unit u;
-    load_request<MT>(P, b, u, blockIdx.x == 0);
-    mine += (long long)u.tiles * u.n_mt * P.C.n_heads;
-  }
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(kFull, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) s_scan[warp] = incl;
-  __syncthreads();
-  long long total = 0;
-  for (int w = 0; w < kTW / 32; ++w) {
-    if (w < warp) incl += s_scan[w];
-    total += s_scan[w];
-  }
-  const int grid = (int)min((long long)gridDim.x, total);  // shares of a tile at least
-  if (blockIdx.x >= grid) {
-    if (tid == 0) L.cut[blockIdx.x * 4] = -1;
-    return;
-  }
-  const long long t0 = total * blockIdx.x / grid, t1 = total * (blockIdx.x + 1) / grid;
-  if (t0 >= incl - mine && t0 < incl) {
-    long long at = incl - mine;
-    Unit u;
-    int b = tid * per;
-    for (;; ++b) {
-      load_request<MT>(P, b, u, false);
-      const long long n = (long long)u.tiles * u.n_mt * P.C.n_heads;
-      if (t0 < at + n) break;
-      at += n;
-    }
-    s_start[0] = b;
-    s_first = t0 - at;  // first tile of the share within its request
-  }
-  __syncthreads();
-
-  // Two cursors over the share: one loads, one computes.
-  struct Cursor {
-    Unit u;
-    int tile;
-  };
-  auto begin = [&](Cursor& c) {
-    load_request<MT>(P, s_start[0], c.u, false);
-    const long long first = s_first;
-    const long long unit = first / c.u.tiles;
-    c.tile = (int)(first - unit * c.u.tiles);
-    c.u.head = (int)(unit / c.u.n_mt);
-    c.u.mt = (int)(unit - (long long)c.u.head * c.u.n_mt);
-  };
-  auto next_unit = [&](Cursor& c) {  // false past the last request
-    c.tile = 0;
-    if (++c.u.mt < c.u.n_mt) return;
-    c.u.mt = 0;
-    if (++c.u.head < P.C.n_heads) return;
-    c.u.head = 0;
-    int b = c.u.b + 1;
-    for (; b < P.S.n; ++b) {
-      load_request<MT>(P, b, c.u, false);
-      if (c.u.tiles) return;
-    }
-  };
-  const int n_tiles = (int)(t1 - t0);
-  Cursor ld, cp;
-  begin(ld);
-  cp = ld;
+  Share sh;
+  Cursor ld;
+  if (!take_share<MT, kTW>(P, L, sh, ld)) return;
+  const int n_tiles = (int)(sh.t1 - sh.t0);
+  Cursor cp = ld;  // two cursors over the share: one loads, one computes
 
   // Page lookups run one tile ahead of the copies: threads 0 .. kTK - 1 hold a token each. The byte offset of a token in K and
   // V, or -1 where it has no page or lies behind the sequence.
@@ -360,7 +315,7 @@ __global__ void __launch_bounds__(Shape<D, WM>::kT, Shape<D, WM>::kCtas) window_
       if (i < n_tiles) {
         lookup(ld, pages[i], places[i]);
         heads[i] = ld.u.head;
-        if (i + 1 < n_tiles && ++ld.tile == ld.u.tiles) next_unit(ld);
+        if (i + 1 < n_tiles && ++ld.tile == ld.u.tiles) next_unit<MT>(P, ld);
       }
     }
 #pragma unroll
@@ -380,10 +335,9 @@ __global__ void __launch_bounds__(Shape<D, WM>::kT, Shape<D, WM>::kCtas) window_
   bool begun = false, from_start = false;
   const int row0 = wm * 16 + (lane >> 2);  // and row0 + 8
 
+  if (S < n_tiles) lookup(ld, page, place);  // tile S, stored in the first round
   for (int i = 0; i < n_tiles; ++i) {
-    const bool ahead = i + S < n_tiles;
-    if (ahead) lookup(ld, page, place);
-
+    if (i + 1 == n_tiles) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may take its place
     if (!begun) {  // a new unit: its rows
       begun = true;
       from_start = cp.tile == 0;
@@ -393,20 +347,8 @@ __global__ void __launch_bounds__(Shape<D, WM>::kT, Shape<D, WM>::kCtas) window_
         const int x = cp.u.mt * MT + row0 + e * 8;
         const bool ok = x < rows;
         const int w = ok ? x / P.group : 0, h = ok ? x - w * P.group : 0;
-        lo[e] = 0;
+        lo[e] = ok ? candidate_start(P, cp.u.w, w) : 0;
         hi[e] = ok ? w : -1 - cp.u.ctx;  // rows past the window see nothing
-        if (ok && P.W.cand) {  // the first row of the row's candidate
-          int a = cp.u.w.c0, z = cp.u.w.c1;
-          while (z - a > 1) {
-            const int mid = (a + z) >> 1;
-            if ((long long)P.W.cu[mid] + mid - cp.u.w.r0 <= w)
-              a = mid;
-            else
-              z = mid;
-          }
-          const long long at = (long long)P.W.cu[a] + a - cp.u.w.r0;
-          lo[e] = at < 0 || at > w ? w : (int)at;
-        }
         const uint32_t* src = reinterpret_cast<const uint32_t*>(P.q + (long long)(cp.u.w.r0 + w) * P.q_row_b +
                                                                 (long long)(cp.u.head * P.group + h) * (D * 2)) + (lane & 3);
 #pragma unroll
@@ -427,6 +369,13 @@ __global__ void __launch_bounds__(Shape<D, WM>::kT, Shape<D, WM>::kCtas) window_
     __syncthreads();  // tile i has landed, the ring's next lookup is there, stage (i - 1) is free
     if (i + S - 1 < n_tiles) copy_tile((i + S - 1) % (S + 1), (i + S - 1) % S);
     cp_commit();
+    if (i + S < n_tiles) {
+      store_lookup((i + S) % (S + 1), ld.u.head, page, place);  // for the next round's copy
+      if (i + S + 1 < n_tiles) {
+        if (++ld.tile == ld.u.tiles) next_unit<MT>(P, ld);
+        lookup(ld, page, place);  // has this round's arithmetic to arrive
+      }
+    }
 
     const uint32_t kb = smem_addr(s_kv) + (i % S) * 2 * Sh::kTile, vb = kb + Sh::kTile;
     const int ring = i % (S + 1);
@@ -513,11 +462,6 @@ __global__ void __launch_bounds__(Shape<D, WM>::kT, Shape<D, WM>::kCtas) window_
       }
     }
 
-    if (ahead) {
-      store_lookup((i + S) % (S + 1), ld.u.head, page, place);
-      if (i + S + 1 < n_tiles && ++ld.tile == ld.u.tiles) next_unit(ld);
-    }
-
     // The unit's end, or the share's: join the warps that split the keys, then write.
     const bool unit_end = cp.tile + 1 == cp.u.tiles;
     if (unit_end || i + 1 == n_tiles) {
@@ -565,13 +509,7 @@ __global__ void __launch_bounds__(Shape<D, WM>::kT, Shape<D, WM>::kCtas) window_
       }
       const bool split = !from_start || !unit_end;
       if (tid == 0 && i + 1 == n_tiles) {
-        // The unit that this share cuts at its end, if it began here: its last CTA ends the unit.
-        int* cut = L.cut + blockIdx.x * 4;
-        cut[0] = !unit_end && from_start ? cp.u.b : -1;
-        cut[1] = cp.u.head;
-        cut[2] = cp.u.mt;
-        const long long last = t1 - 1 + (cp.u.tiles - 1 - cp.tile);  // the unit's last tile in the list
-        cut[3] = (int)(((last + 1) * grid - 1) / total);  // the largest c with total * c / grid <= last
+        tell_cut(L, sh, cp, !unit_end && from_start);
       }
       if (wk == 0) {
         const int rows = cp.u.w.rows * P.group;
@@ -604,69 +542,349 @@ __global__ void __launch_bounds__(Shape<D, WM>::kT, Shape<D, WM>::kCtas) window_
         }
       }
     }
-    if (++cp.tile == cp.u.tiles && i + 1 < n_tiles) next_unit(cp);
+    if (++cp.tile == cp.u.tiles && i + 1 < n_tiles) next_unit<MT>(P, cp);
   }
   cp_wait<0>();
 }
 
-// Joins the parts of a unit that several CTAs share, in the order of the
-// CTAs. Block c takes the unit that CTA c's share cuts at its end, if it began
-// there; blockIdx.y splits its rows. A thread holds 4 elements of a row.
+// ---------------------------------------------------------------------------
+// fp32: the same shares, on the fp32 pipes
+// ---------------------------------------------------------------------------
+template <int D, int MT>
+struct Shape32 {
+  static constexpr int kT = 128;
+  static constexpr int kPitch = D * 4 + 16;        // bytes of a row in shared memory: rows of one column lie in different banks
+  static constexpr int kTile = kTK * kPitch;
+  static constexpr int kStages = D == 64 ? 3 : 2;
+  static constexpr int kCtas = D == 64 ? 2 : 1;    // an SM
+  static constexpr int SP = kTK + 4;               // row pitch of the scores, in floats
+  static constexpr size_t smem = (size_t)kStages * 2 * kTile + (size_t)MT * D * 4 + (size_t)MT * SP * 4 + MT * 16 + kStages * kTK * 8;
+};
+
+// A tile's scores: thread (token, half of the rows) walks d. Its softmax: a
+// warp takes every fourth row. Its product with V: thread (d, share of the
+// tokens) holds every row's sum.
+template <int D, int MT>
+__global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(Params P, Plan L) {
+  using Sh = Shape32<D, MT>;
+  constexpr int S = Sh::kStages, SP = Sh::SP, RH = MT / 2, KH = 128 / D, CPR = D / 4;
+  extern __shared__ __align__(1024) char smem[];
+  char* s_kv = smem;
+  float* s_q = reinterpret_cast<float*>(smem + S * 2 * Sh::kTile);  // [MT][D]
+  float* s_p = s_q + MT * D;                                        // [MT][SP]
+  float* s_m = s_p + MT * SP;                                       // [MT] maximum, sum, factor of the tile, free
+  float* s_l = s_m + MT;
+  float* s_f = s_l + MT;
+  long long* s_off = reinterpret_cast<long long*>(s_f + 2 * MT);    // [S][kTK]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Share sh;
+  Cursor ld;
+  if (!take_share<MT, 128>(P, L, sh, ld)) return;
+  const int n_tiles = (int)(sh.t1 - sh.t0);
+  Cursor cp = ld;
+  const int key = tid % kTK, half = tid / kTK;
+  const int d_own = tid % D, kh = tid / D;
+
+  // The offsets of the loading cursor's tile, and the tile itself.
+  auto load_tile = [&](int n) {
+    if (tid < kTK) {
+      const int t = ld.tile * kTK + tid;
+      long long off = -1;
+      if (t < ld.u.keys) {
+        const int slot = div_page(L, t), page = P.S.table[(long long)ld.u.b * P.S.stride + slot];
+        if (page >= 0 && page < P.C.n_pages)
+          off = page * P.C.page_b + (t - slot * P.C.page_size) * P.C.token_b + ld.u.head * P.C.head_b;
+        else
+          set_status(P.status, SV_DATA_BAD_PAGE);
+      }
+      s_off[n % S * kTK + tid] = off;
+    }
+    __syncthreads();
+    const uint32_t base = smem_addr(s_kv) + (n % S) * 2 * Sh::kTile;
+    for (int x = tid; x < kTK * CPR; x += 128) {
+      const int r = x / CPR, c = x % CPR;
+      const long long off = s_off[n % S * kTK + r];
+      const long long at = (off < 0 ? 0 : off) + c * 16;
+      cp16(base + r * Sh::kPitch + c * 16, P.C.k + at, off >= 0);
+      cp16(base + Sh::kTile + r * Sh::kPitch + c * 16, P.C.v + at, off >= 0);
+    }
+    cp_commit();
+    if (++ld.tile == ld.u.tiles && n + 1 < n_tiles) next_unit<MT>(P, ld);
+  };
+  for (int i = 0; i < S - 1; ++i) {
+    if (i < n_tiles)
+      load_tile(i);
+    else
+      cp_commit();
+  }
+
+  float o[MT];
+  int lo[RH], hi[RH];
+  bool begun = false, from_start = false;
+  for (int i = 0; i < n_tiles; ++i) {
+    if (i + 1 == n_tiles) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int rows = cp.u.w.rows * P.group;
+    if (!begun) {
+      begun = true;
+      from_start = cp.tile == 0;
+      __syncthreads();
+      for (int x = tid; x < MT * D; x += 128) {
+        const int r = cp.u.mt * MT + x / D;
+        float v = 0.f;
+        if (r < rows) {
+          const int w = r / P.group, h = cp.u.head * P.group + (r - w * P.group);
+          v = __ldg(reinterpret_cast<const float*>(P.q + (long long)(cp.u.w.r0 + w) * P.q_row_b + (long long)h * (D * 4)) + x % D);
+        }
+        s_q[x] = v;
+      }
+      if (tid < MT) {
+        s_m[tid] = -INFINITY;
+        s_l[tid] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < RH; ++e) {
+        const int r = cp.u.mt * MT + half * RH + e;
+        const int w = r < rows ? r / P.group : 0;
+        lo[e] = r < rows ? candidate_start(P, cp.u.w, w) : 0;
+        hi[e] = r < rows ? w : -1 - cp.u.ctx;
+      }
+#pragma unroll
+      for (int r = 0; r < MT; ++r) o[r] = 0.f;
+    }
+    cp_wait<S - 2>();
+    __syncthreads();  // the tile has landed; the stage before it is free
+    if (i + S - 1 < n_tiles)
+      load_tile(i + S - 1);
+    else
+      cp_commit();
+    const char* kt = s_kv + (i % S) * 2 * Sh::kTile;
+    const float* vt = reinterpret_cast<const float*>(kt + Sh::kTile);
+
+    // Scores.
+    {
+      float s[RH];
+#pragma unroll
+      for (int e = 0; e < RH; ++e) s[e] = 0.f;
+      const float4* kr = reinterpret_cast<const float4*>(kt + key * Sh::kPitch);
+      const float4* qr = reinterpret_cast<const float4*>(s_q + half * RH * D);
+#pragma unroll 4
+      for (int d = 0; d < D / 4; ++d) {
+        const float4 k4 = kr[d];
+#pragma unroll
+        for (int e = 0; e < RH; ++e) {
+          const float4 q4 = qr[e * (D / 4) + d];
+          s[e] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[e]))));
+        }
+      }
+      const int at = cp.tile * kTK + key - cp.u.ctx;
+      const bool page_ok = s_off[i % S * kTK + key] >= 0;
+#pragma unroll
+      for (int e = 0; e < RH; ++e) {
+        const bool see = page_ok && (at < 0 ? hi[e] >= -cp.u.ctx : at >= lo[e] && at <= hi[e]);
+        s_p[(half * RH + e) * SP + key] = see ? s[e] * P.scale_log2 : -INFINITY;
+      }
+    }
+    __syncthreads();
+    // Softmax of the rows, two tokens a lane.
+    for (int r = warp; r < MT; r += 4) {
+      const float a = s_p[r * SP + lane], b = s_p[r * SP + lane + 32];
+      const float m0 = s_m[r], m = fmaxf(m0, warp_max(fmaxf(a, b)));
+      const float off_m = m == -INFINITY ? 0.f : m;
+      const float pa = ex2(a - off_m), pb = ex2(b - off_m);
+      float sum = pa + pb;
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
+      s_p[r * SP + lane] = pa;
+      s_p[r * SP + lane + 32] = pb;
+      if (lane == 0) {
+        const float f = m0 == -INFINITY ? 0.f : ex2(m0 - m);
+        s_f[r] = f;
+        s_l[r] = s_l[r] * f + sum;
+        s_m[r] = m;
+      }
+    }
+    __syncthreads();
+    // The product with V.
+#pragma unroll
+    for (int r = 0; r < MT; ++r) o[r] *= s_f[r];
+#pragma unroll 2
+    for (int k = kh * (kTK / KH); k < (kh + 1) * (kTK / KH); k += 4) {
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = vt[(k + j) * (Sh::kPitch / 4) + d_own];
+#pragma unroll
+      for (int r = 0; r < MT; ++r) {
+        const float4 p = *reinterpret_cast<const float4*>(s_p + r * SP + k);
+        o[r] = fmaf(p.x, v[0], fmaf(p.y, v[1], fmaf(p.z, v[2], fmaf(p.w, v[3], o[r]))));
+      }
+    }
+
+    const bool unit_end = cp.tile + 1 == cp.u.tiles;
+    if (unit_end || i + 1 == n_tiles) {
+      begun = false;
+      if constexpr (KH > 1) {  // the halves of the tokens, joined in the place of the scores (MT * D floats fit the tile just used)
+        float* buf = reinterpret_cast<float*>(const_cast<char*>(kt));
+        __syncthreads();
+        if (kh == 1)
+#pragma unroll
+          for (int r = 0; r < MT; ++r) buf[r * D + d_own] = o[r];
+        __syncthreads();
+        if (kh == 0)
+#pragma unroll
+          for (int r = 0; r < MT; ++r) o[r] += buf[r * D + d_own];
+      }
+      const bool split = !from_start || !unit_end;
+      if (tid == 0 && i + 1 == n_tiles) tell_cut(L, sh, cp, !unit_end && from_start);
+      if (kh == 0) {
+        float* part = reinterpret_cast<float*>(L.part + (size_t)(blockIdx.x * 2 + (from_start ? 1 : 0)) * part_bytes<D, MT>());
+#pragma unroll
+        for (int r = 0; r < MT; ++r) {
+          const float m = s_m[r], l = s_l[r];
+          if (split) {
+            part[r * D + d_own] = o[r];
+            if (d_own == 0) {
+              part[MT * D + r] = m;
+              part[MT * D + MT + r] = l;
+            }
+            continue;
+          }
+          const int x = cp.u.mt * MT + r;
+          if (x >= rows) break;
+          const int w = x / P.group, h = cp.u.head * P.group + (x - w * P.group);
+          reinterpret_cast<float*>(P.out + (long long)(cp.u.w.r0 + w) * P.out_row_b + (long long)h * (D * 4))[d_own] = l > 0.f ? o[r] / l : 0.f;
+          if (P.lse && d_own == 0) P.lse[(long long)(cp.u.w.r0 + w) * (P.C.n_heads * P.group) + h] = lse_of(m, l, 1.f);
+        }
+      }
+    }
+    if (++cp.tile == cp.u.tiles && i + 1 < n_tiles) next_unit<MT>(P, cp);
+  }
+  cp_wait<0>();
+}
+
+// Joins the parts of a unit that several CTAs share. Block c takes the unit
+// that CTA c's share cuts at its end, if it began there; blockIdx.y takes
+// every gridDim.y-th row. Groups of D / 4 threads (a thread holds 4 elements)
+// take every kG-th part, four parts' loads in flight, and the groups' sums
+// are joined in order. The block is launched while the parts are still being
+// computed and waits for them.
+constexpr int kJoinT = 128;
 template <int DT, int D, int MT>
-__global__ void __launch_bounds__(128) join_kernel(Params P, Plan L, int grid) {
+__global__ void __launch_bounds__(kJoinT) join_kernel(Params P, Plan L, int grid) {
+  const float scale = DT == 1 ? P.scale_log2 : 1.f;  // of the maxima: the fp32 kernel's scores are scaled
+  constexpr int TPR = D / 4, kG = kJoinT / TPR;
+  __shared__ float4 s_o[kG][TPR];
+  __shared__ float2 s_ml[kG];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x;
-  const int* cut = L.cut + c * 4;
-  const int b = cut[0];
-  if (b < 0) return;
-  const int head = cut[1], mt = cut[2], last = min(cut[3], grid - 1);
-  const Window w = find_window(P.W, b);
-  constexpr int TPR = D / 4;
+  const int4 cut = *reinterpret_cast<const int4*>(L.cut + c * 4);
+  if (cut.x < 0) return;
+  const int head = cut.y, mt = cut.z, last = min(cut.w, grid - 1);
+  const Window w = find_window(P.W, cut.x);
   const int rows = w.rows * P.group;
-  for (int r = blockIdx.y * (128 / TPR) + threadIdx.x / TPR; r < MT; r += gridDim.y * (128 / TPR)) {
+  const int g = threadIdx.x / TPR, lane_d = threadIdx.x % TPR;
+  for (int r = blockIdx.y; r < MT; r += gridDim.y) {
     const int x = mt * MT + r;
     if (x >= rows) break;
-    const int d = threadIdx.x % TPR * 4;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = c; k <= last; ++k) {
-      const float* part = reinterpret_cast<const float*>(L.part + (size_t)(k * 2 + (k == c)) * part_bytes<D, MT>());
-      const float pm = part[MT * D + r], pl = part[MT * D + MT + r];
-      const float4 y = *reinterpret_cast<const float4*>(part + r * D + d);
-      const float top = fmaxf(m, pm);
-      const float fa = factor(m, top, P.scale_log2), fb = factor(pm, top, P.scale_log2);
+    for (int k0 = c + g; k0 <= last; k0 += kG * 4) {
+      float pm[4], pl[4];
+      float4 y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = k0 + j * kG;
+        pm[j] = -INFINITY;
+        pl[j] = 0.f;
+        y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k <= last) {
+          const float* part = reinterpret_cast<const float*>(L.part + (size_t)(k * 2 + (k == c)) * part_bytes<D, MT>());
+          pm[j] = part[MT * D + r];
+          pl[j] = part[MT * D + MT + r];
+          y[j] = *reinterpret_cast<const float4*>(part + r * D + lane_d * 4);
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = fmaxf(top, pm[j]);
+      const float fa = factor(m, top, scale);
+      l *= fa;
+      o = make_float4(o.x * fa, o.y * fa, o.z * fa, o.w * fa);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float f = factor(pm[j], top, scale);
+        l = fmaf(pl[j], f, l);
+        o = make_float4(fmaf(y[j].x, f, o.x), fmaf(y[j].y, f, o.y), fmaf(y[j].z, f, o.z), fmaf(y[j].w, f, o.w));
+      }
       m = top;
-      l = l * fa + pl * fb;
-      o.x = o.x * fa + y.x * fb;
-      o.y = o.y * fa + y.y * fb;
-      o.z = o.z * fa + y.z * fb;
-      o.w = o.w * fa + y.w * fb;
     }
-    const int ww = x / P.group, h = head * P.group + (x - ww * P.group);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    char* dst = P.out + (long long)(w.r0 + ww) * P.out_row_b + ((long long)h * D + d) * Elem<DT>::kBytes;
-    if constexpr (DT == 1)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    else
-      *reinterpret_cast<float4*>(dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    if (P.lse && d == 0)
-      P.lse[(long long)(w.r0 + ww) * (P.C.n_heads * P.group) + h] =
-          lse_of(m, l, P.scale_log2);
+    s_o[g][lane_d] = o;
+    if (lane_d == 0) s_ml[g] = make_float2(m, l);
+    __syncthreads();
+    if (g == 0) {
+      float top = m;
+#pragma unroll
+      for (int j = 1; j < kG; ++j) top = fmaxf(top, s_ml[j].x);
+      l = 0.f;
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < kG; ++j) {
+        const float2 ml = s_ml[j];
+        const float4 y = s_o[j][lane_d];
+        const float f = factor(ml.x, top, scale);
+        l = fmaf(ml.y, f, l);
+        o = make_float4(fmaf(y.x, f, o.x), fmaf(y.y, f, o.y), fmaf(y.z, f, o.z), fmaf(y.w, f, o.w));
+      }
+      const int ww = x / P.group, h = head * P.group + (x - ww * P.group);
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      char* dst = P.out + (long long)(w.r0 + ww) * P.out_row_b + ((long long)h * D + lane_d * 4) * Elem<DT>::kBytes;
+      if constexpr (DT == 1)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+      else
+        *reinterpret_cast<float4*>(dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      if (P.lse && lane_d == 0) P.lse[(long long)(w.r0 + ww) * (P.C.n_heads * P.group) + h] = lse_of(top, l, scale);
+    }
+    __syncthreads();
   }
 }
 
-constexpr int kGrid = 152 * 3;  // CTAs of the pipeline, at most
+constexpr int kGrid = 152 * 4;  // CTAs of the pipeline, at most
+
+// The join starts while the shares are computed: its launch is hidden, and it waits for their end.
+template <int DT, int D, int MT>
+cudaError_t launch_join(const Params& P, const Plan& L, int grid, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, MT < 16 ? MT : 16);
+  cfg.blockDim = dim3(kJoinT);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel<DT, D, MT>, P, L, grid);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
 
 template <int D, int WM>
-cudaError_t launch_mma(const Params& P, Plan L, cudaStream_t st) {
+cudaError_t launch_mma(const Params& P, const Plan& L, cudaStream_t st) {
   using Sh = Shape<D, WM>;
   cudaError_t e = cudaFuncSetAttribute(window_mma_kernel<D, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::smem);
   if (e != cudaSuccess) return e;
-  constexpr int grid = 152 * Sh::kCtas;
+  const int grid = 152 * Sh::kCtas;
   window_mma_kernel<D, WM><<<grid, Sh::kT, Sh::smem, st>>>(P, L);
   e = cudaGetLastError();
+  return e == cudaSuccess ? launch_join<1, D, Sh::MT>(P, L, grid, st) : e;
+}
+
+template <int D, int MT>
+cudaError_t launch_fma(const Params& P, const Plan& L, cudaStream_t st) {
+  using Sh = Shape32<D, MT>;
+  cudaError_t e = cudaFuncSetAttribute(window_fma_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::smem);
   if (e != cudaSuccess) return e;
-  join_kernel<1, D, Sh::MT><<<dim3(grid, Sh::MT / 16), 128, 0, st>>>(P, L, grid);
-  return cudaGetLastError();
+  const int grid = 152 * Sh::kCtas;
+  window_fma_kernel<D, MT><<<grid, Sh::kT, Sh::smem, st>>>(P, L);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? launch_join<0, D, MT>(P, L, grid, st) : e;
 }
 
 }  // namespace att
@@ -712,15 +930,18 @@ sv_status sv_window_attention(const void* q, int64_t q_stride, int32_t n_q_heads
   P.group = n_q_heads / P.C.n_heads;
   P.status = status;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  att::Plan L{};
+  L.cut = static_cast<int*>(workspace);
+  L.part = static_cast<char*>(workspace) + att::kGrid * 16;
+  // t / page_size for t < 2^31: with 2^s the next power of two, m = ceil(2^(31 + s) / page_size) errs by less than 2^s.
+  int s = 0;
+  while ((1ll << s) < P.C.page_size) ++s;
+  L.div_shift = 31 + s;
+  L.div_mul = (uint32_t)(((1ull << (31 + s)) + P.C.page_size - 1) / P.C.page_size);
+  // Row tiles as high as the windows' mean number of stacked rows.
+  const long long rows = ((long long)R + P.S.n - 1) / P.S.n * P.group;
+  cudaError_t e;
   if (es == 2) {
-    att::Plan L{};
-    L.cut = static_cast<int*>(workspace);
-    L.part = static_cast<char*>(workspace) + att::kGrid * 16;
-    // t / page_size for t < 2^31: with 2^s the next power of two, m = ceil(2^(31 + s) / page_size) errs by less than 2^s.
-    int s = 0;
-    while ((1ll << s) < P.C.page_size) ++s;
-    L.div_shift = 31 + s;
-    L.div_mul = (uint32_t)(((1ull << (31 + s)) + P.C.page_size - 1) / P.C.page_size);
     P.q_mask = 0xffffffffu;
     if (P.scale_log2 == 0.f) {
       P.scale_log2 = 1.f;
@@ -730,26 +951,22 @@ sv_status sv_window_attention(const void* q, int64_t q_stride, int32_t n_q_heads
       P.scale_log2 = -P.scale_log2;
       P.q_sign = 0x80008000u;
     }
-    // Row tiles as high as the windows' mean number of stacked rows.
-    const long long rows = ((long long)R + P.S.n - 1) / P.S.n * P.group;
-    cudaError_t e;
     if (D == 128)
-      e = rows <= 16 ? att::launch_mma<128, 1>(P, L, st) : rows <= 32 ? att::launch_mma<128, 2>(P, L, st)
-          : rows <= 64 ? att::launch_mma<128, 4>(P, L, st) : att::launch_mma<128, 8>(P, L, st);
+      e = rows <= 16   ? att::launch_mma<128, 1>(P, L, st)
+          : rows <= 32 ? att::launch_mma<128, 2>(P, L, st)
+          : rows <= 64 ? att::launch_mma<128, 4>(P, L, st)
+                       : att::launch_mma<128, 8>(P, L, st);
     else
-      e = rows <= 16 ? att::launch_mma<64, 1>(P, L, st) : rows <= 32 ? att::launch_mma<64, 2>(P, L, st)
-          : rows <= 64 ? att::launch_mma<64, 4>(P, L, st) : att::launch_mma<64, 8>(P, L, st);
-    return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+      e = rows <= 16   ? att::launch_mma<64, 1>(P, L, st)
+          : rows <= 32 ? att::launch_mma<64, 2>(P, L, st)
+          : rows <= 64 ? att::launch_mma<64, 4>(P, L, st)
+                       : att::launch_mma<64, 8>(P, L, st);
+  } else if (D == 128) {
+    e = rows <= 4 ? att::launch_fma<128, 4>(P, L, st) : att::launch_fma<128, 16>(P, L, st);
+  } else {
+    e = rows <= 4 ? att::launch_fma<64, 4>(P, L, st) : att::launch_fma<64, 16>(P, L, st);
   }
-  const int gy = P.S.n > 32768 ? 32768 : P.S.n;
-  const long long per = ((long long)R * n_q_heads + gy - 1) / gy;
-  const long long want = (per + att::kT / 32 - 1) / (att::kT / 32), most = 152 * 64 / gy + 1;
-  const dim3 grid((unsigned)(want < most ? want : most), gy);
-  if (D == 128)
-    att::window_kernel<0, 128><<<grid, att::kT, 0, st>>>(P);
-  else
-    att::window_kernel<0, 64><<<grid, att::kT, 0, st>>>(P);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -157,7 +157,7 @@ BF, F32 = torch.bfloat16, torch.float32
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("Hq,Hkv,D", [(1, 1, 64), (8, 2, 128), (6, 2, 64), (16, 1, 128), (10, 2, 64), (64, 1, 64), (4, 4, 128), (32, 1, 128)])
+@pytest.mark.parametrize("Hq,Hkv,D", [(1, 1, 64), (8, 2, 128), (6, 2, 64), (16, 1, 128), (10, 2, 64), (64, 1, 64), (4, 4, 128), (32, 1, 128), (2, 2, 64)])
 @pytest.mark.parametrize("page", [1, 7, 16, 64])
 def test_windows(cuda_lib, dtype, Hq, Hkv, D, page):
     """Ragged windows over lengths around the tiles' and pages' edges, an empty history and an empty window among them."""
