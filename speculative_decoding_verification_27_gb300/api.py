@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -500,23 +501,26 @@ class TokenLogprobs(NamedTuple):
     top_logprobs: Optional[torch.Tensor]  # [R, n_top] float32
 
 
-def _place(t: torch.Tensor, stream):
-    """(device guard, stream pointer) of a call on t's device: the guard is
-    None when that device is the current one."""
-    idx = t.device.index
-    s = torch.cuda.current_stream(idx) if stream is None else stream
-    return (None if idx == torch.cuda.current_device() else torch.cuda.device(idx)), ctypes.c_void_p(s.cuda_stream)
+def _raw_stream(device: int) -> int:
+    """The current stream of a device as an address."""
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)  # the same without a Stream object
 
 
 def _launch(name: str, t: torch.Tensor, stream, *args):
     """Calls the library on t's device and stream (the current one if None)."""
-    guard, s = _place(t, stream)
-    if guard is None:
-        st = getattr(load(), name)(*args, s)
+    fn = getattr(_lib or load(), name)
+    device = t.get_device()
+    s = _raw_stream(device) if stream is None else stream.cuda_stream
+    if device == torch.cuda.current_device():
+        st = fn(*args, s)
     else:
-        with guard:
-            st = getattr(load(), name)(*args, s)
-    _check(name, st)
+        with torch.cuda.device(device):
+            st = fn(*args, s)
+    if st:
+        raise SpecVerifyError(name, st)
 
 
 def _new(make, shape, dtype, like: torch.Tensor, stream):
@@ -527,14 +531,15 @@ def _new(make, shape, dtype, like: torch.Tensor, stream):
         return make(shape, dtype=dtype, device=like.device)
 
 
-def _vec(t: Optional[torch.Tensor], name: str, dtype, *shape):
-    """Pointer of a contiguous tensor of that type and shape (None in the
-    shape: any length); None stays None."""
+def _vec(t: Optional[torch.Tensor], name: str, dtype, shape: tuple):
+    """Address of a contiguous CUDA tensor of that type and shape; None stays None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {list(shape)}")
-    return _ptr(t)
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on a CUDA device")
+    return t.data_ptr()
 
 
 def sv_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *, cu_draft=None, out_len=None,
@@ -566,11 +571,13 @@ def sv_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = Non
         out_top_ids = _new(make, (R, n_top), i32, logits, stream)
     if n_top > 0 and out_top_logprobs is None:
         out_top_logprobs = _new(make, (R, n_top), f32, logits, stream)
-    _launch("sv_token_logprobs", logits, stream, ctypes.c_void_p(logits.data_ptr()), _dtype(logits), V, ld, R,
-            _vec(tokens, "tokens", i32, R), B, _vec(cu_draft, "cu_draft", i32, B + 1), _vec(out_len, "out_len", i32, B),
-            float(temperature), n_top, _vec(out_logprob, "out_logprob", f32, R), _vec(out_rank, "out_rank", i32, R),
-            _vec(out_entropy, "out_entropy", f32, R), _vec(out_top_ids, "out_top_ids", i32, R, n_top),
-            _vec(out_top_logprobs, "out_top_logprobs", f32, R, n_top), _vec(status, "status", i32, 1))
+    rows, tops = (R,), (R, n_top)
+    _launch("sv_token_logprobs", logits, stream, logits.data_ptr(), _dtype(logits), V, ld, R,
+            _vec(tokens, "tokens", i32, rows), B, _vec(cu_draft, "cu_draft", i32, (B + 1,)),
+            _vec(out_len, "out_len", i32, (B,)), temperature, n_top, _vec(out_logprob, "out_logprob", f32, rows),
+            _vec(out_rank, "out_rank", i32, rows), _vec(out_entropy, "out_entropy", f32, rows),
+            _vec(out_top_ids, "out_top_ids", i32, tops), _vec(out_top_logprobs, "out_top_logprobs", f32, tops),
+            _vec(status, "status", i32, (1,)))
     return TokenLogprobs(out_logprob, out_rank, out_entropy, out_top_ids, out_top_logprobs)
 
 
@@ -591,6 +598,9 @@ class _Cache(ctypes.Structure):
 class _Sequences(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("table_pages", ctypes.c_int32),
                 ("n", ctypes.c_int32), ("ctx_len", ctypes.c_void_p)]
+
+
+_pack_sequences = struct.Struct("@PqiiP").pack  # _Sequences as bytes: the library reads it during the call only
 
 
 class KVCache:
@@ -618,17 +628,17 @@ class KVCache:
         # A dimension of one element takes no step; its stride may be anything.
         steps = [s if m > 1 else 0 for s, m in zip(k.stride(), k.shape)]
         self._c = _Cache(k.data_ptr(), v.data_ptr(), _dtype(k), *k.shape, *steps[:4],
-                         _vec(page_ref, "page_ref", torch.int32, n), _vec(free_bits, "free_bits", torch.int32, words))
+                         _vec(page_ref, "page_ref", torch.int32, (n,)), _vec(free_bits, "free_bits", torch.int32, (words,)))
         self._ref = ctypes.byref(self._c)
 
 
-def _seqs(page_table: torch.Tensor, ctx_len: torch.Tensor):
-    if page_table.dim() != 2 or page_table.dtype != torch.int32 or not page_table.is_cuda or \
-            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("page_table must be an int32 CUDA matrix with contiguous rows")
+def _seqs(page_table: torch.Tensor, ctx_len: torch.Tensor) -> bytes:
     n, width = page_table.shape
-    return ctypes.byref(_Sequences(page_table.data_ptr(), page_table.stride(0) if n > 1 else max(width, 1), width, n,
-                                   _vec(ctx_len, "ctx_len", torch.int32, n)))
+    stride, step = page_table.stride()
+    if page_table.dtype != torch.int32 or not page_table.is_cuda or (step != 1 and width > 1):
+        raise ValueError("page_table must be an int32 CUDA matrix with contiguous rows")
+    return _pack_sequences(page_table.data_ptr(), stride if n > 1 else max(width, 1), width, n,
+                           _vec(ctx_len, "ctx_len", torch.int32, (n,)))
 
 
 def _windows(n: int, cu_draft, cu_cand):
@@ -640,7 +650,7 @@ def _windows(n: int, cu_draft, cu_cand):
     n_cand = cu_draft.shape[0] - 1
     if cu_cand is None and n_cand != n:
         raise ValueError("cu_draft has an offset per sequence and one more")
-    return n_cand, _vec(cu_draft, "cu_draft", torch.int32, n_cand + 1), _vec(cu_cand, "cu_cand", torch.int32, n + 1)
+    return n_cand, _vec(cu_draft, "cu_draft", torch.int32, (n_cand + 1,)), _vec(cu_cand, "cu_cand", torch.int32, (n + 1,))
 
 
 def _scratch(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
@@ -651,8 +661,8 @@ def sv_cache_fork(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Tenso
                   status=None, stream=None) -> None:
     """Sequences dst[i] (empty) become copies of src[i] that share its pages."""
     N = src.shape[0]
-    _launch("sv_cache_fork", cache.k, stream, cache._ref, _seqs(page_table, ctx_len), N, _vec(src, "src", torch.int32, N),
-            _vec(dst, "dst", torch.int32, N), _vec(status, "status", torch.int32, 1))
+    _launch("sv_cache_fork", cache.k, stream, cache._ref, _seqs(page_table, ctx_len), N, _vec(src, "src", torch.int32, (N,)),
+            _vec(dst, "dst", torch.int32, (N,)), _vec(status, "status", torch.int32, (1,)))
 
 
 def sv_cache_free(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Tensor, which: torch.Tensor, *, status=None,
@@ -660,7 +670,7 @@ def sv_cache_free(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Tenso
     """Ends the sequences `which`: their pages are released."""
     N = which.shape[0]
     _launch("sv_cache_free", cache.k, stream, cache._ref, _seqs(page_table, ctx_len), N,
-            _vec(which, "which", torch.int32, N), _vec(status, "status", torch.int32, 1))
+            _vec(which, "which", torch.int32, (N,)), _vec(status, "status", torch.int32, (1,)))
 
 
 def sv_cache_reserve(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Tensor, cu_draft=None, cu_cand=None, *,
@@ -671,10 +681,10 @@ def sv_cache_reserve(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Te
     if granted is None:
         granted = _new(torch.empty, n, torch.int32, page_table, stream)
     if workspace is None:
-        workspace = _scratch(load().sv_cache_reserve_workspace_size(n), page_table, stream)
+        workspace = _scratch((_lib or load()).sv_cache_reserve_workspace_size(n), page_table, stream)
     _launch("sv_cache_reserve", cache.k, stream, cache._ref, _seqs(page_table, ctx_len), *_windows(n, cu_draft, cu_cand),
-            _vec(granted, "granted", torch.int32, n), _ptr(workspace), workspace.numel(),
-            _vec(status, "status", torch.int32, 1))
+            _vec(granted, "granted", torch.int32, (n,)), _ptr(workspace), workspace.numel(),
+            _vec(status, "status", torch.int32, (1,)))
     return granted
 
 
@@ -686,15 +696,15 @@ def sv_cache_append(cache: KVCache, layer: int, k_new: torch.Tensor, v_new: torc
     if k_new.dim() == 3:
         k_new, v_new = k_new[None], v_new[None]
     L, R = k_new.shape[:2]
-    heads = (cache.n_kv_heads, cache.head_dim)
-    for x in (k_new, v_new):
-        if x.dim() != 4 or tuple(x.shape) != (L, R, *heads) or x.dtype != cache.k.dtype or not x.is_cuda or \
-                x.stride() != k_new.stride() or (R and L and not x[0, 0].is_contiguous()):
-            raise ValueError("k_new and v_new must be [n_layers, R, kv_heads, head_dim] of the cache's dtype, alike in "
-                             "strides, with contiguous heads")
+    want = (L, R, cache.n_kv_heads, cache.head_dim)
+    strides = k_new.stride()
+    if k_new.shape != want or v_new.shape != want or v_new.stride() != strides or strides[2:] != (cache.head_dim, 1) or \
+            k_new.dtype != cache.k.dtype or v_new.dtype != cache.k.dtype or not k_new.is_cuda or not v_new.is_cuda:
+        raise ValueError("k_new and v_new must be CUDA tensors [n_layers, R, kv_heads, head_dim] of the cache's dtype, alike "
+                         "in strides, with contiguous heads")
     _launch("sv_cache_append", cache.k, stream, cache._ref, int(layer), L, k_new.data_ptr(), v_new.data_ptr(),
-            k_new.stride(0) if L > 1 else 0, k_new.stride(1) if R > 1 else 0, R, _seqs(page_table, ctx_len),
-            *_windows(page_table.shape[0], cu_draft, cu_cand), _vec(status, "status", torch.int32, 1))
+            strides[0] if L > 1 else 0, strides[1] if R > 1 else 0, R, _seqs(page_table, ctx_len),
+            *_windows(page_table.shape[0], cu_draft, cu_cand), _vec(status, "status", torch.int32, (1,)))
 
 
 def sv_cache_commit(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Tensor, cu_draft, out_len: torch.Tensor,
@@ -707,8 +717,8 @@ def sv_cache_commit(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Ten
         raise ValueError("cu_cand and best come together")
     win = _windows(n, cu_draft, cu_cand)
     _launch("sv_cache_commit", cache.k, stream, cache._ref, _seqs(page_table, ctx_len), *win,
-            _vec(best, "best", torch.int32, n), _vec(out_len, "out_len", torch.int32, win[0]),
-            _vec(status, "status", torch.int32, 1))
+            _vec(best, "best", torch.int32, (n,)), _vec(out_len, "out_len", torch.int32, (win[0],)),
+            _vec(status, "status", torch.int32, (1,)))
 
 
 def sv_window_attention(q: torch.Tensor, cache: KVCache, layer: int, page_table: torch.Tensor, ctx_len: torch.Tensor,
@@ -723,16 +733,15 @@ def sv_window_attention(q: torch.Tensor, cache: KVCache, layer: int, page_table:
     R, heads, D = q.shape
     if out is None:
         out = _new(torch.zeros, (R, heads, D), q.dtype, q, stream)
-    for x in (q, out):
-        if tuple(x.shape) != (R, heads, D) or x.dtype != q.dtype or not x.is_cuda or (R and not x[0].is_contiguous()):
-            raise ValueError("q and out must be [R, q_heads, head_dim] with contiguous heads")
+    if out.shape != q.shape or out.dtype != q.dtype or not out.is_cuda or q.stride()[1:] != (D, 1) or out.stride()[1:] != (D, 1):
+        raise ValueError("q and out must be [R, q_heads, head_dim] with contiguous heads")
     if out_lse is None and want_lse:
         out_lse = _new(torch.zeros, (R, heads), torch.float32, q, stream)
     if workspace is None:
-        workspace = _scratch(load().sv_window_attention_workspace_size(cache._ref, heads, R), q, stream)
+        workspace = _scratch((_lib or load()).sv_window_attention_workspace_size(cache._ref, heads, R), q, stream)
     _launch("sv_window_attention", q, stream, q.data_ptr(), q.stride(0) if R > 1 else heads * D, heads, R, cache._ref,
             int(layer), _seqs(page_table, ctx_len), *_windows(page_table.shape[0], cu_draft, cu_cand),
             D ** -0.5 if scale is None else float(scale), out.data_ptr(), out.stride(0) if R > 1 else heads * D,
-            _vec(out_lse, "out_lse", torch.float32, R, heads), _ptr(workspace), workspace.numel(),
-            _vec(status, "status", torch.int32, 1))
+            _vec(out_lse, "out_lse", torch.float32, (R, heads)), _ptr(workspace), workspace.numel(),
+            _vec(status, "status", torch.int32, (1,)))
     return out, out_lse

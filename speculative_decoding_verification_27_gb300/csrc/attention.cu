@@ -46,7 +46,6 @@ constexpr int kTK = 64;    // tokens of a key tile
 struct Plan {
   char* part;          // partial results: two slots a CTA
   int* cut;            // [grid][4]: the unit that a CTA's share cuts at its end: b, head, row tile, its last CTA (b = -1: none)
-  uint32_t div_mul, div_shift;  // t / page_size
 };
 
 struct Unit {
@@ -55,10 +54,6 @@ struct Unit {
   Window w;
   int n_mt, ctx;
 };
-
-__device__ __forceinline__ int div_page(const Plan& L, uint32_t t) {
-  return (int)(((unsigned long long)t * L.div_mul) >> L.div_shift);
-}
 
 // Request b's window, tokens and key tiles, and its number of row tiles (0 tiles where there is nothing to do).
 template <int MT>
@@ -238,6 +233,7 @@ struct Shape {
   static constexpr int kStages = D == 64 ? (WM <= 2 ? 3 : WM == 4 ? 4 : 6) : (WM <= 4 ? 3 : 5);
   static constexpr int kTile = kTK * D * 2;     // bytes of K (or V) of a tile
   static constexpr size_t smem = (size_t)kStages * 2 * kTile + (kStages + 1) * (kTK * 8 + 16);
+  static_assert(kCtas * MT <= 256, "the workspace has room for the partial results");
   // The warps that split the keys join in the stage that they have just used.
   static_assert(WK == 1 || (WK / 2) * MT * (D + 4) * 4 <= 2 * kTile, "a stage holds the results of half the warps");
 };
@@ -278,7 +274,7 @@ __global__ void __launch_bounds__(Shape<D, WM>::kT, Shape<D, WM>::kCtas) window_
     page = -2;
     place = 0;
     if (tid < kTK && t < c.u.keys) {
-      const int slot = div_page(L, t);
+      const int slot = page_slot(P.C, t);
       place = t - slot * P.C.page_size;
       page = P.S.table[(long long)c.u.b * P.S.stride + slot];
     }
@@ -591,7 +587,7 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
       const int t = ld.tile * kTK + tid;
       long long off = -1;
       if (t < ld.u.keys) {
-        const int slot = div_page(L, t), page = P.S.table[(long long)ld.u.b * P.S.stride + slot];
+        const int slot = page_slot(P.C, t), page = P.S.table[(long long)ld.u.b * P.S.stride + slot];
         if (page >= 0 && page < P.C.n_pages)
           off = page * P.C.page_b + (t - slot * P.C.page_size) * P.C.token_b + ld.u.head * P.C.head_b;
         else
@@ -894,8 +890,8 @@ extern "C" {
 
 size_t sv_window_attention_workspace_size(const sv_kv_cache* cache, int32_t n_q_heads, int32_t R) {
   if (!cache || n_q_heads < 1 || R < 0) return 0;
-  // The cuts, then two partial results of at most 128 rows a CTA.
-  return (size_t)sv::att::kGrid * 16 + (size_t)sv::att::kGrid * 2 * 128 * ((size_t)128 + 2) * 4;
+  // The cuts, then two partial results a CTA: of any kernel, 256 rows an SM at most.
+  return (size_t)sv::att::kGrid * 16 + 2 * (size_t)152 * 256 * ((size_t)cache->head_dim + 2) * 4;
 }
 
 sv_status sv_window_attention(const void* q, int64_t q_stride, int32_t n_q_heads, int32_t R, const sv_kv_cache* cache,
@@ -933,11 +929,6 @@ sv_status sv_window_attention(const void* q, int64_t q_stride, int32_t n_q_heads
   att::Plan L{};
   L.cut = static_cast<int*>(workspace);
   L.part = static_cast<char*>(workspace) + att::kGrid * 16;
-  // t / page_size for t < 2^31: with 2^s the next power of two, m = ceil(2^(31 + s) / page_size) errs by less than 2^s.
-  int s = 0;
-  while ((1ll << s) < P.C.page_size) ++s;
-  L.div_shift = 31 + s;
-  L.div_mul = (uint32_t)(((1ull << (31 + s)) + P.C.page_size - 1) / P.C.page_size);
   // Row tiles as high as the windows' mean number of stacked rows.
   const long long rows = ((long long)R + P.S.n - 1) / P.S.n * P.group;
   cudaError_t e;

@@ -310,37 +310,60 @@ __global__ void __launch_bounds__(kT) copy_kernel(CacheView C, const ReserveWs* 
 }
 
 // ---------------------------------------------------------------------------
-// Append: blockIdx.y is the sequence, one warp a (layer, row)
+// Append: blockIdx.y is the sequence, blockIdx.z the layer, one warp a row
 // ---------------------------------------------------------------------------
+// A warp's next row is read before its page is looked up: the row's bytes and
+// the two lookups are in flight together. kIn vectors of K and of V a lane.
+constexpr int kIn = 4;
 __global__ void __launch_bounds__(kT) append_kernel(CacheView C, SeqView S, WindowView W, int layer, int n_layers,
                                                     const char* k_new, const char* v_new, long long new_layer_b,
                                                     long long new_row_b, uint32_t* status) {
-  const int lane = threadIdx.x & 31, vecs = C.head_bytes / 16;
+  const int lane = threadIdx.x & 31, vecs = C.head_bytes / 16, n_vec = C.n_heads * vecs;
+  const bool whole = C.head_b == C.head_bytes;  // a token's heads lie together
   for (int b = blockIdx.y; b < S.n; b += gridDim.y) {
     const Window w = find_window(W, b);
-    const long long len = S.ctx[b];
+    const int len = S.ctx[b];
     if (w.rows < 0 || !length_ok(C, S, len)) {
-      if (blockIdx.x == 0 && threadIdx.x == 0) set_status(status, w.rows < 0 ? SV_DATA_BAD_OFFSETS : SV_DATA_BAD_SEQ);
+      if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0)
+        set_status(status, w.rows < 0 ? SV_DATA_BAD_OFFSETS : SV_DATA_BAD_SEQ);
       continue;
     }
     const int32_t* row = S.table + (long long)b * S.stride;
-    const long long n = (long long)w.rows * n_layers;
-    for (long long u = blockIdx.x * (kT / 32) + (threadIdx.x >> 5); u < n; u += gridDim.x * (kT / 32)) {
-      const int l = (int)(u / w.rows), r = (int)(u % w.rows);
-      const long long at = len + r;
-      const long long slot = at / C.page_size;
-      const int page = slot < S.width ? row[slot] : -1;
-      // A page that others hold too is not written: reserve refused this window.
-      if (page < 0 || page >= C.n_pages || C.ref[page] != 1) {
-        if (lane == 0) set_status(status, SV_DATA_BAD_PAGE);
-        continue;
-      }
-      const long long to = (layer + l) * C.layer_b + page * C.page_b + (at % C.page_size) * C.token_b;
-      const long long from = l * new_layer_b + (w.r0 + r) * new_row_b;
-      for (int x = lane; x < C.n_heads * vecs; x += 32) {
-        const long long o = to + (x / vecs) * C.head_b + (x % vecs) * 16;
-        *reinterpret_cast<uint4*>(C.k + o) = ld_stream16(k_new + from + x * 16);
-        *reinterpret_cast<uint4*>(C.v + o) = ld_stream16(v_new + from + x * 16);
+    for (int l = blockIdx.z; l < n_layers; l += gridDim.z) {
+      for (int r = blockIdx.x * (kT / 32) + (threadIdx.x >> 5); r < w.rows; r += gridDim.x * (kT / 32)) {
+        const long long from = l * new_layer_b + (long long)(w.r0 + r) * new_row_b;
+        uint4 kv[2][kIn];
+#pragma unroll
+        for (int j = 0; j < kIn; ++j) {
+          const int x = j * 32 + lane;
+          if (x < n_vec) {
+            kv[0][j] = ld_stream16(k_new + from + (long long)x * 16);
+            kv[1][j] = ld_stream16(v_new + from + (long long)x * 16);
+          }
+        }
+        const long long at = (long long)len + r;
+        const int slot = at <= 0x7fffffffll ? page_slot(C, (int)at) : S.width;
+        const int page = slot < S.width ? row[slot] : -1;
+        // A page that others hold too is not written: reserve refused this window.
+        if (page < 0 || page >= C.n_pages || C.ref[page] != 1) {
+          if (lane == 0) set_status(status, SV_DATA_BAD_PAGE);
+          continue;
+        }
+        const long long to = (layer + l) * C.layer_b + page * C.page_b + (at - (long long)slot * C.page_size) * C.token_b;
+        for (int x0 = 0; x0 < n_vec; x0 += kIn * 32) {
+#pragma unroll
+          for (int j = 0; j < kIn; ++j) {
+            const int x = x0 + j * 32 + lane;
+            if (x >= n_vec) break;
+            if (x0) {
+              kv[0][j] = ld_stream16(k_new + from + (long long)x * 16);
+              kv[1][j] = ld_stream16(v_new + from + (long long)x * 16);
+            }
+            const long long o = to + (whole ? (long long)x * 16 : (x / vecs) * C.head_b + (x % vecs) * 16);
+            *reinterpret_cast<uint4*>(C.k + o) = kv[0][j];
+            *reinterpret_cast<uint4*>(C.v + o) = kv[1][j];
+          }
+        }
       }
     }
   }
@@ -512,11 +535,11 @@ sv_status sv_cache_append(const sv_kv_cache* cache, int32_t layer, int32_t n_lay
     return SV_ERR_INVALID_ARG;
   if (S.n == 0 || R == 0 || n_layers == 0) return SV_OK;
   if (!k_new || !v_new || (uintptr_t)k_new % 16 || (uintptr_t)v_new % 16) return SV_ERR_INVALID_ARG;
-  const int gy = cache::y_grid(S.n);
-  const long long per = ((long long)R * n_layers + gy - 1) / gy;
-  const long long most = (152 * 8 + gy - 1) / gy;
-  const long long gx = (per + cache::kT / 32 - 1) / (cache::kT / 32);
-  cache::append_kernel<<<dim3((unsigned)(gx < most ? gx : most), gy), cache::kT, 0, static_cast<cudaStream_t>(cuda_stream)>>>(
+  // A warp a row of the mean window, up to eight CTAs an SM.
+  const int gy = cache::y_grid(S.n), gz = n_layers < 64 ? n_layers : 64;
+  const long long gx = ((R + gy - 1) / gy + cache::kT / 32 - 1) / (cache::kT / 32);
+  const long long most = (152 * 8 + (long long)gy * gz - 1) / ((long long)gy * gz);
+  cache::append_kernel<<<dim3((unsigned)(gx < most ? gx : most), gy, gz), cache::kT, 0, static_cast<cudaStream_t>(cuda_stream)>>>(
       C, S, W, layer, n_layers, static_cast<const char*>(k_new), static_cast<const char*>(v_new), new_layer_stride * es,
       new_row_stride * es, status);
   return cache::launched();

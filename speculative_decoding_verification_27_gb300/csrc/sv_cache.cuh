@@ -19,6 +19,7 @@ struct CacheView {
   int n_layers, n_pages, page_size, n_heads, head_bytes;
   int32_t* ref;
   uint32_t* free_bits;
+  uint32_t div_mul, div_shift;  // t / page_size = t * div_mul >> div_shift
 };
 
 struct SeqView {
@@ -49,7 +50,13 @@ inline bool cache_view(const sv_kv_cache* c, CacheView* out) {
     if (x < 0 || x > INT64_MAX / 4 || x * es % 16) return false;
   if ((int64_t)c->head_dim * es % 16) return false;
   *out = CacheView{static_cast<char*>(c->k), static_cast<char*>(c->v), s[0] * es, s[1] * es, s[2] * es, s[3] * es,
-                   c->n_layers, c->n_pages, c->page_size, c->n_kv_heads, c->head_dim * es, c->page_ref, c->free_bits};
+                   c->n_layers, c->n_pages, c->page_size, c->n_kv_heads, c->head_dim * es, c->page_ref, c->free_bits, 0, 0};
+  // For t < 2^31: with 2^s the next power of two, m = ceil(2^(31 + s) / page_size) errs by less than 2^s, so that t m / 2^(31 + s)
+  // is less than 1 / page_size too large.
+  int log2 = 0;
+  while ((1ll << log2) < c->page_size) ++log2;
+  out->div_shift = 31 + log2;
+  out->div_mul = (uint32_t)(((1ull << (31 + log2)) + c->page_size - 1) / c->page_size);
   return true;
 }
 
@@ -84,6 +91,11 @@ __device__ __forceinline__ Window find_window(const WindowView& W, int b) {
   const long long r0 = (long long)W.cu[c0] + c0, r1 = (long long)W.cu[c1] + c1;
   if (W.cu[c0] < 0 || r1 < r0 + (c1 - c0) || r1 > 0x7fffffffll || (W.R >= 0 && r1 > W.R)) return Window{0, 0, 0, -1};
   return Window{c0, c1, (int)r0, (int)(r1 - r0)};
+}
+
+// t / page_size, 0 <= t < 2^31.
+__device__ __forceinline__ int page_slot(const CacheView& C, int t) {
+  return (int)(((unsigned long long)(uint32_t)t * C.div_mul) >> C.div_shift);
 }
 
 // A length that fits its table (and 31 bits with the window).
