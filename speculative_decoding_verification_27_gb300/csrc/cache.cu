@@ -145,24 +145,60 @@ __device__ __forceinline__ int block_excl_scan(int v, int* s_warp, int& total) {
   return x - v + (warp ? s_warp[warp - 1] : 0);
 }
 
+// Place of the n-th set bit (n counts from 0).
+__device__ __forceinline__ int nth_bit(uint32_t x, int n) {
+  int at = 0;
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) {
+    const int c = __popc(x & ((1u << w) - 1u));
+    if (n >= c) {
+      n -= c;
+      at += w;
+      x >>= w;
+    }
+  }
+  return at;
+}
+
+// The last i in [0, n) with first[i] <= k, of an ascending list with first[0] <= k.
+__device__ __forceinline__ int last_at_most(const int* first, int n, int k) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= k)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
 // One CTA: needs, the order among the sharers of a partial page, a scan, and
-// the lowest free bits. Shared memory: three words a sequence.
+// the lowest free bits, whose k-th goes to the request whose range of the
+// scan holds k (a thread a page). Shared memory: three words a sequence.
+// Bound by the chain of its steps (9 us for a few requests, of which the
+// launch and the first loads are half).
 __global__ void __launch_bounds__(kR) reserve_kernel(CacheView C, SeqView S, WindowView W, int32_t* granted, ReserveWs* ws,
                                                      uint32_t* status) {
-  extern __shared__ int s_mem[];
-  int* s_first = s_mem;            // needs, then their exclusive scan [n + 1]
-  int* s_have = s_mem + S.n + 1;   // pages held * 2 + 1 if the partial page is copied; -1: refused
-  int* s_part = s_have + S.n;      // the shared partial page, or -1
-  __shared__ int s_warp[32];
-  __shared__ int s_jobs, s_end;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ __align__(16) int s_mem[];
+  const int n_pad = (S.n + 4) & ~3;
+  int* s_part = s_mem;             // the shared partial page, or -1
+  int* s_first = s_mem + n_pad;    // needs, then their exclusive scan [n + 1]
+  int* s_have = s_first + n_pad;   // pages held * 2 + 1 if the partial page is copied; -1: refused
+  __shared__ int s_warp[32], s_word_first[kR];
+  __shared__ uint32_t s_bits[kR];
+  __shared__ int s_jobs, s_end, s_shared;
   const int tid = threadIdx.x, n_words = (C.n_pages + 31) / 32;
+  uint32_t bits0 = tid < n_words ? C.free_bits[tid] : 0u;  // early: needed last
   if (tid == 0) {
-    s_jobs = 0;
+    s_jobs = s_shared = 0;
     s_end = INT_MAX;
   }
+  __syncthreads();
   for (int b = tid; b < S.n; b += kR) {
+    const int len = S.ctx[b];
     const Window w = find_window(W, b);
-    const long long len = S.ctx[b];
     const int32_t* row = S.table + (long long)b * S.stride;
     int have = -1, need = 0, part = -1;
     uint32_t bad = 0;
@@ -170,50 +206,58 @@ __global__ void __launch_bounds__(kR) reserve_kernel(CacheView C, SeqView S, Win
       bad = SV_DATA_BAD_OFFSETS;
     else if (!length_ok(C, S, len))
       bad = SV_DATA_BAD_SEQ;
-    else if (w.rows > 0 && !length_ok(C, S, len + w.rows))
+    else if (w.rows > 0 && !length_ok(C, S, (long long)len + w.rows))
       bad = SV_DATA_BAD_PAGE;
     else {
-      const int want = pages_of(len + w.rows, C.page_size);
+      const int want = pages_of((long long)len + w.rows, C.page_size);
+      const int full = page_slot(C, len);
       have = pages_of(len, C.page_size);
+      const bool partial = w.rows > 0 && have > full;
+      part = partial ? row[full] : -1;
       while (have < S.width && row[have] >= 0) ++have;  // reserved before
       need = max(0, want - have);
-      if (w.rows > 0 && len % C.page_size) {
-        part = row[len / C.page_size];
-        if (part < 0 || part >= C.n_pages || C.ref[part] < 1) {
+      if (partial) {
+        const int ref = part >= 0 && part < C.n_pages ? C.ref[part] : 0;
+        if (ref < 1) {
           bad = SV_DATA_BAD_PAGE;
           have = -1;
           need = 0;
+        }
+        if (ref <= 1)
           part = -1;
-        } else if (C.ref[part] == 1)
-          part = -1;
+        else
+          s_shared = 1;
       }
     }
     if (bad) set_status(status, bad);
     s_first[b] = need;
-    s_have[b] = have;
+    s_have[b] = have < 0 ? -1 : have * 2;
     s_part[b] = part;
   }
+  for (int b = S.n + tid; b < n_pad; b += kR) s_part[b] = -1;
   __syncthreads();
   // Who copies: a sharer, unless those before it in this call leave it alone with the page.
-  for (int b = tid; b < S.n; b += kR) {
-    const int part = s_part[b];
-    if (part < 0) {
-      s_have[b] = s_have[b] < 0 ? -1 : s_have[b] * 2;
-      continue;
+  if (s_shared) {
+    for (int b = tid; b < S.n; b += kR) {
+      const int part = s_part[b];
+      if (part < 0) continue;
+      int before = 0;
+      for (int j = 0; j < b; j += 4) {
+        const int4 y = *reinterpret_cast<const int4*>(s_part + j);
+        before += (y.x == part && j < b) + (y.y == part && j + 1 < b) + (y.z == part && j + 2 < b) + (y.w == part && j + 3 < b);
+      }
+      const int left = C.ref[part] - before;
+      if (left < 1) {  // more sharers than the count says
+        set_status(status, SV_DATA_BAD_PAGE);
+        s_have[b] = -1;
+        s_first[b] = 0;
+      } else if (left > 1) {
+        s_have[b] += 1;
+        s_first[b] += 1;
+      }
     }
-    int before = 0;
-    for (int j = 0; j < b; ++j) before += s_part[j] == part;
-    const int left = C.ref[part] - before;
-    if (left < 1) {  // more sharers than the count says
-      set_status(status, SV_DATA_BAD_PAGE);
-      s_have[b] = -1;
-      s_first[b] = 0;
-    } else {
-      s_have[b] = s_have[b] * 2 + (left > 1);
-      s_first[b] += left > 1;
-    }
+    __syncthreads();
   }
-  __syncthreads();
   int total = 0;
   for (int b0 = 0; b0 < S.n; b0 += kR) {
     const int b = b0 + tid, v = b < S.n ? s_first[b] : 0;
@@ -223,15 +267,15 @@ __global__ void __launch_bounds__(kR) reserve_kernel(CacheView C, SeqView S, Win
     total += sum;
   }
   if (tid == 0) s_first[S.n] = total;
-  __syncthreads();
-  // Free pages, as far as they are asked for.
-  int avail = 0;
+  // Free pages, as far as they are asked for. With up to 32 kR pages this scan serves the hand-out too.
+  int avail = 0, word_first = 0;
   for (int w0 = 0; w0 < n_words && avail < total; w0 += kR) {
     const int w = w0 + tid;
     int sum;
-    block_excl_scan(w < n_words ? __popc(C.free_bits[w]) : 0, s_warp, sum);
+    word_first = block_excl_scan(w0 == 0 ? __popc(bits0) : w < n_words ? __popc(C.free_bits[w]) : 0, s_warp, sum);
     avail += sum;
   }
+  __syncthreads();
   if (avail < total) {
     for (int b = tid; b < S.n; b += kR)
       if (s_first[b + 1] > s_first[b] && s_first[b + 1] > avail) atomicMin(&s_end, b);
@@ -240,71 +284,83 @@ __global__ void __launch_bounds__(kR) reserve_kernel(CacheView C, SeqView S, Win
     total = s_first[s_end];
   }
   const int end = s_end;
-  __syncthreads();
   for (int b = tid; b < S.n; b += kR) {
     const bool late = b >= end && (s_first[b + 1] > s_first[b] || s_part[b] >= 0);
     if (late) s_have[b] = -1;
     if (granted) granted[b] = s_have[b] >= 0 ? find_window(W, b).rows : 0;
   }
-  __syncthreads();
-  // The k-th lowest free page goes to the request whose range of the scan holds k.
   int taken = 0;
   for (int w0 = 0; w0 < n_words && taken < total; w0 += kR) {
     const int w = w0 + tid;
-    uint32_t bits = w < n_words ? C.free_bits[w] : 0u;
-    int sum;
-    int k = taken + block_excl_scan(__popc(bits), s_warp, sum);
-    taken += sum;
-    uint32_t left = bits;
-    for (; left && k < total; ++k) {
-      const int bit = __ffs(left) - 1;
-      left &= left - 1;
-      const int page = w * 32 + bit;
-      int lo = 0, hi = S.n;  // the last request that begins at or before k
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_first[mid] <= k)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      const int i = k - s_first[lo], have = s_have[lo] >> 1, copy = s_have[lo] & 1;
-      int32_t* row = S.table + (long long)lo * S.stride;
+    const uint32_t bits = w0 == 0 ? bits0 : w < n_words ? C.free_bits[w] : 0u;
+    const int mine = __popc(bits);
+    int sum = min(avail, INT_MAX), first = word_first;
+    if (n_words > kR) first = block_excl_scan(mine, s_warp, sum);
+    s_word_first[tid] = first;
+    s_bits[tid] = bits;
+    const int use = min(max(total - taken - first, 0), mine);
+    if (use) {
+      uint32_t left = bits;
+      for (int i = 0; i < use; ++i) left &= left - 1;
+      C.free_bits[w] = left;
+    }
+    __syncthreads();
+    for (int k = taken + tid; k < min(taken + sum, total); k += kR) {
+      const int word = last_at_most(s_word_first, kR, k - taken);
+      const int page = (w0 + word) * 32 + nth_bit(s_bits[word], k - taken - s_word_first[word]);
+      const int b = last_at_most(s_first, S.n, k);
+      const int i = k - s_first[b], have = s_have[b] >> 1, copy = s_have[b] & 1;
+      int32_t* row = S.table + (long long)b * S.stride;
       C.ref[page] = 1;
       if (copy && i == 0) {
-        const int len = S.ctx[lo], at = len / C.page_size, old = row[at];
+        const int len = S.ctx[b], at = page_slot(C, len), old = row[at];
         row[at] = page;
         atomicSub(&C.ref[old], 1);
-        ws->jobs[atomicAdd(&s_jobs, 1)] = CopyJob{old, page, len % C.page_size, 0};
+        ws->jobs[atomicAdd(&s_jobs, 1)] = CopyJob{old, page, len - at * C.page_size, 0};
       } else {
         row[have + i - copy] = page;
       }
     }
-    if (left != bits) C.free_bits[w] = left;
+    taken += sum;
+    __syncthreads();
   }
-  __syncthreads();
   if (tid == 0) ws->n_jobs = s_jobs;
 }
 
-// The copies that reserve asked for: one warp a (job, layer, K or V, token).
+// The copies that reserve asked for: a CTA a (job, layer, K or V), 16-byte
+// vectors of whole tokens, four a thread in flight.
 __global__ void __launch_bounds__(kT) copy_kernel(CacheView C, const ReserveWs* ws) {
-  const int lane = threadIdx.x & 31;
-  const long long warp = blockIdx.x * (long long)(kT / 32) + (threadIdx.x >> 5);
-  const long long step = gridDim.x * (long long)(kT / 32);
-  const int vecs = C.head_bytes / 16;
-  const long long n = (long long)ws->n_jobs * C.n_layers * 2 * C.page_size;
-  for (long long u = warp; u < n; u += step) {
-    const int token = (int)(u % C.page_size);
-    const long long rest = u / C.page_size;
-    const int kv = (int)(rest & 1), layer = (int)((rest >> 1) % C.n_layers);
-    const CopyJob j = ws->jobs[(rest >> 1) / C.n_layers];
-    if (token >= j.tokens) continue;
-    char* base = (kv ? C.v : C.k) + layer * C.layer_b + token * C.token_b;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int vecs = C.head_bytes / 16, n_vec = C.n_heads * vecs;
+  const bool whole = C.head_b == C.head_bytes && C.token_b == (long long)C.n_heads * C.head_b;  // tokens lie one after another
+  const long long n = (long long)ws->n_jobs * C.n_layers * 2;
+  for (long long u = blockIdx.x; u < n; u += gridDim.x) {
+    const int part = (int)(u % (C.n_layers * 2));
+    const CopyJob j = ws->jobs[u / (C.n_layers * 2)];
+    char* base = (part & 1 ? C.v : C.k) + (part >> 1) * C.layer_b;
     const char* from = base + j.from * C.page_b;
     char* to = base + j.to * C.page_b;
-    for (int x = lane; x < C.n_heads * vecs; x += 32) {
-      const long long at = (x / vecs) * C.head_b + (x % vecs) * 16;
-      *reinterpret_cast<uint4*>(to + at) = *reinterpret_cast<const uint4*>(from + at);
+    const int items = j.tokens * n_vec;  // page_size <= 2^20, heads and vectors within 2^31 in all: see the host checks
+    for (int x0 = threadIdx.x; x0 < items; x0 += kT * 4) {
+      uint4 v[4];
+      long long at[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int x = x0 + i * kT;
+        if (x >= items) break;
+        if (whole) {
+          at[i] = (long long)x * 16;
+        } else {
+          const int token = x / n_vec, y = x - token * n_vec, head = y / vecs;
+          at[i] = token * C.token_b + head * C.head_b + (y - head * vecs) * 16;
+        }
+        v[i] = *reinterpret_cast<const uint4*>(from + at[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (x0 + i * kT >= items) break;
+        *reinterpret_cast<uint4*>(to + at[i]) = v[i];
+      }
     }
   }
 }
@@ -312,17 +368,19 @@ __global__ void __launch_bounds__(kT) copy_kernel(CacheView C, const ReserveWs* 
 // ---------------------------------------------------------------------------
 // Append: blockIdx.y is the sequence, blockIdx.z the layer, one warp a row
 // ---------------------------------------------------------------------------
-// A warp's next row is read before its page is looked up: the row's bytes and
-// the two lookups are in flight together. kIn vectors of K and of V a lane.
+// A warp looks up the pages of its next 32 rows at once (a lane a row), and
+// reads a row before it writes the one ahead of it. kIn vectors of K and of V
+// a lane.
 constexpr int kIn = 4;
 __global__ void __launch_bounds__(kT) append_kernel(CacheView C, SeqView S, WindowView W, int layer, int n_layers,
                                                     const char* k_new, const char* v_new, long long new_layer_b,
                                                     long long new_row_b, uint32_t* status) {
   const int lane = threadIdx.x & 31, vecs = C.head_bytes / 16, n_vec = C.n_heads * vecs;
+  const int warp0 = blockIdx.x * (kT / 32) + (threadIdx.x >> 5), step = gridDim.x * (kT / 32);
   const bool whole = C.head_b == C.head_bytes;  // a token's heads lie together
   for (int b = blockIdx.y; b < S.n; b += gridDim.y) {
-    const Window w = find_window(W, b);
     const int len = S.ctx[b];
+    const Window w = find_window(W, b);
     if (w.rows < 0 || !length_ok(C, S, len)) {
       if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0)
         set_status(status, w.rows < 0 ? SV_DATA_BAD_OFFSETS : SV_DATA_BAD_SEQ);
@@ -330,38 +388,54 @@ __global__ void __launch_bounds__(kT) append_kernel(CacheView C, SeqView S, Wind
     }
     const int32_t* row = S.table + (long long)b * S.stride;
     for (int l = blockIdx.z; l < n_layers; l += gridDim.z) {
-      for (int r = blockIdx.x * (kT / 32) + (threadIdx.x >> 5); r < w.rows; r += gridDim.x * (kT / 32)) {
-        const long long from = l * new_layer_b + (long long)(w.r0 + r) * new_row_b;
-        uint4 kv[2][kIn];
+      const char* k_from = k_new + l * new_layer_b + (long long)w.r0 * new_row_b + lane * 16;
+      const char* v_from = v_new + (k_from - k_new);
+      uint4 kv[2][kIn];
+      auto read = [&](int r, int x0) {
+        const long long from = (long long)r * new_row_b + (long long)x0 * 16;
 #pragma unroll
         for (int j = 0; j < kIn; ++j) {
-          const int x = j * 32 + lane;
-          if (x < n_vec) {
-            kv[0][j] = ld_stream16(k_new + from + (long long)x * 16);
-            kv[1][j] = ld_stream16(v_new + from + (long long)x * 16);
-          }
+          if (x0 + j * 32 + lane >= n_vec) break;
+          kv[0][j] = ld_stream16(k_from + from + j * 512);
+          kv[1][j] = ld_stream16(v_from + from + j * 512);
         }
-        const long long at = (long long)len + r;
-        const int slot = at <= 0x7fffffffll ? page_slot(C, (int)at) : S.width;
-        const int page = slot < S.width ? row[slot] : -1;
-        // A page that others hold too is not written: reserve refused this window.
-        if (page < 0 || page >= C.n_pages || C.ref[page] != 1) {
-          if (lane == 0) set_status(status, SV_DATA_BAD_PAGE);
-          continue;
+      };
+      for (long long r0 = warp0; r0 < w.rows; r0 += 32ll * step) {
+        read((int)r0, 0);
+        const long long mine = r0 + (long long)lane * step;
+        long long to = -1;
+        if (mine < w.rows) {
+          const long long at = len + mine;
+          const int slot = at <= 0x7fffffffll ? page_slot(C, (int)at) : S.width;
+          const int page = slot < S.width ? row[slot] : -1;
+          // A page that others hold too is not written: reserve refused this window.
+          if (page >= 0 && page < C.n_pages && C.ref[page] == 1)
+            to = (layer + l) * C.layer_b + page * C.page_b + (at - (long long)slot * C.page_size) * C.token_b;
+          else
+            set_status(status, SV_DATA_BAD_PAGE);
         }
-        const long long to = (layer + l) * C.layer_b + page * C.page_b + (at - (long long)slot * C.page_size) * C.token_b;
-        for (int x0 = 0; x0 < n_vec; x0 += kIn * 32) {
+        const int n = (int)min(32ll, (w.rows - r0 + step - 1) / step);
+        for (int i = 0; i < n; ++i) {
+          const int r = (int)(r0 + (long long)i * step);
+          const long long dst = __shfl_sync(kFull, to, i);
+          for (int x0 = 0; x0 < n_vec; x0 += kIn * 32) {
+            if (x0) read(r, x0);
+            uint4 out[2][kIn];
 #pragma unroll
-          for (int j = 0; j < kIn; ++j) {
-            const int x = x0 + j * 32 + lane;
-            if (x >= n_vec) break;
-            if (x0) {
-              kv[0][j] = ld_stream16(k_new + from + (long long)x * 16);
-              kv[1][j] = ld_stream16(v_new + from + (long long)x * 16);
+            for (int j = 0; j < kIn; ++j) {
+              out[0][j] = kv[0][j];
+              out[1][j] = kv[1][j];
             }
-            const long long o = to + (whole ? (long long)x * 16 : (x / vecs) * C.head_b + (x % vecs) * 16);
-            *reinterpret_cast<uint4*>(C.k + o) = kv[0][j];
-            *reinterpret_cast<uint4*>(C.v + o) = kv[1][j];
+            if (x0 + kIn * 32 >= n_vec && i + 1 < n) read((int)(r + (long long)step), 0);
+            if (dst < 0) continue;
+#pragma unroll
+            for (int j = 0; j < kIn; ++j) {
+              const int x = x0 + j * 32 + lane;
+              if (x >= n_vec) break;
+              const long long o = dst + (whole ? (long long)x * 16 : (x / vecs) * C.head_b + (x % vecs) * 16);
+              *reinterpret_cast<uint4*>(C.k + o) = out[0][j];
+              *reinterpret_cast<uint4*>(C.v + o) = out[1][j];
+            }
           }
         }
       }
@@ -379,52 +453,68 @@ struct Kept {
 };
 __device__ __forceinline__ Kept kept_rows(const CacheView& C, const SeqView& S, const WindowView& W, const int32_t* best,
                                           const int32_t* out_len, int b) {
+  // The loads that need nothing first.
+  const long long len = S.ctx[b];
+  const int c = best ? best[b] : b;
+  const bool c_ok = c >= 0 && c < W.n_cand;
+  const int n = c_ok ? out_len[c] : 0;
+  const int cu0 = c_ok && W.cu ? W.cu[c] : 0, cu1 = c_ok && W.cu ? W.cu[c + 1] : 0;
   const Window w = find_window(W, b);
   if (w.rows < 0) return Kept{0, 0, SV_DATA_BAD_OFFSETS};
-  const long long len = S.ctx[b];
   if (!length_ok(C, S, len)) return Kept{0, 0, SV_DATA_BAD_SEQ};
-  const int c = best ? best[b] : b;
   if (best && c == -1) return Kept{0, 0, 0};
   if (c < w.c0 || c >= w.c1) return Kept{0, 0, SV_DATA_BAD_OFFSETS};
-  const int n = out_len[c];
   long long begin = 0, rows = 1;
   if (W.cu) {
-    begin = (long long)W.cu[c] + c - w.r0;
-    rows = (long long)W.cu[c + 1] + 1 - W.cu[c];
+    begin = (long long)cu0 + c - w.r0;
+    rows = (long long)cu1 + 1 - cu0;
   }
   if (begin < 0 || rows < 1 || begin + rows > w.rows || n < 0 || n > rows) return Kept{0, 0, SV_DATA_BAD_OFFSETS};
   if (n == 0) return Kept{0, 0, 0};
   // Every page from the history's end to the kept rows' must be there, and be this sequence's alone.
   if (!length_ok(C, S, len + begin + n)) return Kept{0, 0, SV_DATA_BAD_PAGE};
   const int32_t* row = S.table + (long long)b * S.stride;
-  for (long long p = len / C.page_size; p <= (len + begin + n - 1) / C.page_size; ++p)
+  for (int p = page_slot(C, (int)len), end = page_slot(C, (int)(len + begin + n - 1)); p <= end; ++p)
     if (row[p] < 0 || row[p] >= C.n_pages || C.ref[row[p]] != 1) return Kept{0, 0, SV_DATA_BAD_PAGE};
   return Kept{(int)begin, n, 0};
 }
 
-// The kept candidate's rows to the front of the window. A thread owns one
-// 16-byte column and walks it upwards: a row is read before a lower one's
-// place that it lies in is written.
+// The kept candidate's rows to the front of the window. A thread owns 16-byte
+// columns and walks each upwards, kMove rows at a time, all read before the
+// first is written: a row is read before a lower one's place that it lies in
+// is written.
+constexpr int kMove = 8;
 __global__ void __launch_bounds__(kT) move_kernel(CacheView C, SeqView S, WindowView W, const int32_t* best,
                                                   const int32_t* out_len) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ long long s_from[kMove], s_to[kMove];
   const int vecs = C.head_bytes / 16;
   const long long cols = 2ll * C.n_layers * C.n_heads * vecs;
   for (int b = blockIdx.y; b < S.n; b += gridDim.y) {
     const Kept kept = kept_rows(C, S, W, best, out_len, b);
     if (kept.bad || kept.begin == 0 || kept.rows == 0) continue;
     const int32_t* row = S.table + (long long)b * S.stride;
-    const long long len = S.ctx[b];
-    for (long long x = blockIdx.x * kT + threadIdx.x; x < cols; x += gridDim.x * kT) {
-      const int vec = (int)(x % vecs);
-      const long long y = x / vecs;
-      const int head = (int)(y % C.n_heads);
-      const int layer = (int)(y / C.n_heads) >> 1;
-      char* base = ((y / C.n_heads) & 1 ? C.v : C.k) + layer * C.layer_b + head * C.head_b + vec * 16;
-      for (int j = 0; j < kept.rows; ++j) {
-        const long long a = len + kept.begin + j, d = len + j;
-        const char* from = base + row[a / C.page_size] * C.page_b + (a % C.page_size) * C.token_b;
-        char* to = base + row[d / C.page_size] * C.page_b + (d % C.page_size) * C.token_b;
-        *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+    const int len = S.ctx[b];
+    for (int j0 = 0; j0 < kept.rows; j0 += kMove) {
+      const int n = min(kMove, kept.rows - j0);
+      __syncthreads();
+      if ((int)threadIdx.x < 2 * n) {
+        const int j = threadIdx.x >> 1, t = len + j0 + j + (threadIdx.x & 1 ? 0 : kept.begin), slot = page_slot(C, t);
+        (threadIdx.x & 1 ? s_to : s_from)[j] = row[slot] * C.page_b + (t - slot * C.page_size) * C.token_b;
+      }
+      __syncthreads();
+      for (long long x = blockIdx.x * kT + threadIdx.x; x < cols; x += gridDim.x * kT) {
+        const int vec = (int)(x % vecs);
+        const long long y = x / vecs;
+        const int head = (int)(y % C.n_heads), part = (int)(y / C.n_heads);
+        char* base = (part & 1 ? C.v : C.k) + (part >> 1) * C.layer_b + head * C.head_b + vec * 16;
+        uint4 v[kMove];
+#pragma unroll
+        for (int j = 0; j < kMove; ++j)
+          if (j < n) v[j] = *reinterpret_cast<const uint4*>(base + s_from[j]);
+#pragma unroll
+        for (int j = 0; j < kMove; ++j)
+          if (j < n) *reinterpret_cast<uint4*>(base + s_to[j]) = v[j];
       }
     }
   }
@@ -433,6 +523,7 @@ __global__ void __launch_bounds__(kT) move_kernel(CacheView C, SeqView S, Window
 // The new length, and the pages behind it released: one warp a request.
 __global__ void __launch_bounds__(kT) trim_kernel(CacheView C, SeqView S, WindowView W, const int32_t* best,
                                                   const int32_t* out_len, uint32_t* status) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.x * (kT / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (b >= S.n) return;
   const Kept kept = kept_rows(C, S, W, best, out_len, b);
@@ -451,6 +542,21 @@ inline sv_status launched() { return cudaGetLastError() == cudaSuccess ? SV_OK :
 inline int warps_grid(long long n) {
   const long long g = (n + kT / 32 - 1) / (kT / 32);
   return (int)(g > (1 << 30) ? (1 << 30) : g);
+}
+// Launches a kernel that waits for the one before it in the stream by itself (griddepcontrol.wait): the launches overlap.
+template <typename... A>
+sv_status launch_after(void (*kernel)(A...), dim3 grid, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kT);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e == cudaSuccess ? launched() : SV_ERR_CUDA;
 }
 inline int y_grid(int n) { return n > 32768 ? 32768 : n; }
 
@@ -505,16 +611,16 @@ sv_status sv_cache_reserve(const sv_kv_cache* cache, const sv_sequences* seqs, i
     return SV_ERR_INVALID_ARG;
   W.R = -1;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  const int smem = (3 * S.n + 1) * 4;
+  const int smem = 3 * ((S.n + 4) & ~3) * 4;
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(cache::reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return SV_ERR_CUDA;
   cache::ReserveWs* ws = static_cast<cache::ReserveWs*>(workspace);
   cache::reserve_kernel<<<1, cache::kR, smem, st>>>(C, S, W, granted, ws, status);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
-  const int most = cache::warps_grid((long long)S.n * C.n_layers * 2 * C.page_size);
-  cache::copy_kernel<<<most < 152 * 8 ? most : 152 * 8, cache::kT, 0, st>>>(C, ws);
-  return cache::launched();
+  const long long most = (long long)S.n * C.n_layers * 2;
+  return cache::launch_after(cache::copy_kernel, dim3((unsigned)(most < 152 * 8 ? most : 152 * 8)), st, C,
+                             static_cast<const cache::ReserveWs*>(ws));
 }
 
 sv_status sv_cache_append(const sv_kv_cache* cache, int32_t layer, int32_t n_layers, const void* k_new, const void* v_new,
@@ -560,15 +666,17 @@ sv_status sv_cache_commit(const sv_kv_cache* cache, const sv_sequences* seqs, in
   if (!out_len) return SV_ERR_INVALID_ARG;
   W.R = -1;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  if (cu_cand) {  // without candidates the kept rows are in place
-    const long long cols = 2ll * C.n_layers * C.n_heads * (C.head_bytes / 16);
-    const int gy = cache::y_grid(S.n);
-    const long long gx = (cols + cache::kT - 1) / cache::kT, most = (152 * 8 + gy - 1) / gy;
-    cache::move_kernel<<<dim3((unsigned)(gx < most ? gx : most), gy), cache::kT, 0, st>>>(C, S, W, best, out_len);
-    if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  const dim3 trim((unsigned)cache::warps_grid(S.n));
+  if (!cu_cand) {  // without candidates the kept rows are in place
+    cache::trim_kernel<<<trim, cache::kT, 0, st>>>(C, S, W, best, out_len, status);
+    return cache::launched();
   }
-  cache::trim_kernel<<<cache::warps_grid(S.n), cache::kT, 0, st>>>(C, S, W, best, out_len, status);
-  return cache::launched();
+  const long long cols = 2ll * C.n_layers * C.n_heads * (C.head_bytes / 16);
+  const int gy = cache::y_grid(S.n);
+  const long long gx = (cols + cache::kT - 1) / cache::kT, most = (152 * 8 + gy - 1) / gy;
+  cache::move_kernel<<<dim3((unsigned)(gx < most ? gx : most), gy), cache::kT, 0, st>>>(C, S, W, best, out_len);
+  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  return cache::launch_after(cache::trim_kernel, trim, st, C, S, W, best, out_len, status);
 }
 
 }  // extern "C"

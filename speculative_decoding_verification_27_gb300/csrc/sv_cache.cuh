@@ -49,6 +49,9 @@ inline bool cache_view(const sv_kv_cache* c, CacheView* out) {
   for (int64_t x : s)
     if (x < 0 || x > INT64_MAX / 4 || x * es % 16) return false;
   if ((int64_t)c->head_dim * es % 16) return false;
+  // The 16-byte vectors of a page (of one layer, K or V) are counted in 31 bits.
+  if ((int64_t)c->n_kv_heads * (c->head_dim * es / 16) > (1 << 20)) return false;
+  if ((int64_t)c->n_kv_heads * (c->head_dim * es / 16) * c->page_size > (1 << 30)) return false;
   *out = CacheView{static_cast<char*>(c->k), static_cast<char*>(c->v), s[0] * es, s[1] * es, s[2] * es, s[3] * es,
                    c->n_layers, c->n_pages, c->page_size, c->n_kv_heads, c->head_dim * es, c->page_ref, c->free_bits, 0, 0};
   // For t < 2^31: with 2^s the next power of two, m = ceil(2^(31 + s) / page_size) errs by less than 2^s, so that t m / 2^(31 + s)
