@@ -544,6 +544,460 @@ __global__ void __launch_bounds__(Shape<D, WM>::kT, Shape<D, WM>::kCtas) window_
 }
 
 // ---------------------------------------------------------------------------
+// bf16, row tiles of 128: the fifth-generation tensor cores
+// ---------------------------------------------------------------------------
+// S = Q K^T and O += P V by tcgen05.mma with S, P and O in tensor memory.
+// Three roles, joined by mbarriers only:
+//   warps 0 - 3  softmax and output: a thread owns a row (a TMEM lane). The
+//                reference maximum moves only when a row's maximum outgrows it
+//                by 2^8, since moving it means rescaling O in TMEM;
+//   2 or 4 more  copies: Q tiles (two buffers), then K and V tiles gathered
+//                over the pages into a ring of swizzled stages;
+//   the last     one thread issues the products: S of tile i, then P V of tile
+//                i - 1, so that the softmax of a tile runs beside the next S.
+// Every wait is bounded: where one gives up the CTA sets SV_DEV_COPY_TIMEOUT,
+// lets its copies and products end, frees its tensor memory and leaves.
+template <int D>
+struct TcShape {
+  static constexpr int MT = 128;
+  static constexpr int kCopy = D == 64 ? 64 : 128;  // threads that copy
+  static constexpr int kT = 128 + kCopy + 32;
+  static constexpr int kMmaWarp = 4 + kCopy / 32;
+  static constexpr int kCtas = D == 64 ? 2 : 1;   // an SM
+  static constexpr int kStages = 4;
+  static constexpr int kRing = kStages + 2;        // tiles whose page lookups are kept
+  static constexpr int kTile = kTK * D * 2;        // bytes of K (or V) of a tile
+  static constexpr int kQ = MT * D * 2;            // bytes of a Q tile
+  static constexpr size_t smem = 1024 + 2 * kQ + (size_t)kStages * 2 * kTile + kRing * (kTK * 8 + 16);
+  static constexpr int kCols = 256;                // TMEM columns: O (D), then two S tiles (64 each, P in their first half)
+};
+
+__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lead_bytes) {
+  // 128-byte swizzle, eight rows of 128 bytes an atom of 1024 bytes; atoms follow each other.
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lead_bytes >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+constexpr uint32_t umma_idesc(int n, bool b_mn_major) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 | (uint32_t)(128 / 16) << 24;
+}
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// Arrives on the mbarrier when the products issued before have ended.
+__device__ __forceinline__ void umma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+      "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+          addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// A barrier of the N copying threads; true where all of them are alive, so
+// that all of them go on or leave.
+template <int N>
+__device__ __forceinline__ bool copies_sync(bool alive) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)alive), "n"(N)
+      : "memory");
+  return all != 0;
+}
+// Arrives on the mbarrier when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+struct TcBars {
+  uint64_t full[4], empty[4];  // a stage's tile has landed; its P V has ended
+  uint64_t s_full[2];          // S has been computed
+  uint64_t p_ready[2];         // S has been read, P written, O rescaled
+  uint64_t q_full[2], q_empty[2];
+  uint64_t o_done;             // a tile's P V has ended
+  uint64_t o_free;             // a unit's O has been read
+  uint64_t end;                // every product has ended
+};
+
+template <int D>
+__global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_kernel(Params P, Plan L) {
+  using Sh = TcShape<D>;
+  constexpr int S = Sh::kStages, R = Sh::kRing, CH = D / 64;  // CH: chunks of 64 elements (128 bytes) of a row
+  extern __shared__ char smem_raw[];
+  __shared__ TcBars bars;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  Share sh;
+  Cursor c;
+  if (!take_share<128, Sh::kT>(P, L, sh, c)) return;
+  const int n_tiles = (int)(sh.t1 - sh.t0);
+
+  char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  const uint32_t q_base = smem_addr(smem), kv_base = q_base + 2 * Sh::kQ;
+  long long* s_off = reinterpret_cast<long long*>(smem + 2 * Sh::kQ + S * 2 * Sh::kTile);  // [R][kTK]
+  uint32_t* s_valid = reinterpret_cast<uint32_t*>(s_off + R * kTK);                        // [R][4]
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(smem_addr(&bars.full[i]), Sh::kCopy + 1);
+      mbar_init(smem_addr(&bars.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&bars.s_full[i]), 1);
+      mbar_init(smem_addr(&bars.p_ready[i]), 128);
+      mbar_init(smem_addr(&bars.q_full[i]), Sh::kCopy);
+      mbar_init(smem_addr(&bars.q_empty[i]), 1);
+    }
+    mbar_init(smem_addr(&bars.o_done), 1);
+    mbar_init(smem_addr(&bars.o_free), 128);
+    mbar_init(smem_addr(&bars.end), 1);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == Sh::kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem)), "r"(Sh::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  volatile int* abort_flag = &s_abort;
+  // Waits for a phase; false once any wait of the CTA has given up.
+  auto wait = [&](uint64_t& bar, int parity) {
+    const uint32_t a = smem_addr(&bar);
+    for (int it = 0; it < kSpinLimit; ++it) {
+      if (mbar_try_wait(a, (uint32_t)parity)) return true;
+      if (*abort_flag) return false;
+    }
+    *abort_flag = 1;
+    set_status(P.status, SV_DEV_COPY_TIMEOUT);
+    return false;
+  };
+
+  if (warp >= 4 && warp < Sh::kMmaWarp) {
+    // ---------------------------------------------------------------- copies
+    const int t = tid - 128;
+    int page = -2, place = 0;
+    static_assert(Sh::kCopy >= kTK, "a copying thread looks up a token at most");
+    Cursor ld = c;        // the tile whose lookup is in the registers
+    int unit = 0;
+    auto lookup = [&]() {
+      const int k = ld.tile * kTK + t;
+      page = -2;
+      place = 0;
+      if (t < kTK && k < ld.u.keys) {
+        const int slot = page_slot(P.C, k);
+        place = k - slot * P.C.page_size;
+        page = P.S.table[(long long)ld.u.b * P.S.stride + slot];
+      }
+    };
+    auto store_lookup = [&](int ring) {
+      if (t < kTK) {
+        const bool ok = page >= 0 && page < P.C.n_pages;
+        if (!ok && page != -2) set_status(P.status, SV_DATA_BAD_PAGE);
+        s_off[ring * kTK + t] = ok ? page * P.C.page_b + place * P.C.token_b + ld.u.head * P.C.head_b : -1;
+        const unsigned m = __ballot_sync(kFull, ok);
+        if (lane == 0) s_valid[ring * 4 + (t >> 5)] = m;
+      }
+    };
+    lookup();
+    store_lookup(0);
+    if (n_tiles > 1) {
+      if (++ld.tile == ld.u.tiles) next_unit<128>(P, ld);
+      lookup();
+    }
+    for (int i = 0; i < n_tiles; ++i) {
+      bool alive = true;
+      const bool new_unit = i == 0 || c.tile == 0;
+      if (new_unit && unit >= 2) alive = wait(bars.q_empty[unit & 1], ((unit >> 1) - 1) & 1);
+      if (i >= S) alive = alive && wait(bars.empty[i % S], (i / S - 1) & 1);
+      if (!copies_sync<Sh::kCopy>(alive)) break;  // tile i's offsets are there, too
+      if (new_unit) {  // a unit's rows
+        const uint32_t qb = q_base + (unit & 1) * Sh::kQ;
+        const int rows = c.u.w.rows * P.group;
+        for (int x = t; x < 128 * (D / 8); x += Sh::kCopy) {
+          const int r = x / (D / 8), ch = x % (D / 8), row = c.u.mt * 128 + r;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (row < rows) {
+            const int w = row / P.group, h = row - w * P.group;
+            v = *reinterpret_cast<const uint4*>(P.q + (long long)(c.u.w.r0 + w) * P.q_row_b +
+                                                (long long)(c.u.head * P.group + h) * (D * 2) + ch * 16);
+            v.x = (v.x & P.q_mask) ^ P.q_sign;
+            v.y = (v.y & P.q_mask) ^ P.q_sign;
+            v.z = (v.z & P.q_mask) ^ P.q_sign;
+            v.w = (v.w & P.q_mask) ^ P.q_sign;
+          }
+          const uint32_t a = qb + (ch >> 3) * (128 * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(smem_addr(&bars.q_full[unit & 1]));
+        ++unit;
+      }
+      {
+        const uint32_t base = kv_base + (i % S) * 2 * Sh::kTile;
+        constexpr int CPR = D / 8, RPP = Sh::kCopy / CPR;
+        const int ch = t % CPR;
+#pragma unroll 8
+        for (int j = 0; j < kTK / RPP; ++j) {
+          const int r = t / CPR + j * RPP;
+          const long long off = s_off[(i % R) * kTK + r];
+          const bool ok = off >= 0;
+          const long long at = (ok ? off : 0) + ch * 16;
+          const uint32_t dst = base + (ch >> 3) * (kTK * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+          cp16(dst, P.C.k + at, ok);
+          cp16(dst + Sh::kTile, P.C.v + at, ok);
+        }
+        cp_arrive(smem_addr(&bars.full[i % S]));
+        if (t == 0) mbar_arrive(smem_addr(&bars.full[i % S]));  // releases the tile's s_valid, written before the last barrier
+      }
+      if (i + 1 < n_tiles) {
+        store_lookup((i + 1) % R);
+        if (i + 2 < n_tiles) {
+          if (++ld.tile == ld.u.tiles) next_unit<128>(P, ld);
+          lookup();
+        }
+      }
+      if (++c.tile == c.u.tiles && i + 1 < n_tiles) next_unit<128>(P, c);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == Sh::kMmaWarp) {
+    // -------------------------------------------------------------- products
+    if (lane == 0) {
+      bool alive = true;
+      int unit = -1;                      // of the S being issued
+      int pv_unit = 0;                    // of the P V being issued
+      bool pv_first = true;
+      auto issue_pv = [&](int i) {
+        alive = alive && wait(bars.p_ready[i & 1], (i >> 1) & 1);
+        if (alive && pv_first && pv_unit > 0) alive = wait(bars.o_free, (pv_unit - 1) & 1);
+        if (!alive) return;
+        tc_fence_after();
+        const uint32_t vb = kv_base + (i % S) * 2 * Sh::kTile + Sh::kTile, pa = tmem + D + (i & 1) * 64;
+#pragma unroll
+        for (int k = 0; k < kTK / 16; ++k)
+          umma_ts(tmem, pa + k * 8, umma_desc(vb + k * 2048, kTK * 128), umma_idesc(D, true), !(pv_first && k == 0));
+        umma_commit(smem_addr(&bars.empty[i % S]));
+        umma_commit(smem_addr(&bars.o_done));
+      };
+      bool prev_last = false;  // tile i - 1 ends its unit
+      for (int i = 0; i < n_tiles && alive; ++i) {
+        if (i == 0 || c.tile == 0) {
+          ++unit;
+          alive = wait(bars.q_full[unit & 1], (unit >> 1) & 1);
+        }
+        alive = alive && wait(bars.full[i % S], (i / S) & 1);
+        if (!alive) break;
+        fence_proxy_async_smem();  // the copies wrote the tile through the generic proxy, the products read it through the other
+        tc_fence_after();
+        const uint32_t qb = q_base + (unit & 1) * Sh::kQ, kb = kv_base + (i % S) * 2 * Sh::kTile;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          umma_ss(tmem + D + (i & 1) * 64, umma_desc(qb + (k >> 2) * (128 * 128) + (k & 3) * 32, 16),
+                  umma_desc(kb + (k >> 2) * (kTK * 128) + (k & 3) * 32, 16), umma_idesc(kTK, false), k > 0);
+        umma_commit(smem_addr(&bars.s_full[i & 1]));
+        const bool last = c.tile + 1 == c.u.tiles || i + 1 == n_tiles;
+        if (last) umma_commit(smem_addr(&bars.q_empty[unit & 1]));
+        if (i > 0) {
+          issue_pv(i - 1);
+          pv_first = prev_last;
+          pv_unit += prev_last;
+        }
+        prev_last = last;
+        if (++c.tile == c.u.tiles && i + 1 < n_tiles) next_unit<128>(P, c);
+      }
+      if (alive) issue_pv(n_tiles - 1);
+      umma_commit(smem_addr(&bars.end));
+      for (int it = 0; it < kSpinLimit && !mbar_try_wait(smem_addr(&bars.end), 0); ++it) {
+      }
+    }
+    __syncwarp();
+  } else {
+    // --------------------------------------------------- softmax and output
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    bool alive = true, from_start = false;
+    int lo = 0, hi = 0;
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < n_tiles; ++i) {
+      if (i + 1 == n_tiles) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      const int rows = c.u.w.rows * P.group, row = c.u.mt * 128 + tid;
+      if (i == 0 || c.tile == 0) {
+        from_start = c.tile == 0;
+        const int w = row < rows ? row / P.group : 0;
+        lo = row < rows ? candidate_start(P, c.u.w, w) : 0;
+        hi = row < rows ? w : -1 - c.u.ctx;  // rows past the window see nothing
+        m = -INFINITY;
+        l = 0.f;
+      }
+      alive = wait(bars.full[i % S], (i / S) & 1) && wait(bars.s_full[i & 1], (i >> 1) & 1);
+      if (__any_sync(kFull, !alive)) break;
+      tc_fence_after();
+      const uint32_t s_addr = tmem + lanes + D + (i & 1) * 64;
+      uint32_t s[2][32];
+      tc_ld32(s[0], s_addr);
+      tc_ld32(s[1], s_addr + 32);
+      tc_wait_ld();
+      const uint32_t valid[2] = {s_valid[(i % R) * 4], s_valid[(i % R) * 4 + 1]};
+      if ((c.tile + 1) * kTK > c.u.ctx || (valid[0] & valid[1]) != 0xffffffffu) {
+        const int at0 = c.tile * kTK - c.u.ctx;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int at = at0 + h * 32 + j;
+            const bool see = (at < 0 ? hi >= -c.u.ctx : at >= lo && at <= hi) && (valid[h] >> j & 1u);
+            if (!see) s[h][j] = 0xff800000u;
+          }
+      }
+      float most[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) most[j] = fmaxf(__uint_as_float(s[0][j]), __uint_as_float(s[1][j]));
+#pragma unroll
+      for (int j = 4; j < 32; ++j) most[j & 3] = fmaxf(most[j & 3], fmaxf(__uint_as_float(s[0][j]), __uint_as_float(s[1][j])));
+      const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+      // The reference moves where the maximum is 2^8 above it. Before a row's first token there is nothing to rescale.
+      float f = 1.f;
+      if (m == -INFINITY) {
+        m = top;
+      } else if ((top - m) * P.scale_log2 > 8.f) {
+        f = factor(m, top, P.scale_log2);
+        m = top;
+        l *= f;
+      }
+      // The last tile's P V: every phase is waited for in turn, so that its parity tells which one has ended.
+      alive = i < 1 || wait(bars.o_done, (i - 1) & 1);
+      if (__any_sync(kFull, !alive)) break;
+      if (__any_sync(kFull, f != 1.f)) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int d = 0; d < D; d += 16) {
+          uint32_t o[16];
+          asm volatile(
+              "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+              : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]), "=r"(o[8]),
+                "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+              : "r"(tmem + lanes + d));
+          tc_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+          tc_st16(tmem + lanes + d, o);
+        }
+        tc_wait_st();
+      }
+      const float off = m == -INFINITY ? 0.f : __fmul_rn(m, P.scale_log2);
+      const f2_t sl = f2_splat(P.scale_log2), neg = f2_splat(-off);
+      f2_t sum = 0ull;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t p[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const f2_t e = f2_ex2(f2_fma(f2_pack(__uint_as_float(s[h][2 * j]), __uint_as_float(s[h][2 * j + 1])), sl, neg));
+          sum = f2_add(sum, e);
+          float a, b;
+          f2_unpack(e, a, b);
+          p[j] = pack_bf16(a, b);
+        }
+        tc_st16(s_addr + h * 16, p);
+      }
+      float sa, sb;
+      f2_unpack(sum, sa, sb);
+      l += sa + sb;
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(smem_addr(&bars.p_ready[i & 1]));
+
+      const bool unit_end = c.tile + 1 == c.u.tiles;
+      if (unit_end || i + 1 == n_tiles) {
+        if (tid == 0 && i + 1 == n_tiles) tell_cut(L, sh, c, !unit_end && from_start);
+        alive = wait(bars.o_done, i & 1);
+        if (__any_sync(kFull, !alive)) break;
+        tc_fence_after();
+        const bool split = !from_start || !unit_end;
+        float* part = reinterpret_cast<float*>(L.part + (size_t)(blockIdx.x * 2 + (from_start ? 1 : 0)) * part_bytes<D, 128>());
+        const int w = row / P.group, h = c.u.head * P.group + (row - w * P.group);
+        char* dst = P.out + (long long)(c.u.w.r0 + w) * P.out_row_b + (long long)h * (D * 2);
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          uint32_t o[32];
+          tc_ld32(o, tmem + lanes + d);
+          tc_wait_ld();
+          if (split) {
+            uint4* to = reinterpret_cast<uint4*>(part + tid * D + d);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) to[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          } else if (row < rows) {
+            uint4* to = reinterpret_cast<uint4*>(dst + d * 2);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                v[e] = pack_bf16(__uint_as_float(o[8 * j + 2 * e]) * inv, __uint_as_float(o[8 * j + 2 * e + 1]) * inv);
+              to[j] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+          }
+        }
+        if (split) {
+          part[128 * D + tid] = m;
+          part[128 * D + 128 + tid] = l;
+        } else if (row < rows && P.lse) {
+          P.lse[(long long)(c.u.w.r0 + w) * (P.C.n_heads * P.group) + h] = lse_of(m, l, P.scale_log2);
+        }
+        tc_fence_before();
+        mbar_arrive(smem_addr(&bars.o_free));
+      }
+      if (++c.tile == c.u.tiles && i + 1 < n_tiles) next_unit<128>(P, c);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == Sh::kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Sh::kCols) : "memory");
+}
+
+// ---------------------------------------------------------------------------
 // fp32: the same shares, on the fp32 pipes
 // ---------------------------------------------------------------------------
 template <int D, int MT>
@@ -872,6 +1326,18 @@ cudaError_t launch_mma(const Params& P, const Plan& L, cudaStream_t st) {
   return e == cudaSuccess ? launch_join<1, D, Sh::MT>(P, L, grid, st) : e;
 }
 
+template <int D>
+cudaError_t launch_tc(const Params& P, const Plan& L, cudaStream_t st) {
+  using Sh = TcShape<D>;
+  static_assert(Sh::kCtas * Sh::MT <= 256, "the workspace has room for the partial results");
+  cudaError_t e = cudaFuncSetAttribute(window_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::smem);
+  if (e != cudaSuccess) return e;
+  const int grid = 152 * Sh::kCtas;
+  window_tc_kernel<D><<<grid, Sh::kT, Sh::smem, st>>>(P, L);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? launch_join<1, D, Sh::MT>(P, L, grid, st) : e;
+}
+
 template <int D, int MT>
 cudaError_t launch_fma(const Params& P, const Plan& L, cudaStream_t st) {
   using Sh = Shape32<D, MT>;
@@ -946,12 +1412,12 @@ sv_status sv_window_attention(const void* q, int64_t q_stride, int32_t n_q_heads
       e = rows <= 16   ? att::launch_mma<128, 1>(P, L, st)
           : rows <= 32 ? att::launch_mma<128, 2>(P, L, st)
           : rows <= 64 ? att::launch_mma<128, 4>(P, L, st)
-                       : att::launch_mma<128, 8>(P, L, st);
+                       : att::launch_tc<128>(P, L, st);
     else
       e = rows <= 16   ? att::launch_mma<64, 1>(P, L, st)
           : rows <= 32 ? att::launch_mma<64, 2>(P, L, st)
           : rows <= 64 ? att::launch_mma<64, 4>(P, L, st)
-                       : att::launch_mma<64, 8>(P, L, st);
+                       : att::launch_tc<64>(P, L, st);
   } else if (D == 128) {
     e = rows <= 4 ? att::launch_fma<128, 4>(P, L, st) : att::launch_fma<128, 16>(P, L, st);
   } else {

@@ -219,6 +219,18 @@ def test_many_requests(cuda_lib, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_short_units_of_high_tiles(cuda_lib, D):
+    """Many stacked rows over few tokens: units of one or two key tiles, several to a share, some longer ones between them."""
+    gen = torch.Generator().manual_seed(10)
+    ctx = torch.randint(0, 100, (260,), generator=gen).tolist()
+    ctx[100], ctx[101], ctx[200] = 700, 0, 400
+    lens = [[int(x)] if x < 9 else [3, int(x)] for x in torch.randint(1, 12, (260,), generator=gen)]
+    lens[7] = []
+    Case(ctx, lens, 64, 4, D, 16, BF, seed=10).check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_single_tokens(cuda_lib, dtype):
     """cu_draft None: one row a sequence, as with offsets of zeros."""
