@@ -548,28 +548,34 @@ __global__ void __launch_bounds__(Shape<D, WM>::kT, Shape<D, WM>::kCtas) window_
 // ---------------------------------------------------------------------------
 // S = Q K^T and O += P V by tcgen05.mma with S, P and O in tensor memory.
 // Three roles, joined by mbarriers only:
-//   warps 0 - 3  softmax and output: a thread owns a row (a TMEM lane). The
-//                reference maximum moves only when a row's maximum outgrows it
-//                by 2^8, since moving it means rescaling O in TMEM;
-//   2 or 4 more  copies: Q tiles (two buffers), then K and V tiles gathered
+//   G groups of 4 warps   softmax and output: group i % G takes tile i, with
+//                an O of its own (a tile's softmax is a chain of about 1500
+//                cycles: two at a time on an SM). A thread owns a row (a TMEM lane). The reference
+//                maximum moves only when a row's maximum outgrows it by 2^8,
+//                since moving it means rescaling O in TMEM. At a unit's end
+//                the group of its last tile joins the groups' O;
+//   4 warps      copies: Q tiles (two buffers), then K and V tiles gathered
 //                over the pages into a ring of swizzled stages;
-//   the last     one thread issues the products: S of tile i, then P V of tile
-//                i - 1, so that the softmax of a tile runs beside the next S.
+//   the last     issues the products: S of tile i, then P V of tile i - 1
+//                (two S tiles).
 // Every wait is bounded: where one gives up the CTA sets SV_DEV_COPY_TIMEOUT,
 // lets its copies and products end, frees its tensor memory and leaves.
 template <int D>
 struct TcShape {
   static constexpr int MT = 128;
+  static constexpr int G = D == 64 ? 1 : 2;         // softmax groups
+  static constexpr int NB = 2;                      // S tiles
   static constexpr int kCopy = D == 64 ? 64 : 128;  // threads that copy
-  static constexpr int kT = 128 + kCopy + 32;
-  static constexpr int kMmaWarp = 4 + kCopy / 32;
-  static constexpr int kCtas = D == 64 ? 2 : 1;   // an SM
+  static constexpr int kMmaWarp = G * 4 + kCopy / 32;
+  static constexpr int kT = (kMmaWarp + 1) * 32;
+  static constexpr int kCtas = D == 64 ? 2 : 1;     // an SM
   static constexpr int kStages = 4;
-  static constexpr int kRing = kStages + 2;        // tiles whose page lookups are kept
-  static constexpr int kTile = kTK * D * 2;        // bytes of K (or V) of a tile
-  static constexpr int kQ = MT * D * 2;            // bytes of a Q tile
+  static constexpr int kRing = kStages + 2;         // tiles whose page lookups are kept
+  static constexpr int kTile = kTK * D * 2;         // bytes of K (or V) of a tile
+  static constexpr int kQ = MT * D * 2;             // bytes of a Q tile
   static constexpr size_t smem = 1024 + 2 * kQ + (size_t)kStages * 2 * kTile + kRing * (kTK * 8 + 16);
-  static constexpr int kCols = 256;                // TMEM columns: O (D), then two S tiles (64 each, P in their first half)
+  static constexpr int kCols = 512 / kCtas;         // TMEM columns: G times O (D), then the S tiles (64 each, P in their first half)
+  static_assert(G * D + NB * kTK <= kCols && kStages > NB && NB >= G && NB % G == 0, "");
 };
 
 __device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lead_bytes) {
@@ -591,6 +597,14 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
+// One lane of the (whole, converged) warp. The products' warp runs its loop
+// as a whole and only issues under this, so that the instructions' operands
+// stay uniform: issued from a lane's own branch each took about 90 cycles.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+  return is != 0;
+}
 // Arrives on the mbarrier when the products issued before have ended.
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -609,15 +623,12 @@ __device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
-__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tc_ld16(uint32_t (&r)[16], uint32_t addr) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
-      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
-      "r"(r[31])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
 }
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -645,22 +656,35 @@ __device__ __forceinline__ void cp_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
+  for (int it = 0; it < kSpinLimit; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+  }
+  *abort_flag = 1;
+  set_status(status, SV_DEV_COPY_TIMEOUT);
+  return false;
+}
+
+template <int S, int G, int NB>
 struct TcBars {
-  uint64_t full[4], empty[4];  // a stage's tile has landed; its P V has ended
-  uint64_t s_full[2];          // S has been computed
-  uint64_t p_ready[2];         // S has been read, P written, O rescaled
+  uint64_t full[S], empty[S];  // a stage's tile has landed; its P V has ended
+  uint64_t s_full[NB];         // S has been computed
+  uint64_t p_ready[NB];        // S has been read, P written, O rescaled
+  uint64_t o_done[G];          // a tile's P V has ended
+  uint64_t ml[G];              // a group's maxima and sums of a unit are in shared memory
   uint64_t q_full[2], q_empty[2];
-  uint64_t o_done;             // a tile's P V has ended
-  uint64_t o_free;             // a unit's O has been read
+  uint64_t o_free;             // a unit's O have been read
   uint64_t end;                // every product has ended
 };
 
 template <int D>
 __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_kernel(Params P, Plan L) {
   using Sh = TcShape<D>;
-  constexpr int S = Sh::kStages, R = Sh::kRing, CH = D / 64;  // CH: chunks of 64 elements (128 bytes) of a row
+  constexpr int S = Sh::kStages, R = Sh::kRing, G = Sh::G, NB = Sh::NB;
   extern __shared__ char smem_raw[];
-  __shared__ TcBars bars;
+  __shared__ TcBars<S, G, NB> bars;
+  __shared__ float2 s_ml[G][128];  // a group's (maximum, sum) of a row, at a unit's end
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -679,13 +703,18 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
       mbar_init(smem_addr(&bars.full[i]), Sh::kCopy + 1);
       mbar_init(smem_addr(&bars.empty[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NB; ++i) {
       mbar_init(smem_addr(&bars.s_full[i]), 1);
       mbar_init(smem_addr(&bars.p_ready[i]), 128);
+    }
+    for (int i = 0; i < G; ++i) {
+      mbar_init(smem_addr(&bars.o_done[i]), 1);
+      mbar_init(smem_addr(&bars.ml[i]), 128);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&bars.q_full[i]), Sh::kCopy);
       mbar_init(smem_addr(&bars.q_empty[i]), 1);
     }
-    mbar_init(smem_addr(&bars.o_done), 1);
     mbar_init(smem_addr(&bars.o_free), 128);
     mbar_init(smem_addr(&bars.end), 1);
     s_abort = 0;
@@ -700,22 +729,14 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  volatile int* abort_flag = &s_abort;
-  // Waits for a phase; false once any wait of the CTA has given up.
+  // Waits for a phase; false once any wait of the CTA has given up. The first try is all that a phase that has ended costs.
   auto wait = [&](uint64_t& bar, int parity) {
-    const uint32_t a = smem_addr(&bar);
-    for (int it = 0; it < kSpinLimit; ++it) {
-      if (mbar_try_wait(a, (uint32_t)parity)) return true;
-      if (*abort_flag) return false;
-    }
-    *abort_flag = 1;
-    set_status(P.status, SV_DEV_COPY_TIMEOUT);
-    return false;
+    return mbar_try_wait(smem_addr(&bar), (uint32_t)parity) || wait_long(smem_addr(&bar), (uint32_t)parity, &s_abort, P.status);
   };
-
-  if (warp >= 4 && warp < Sh::kMmaWarp) {
+  const uint32_t s_col = tmem + G * D;  // the first S
+  if (warp >= G * 4 && warp < Sh::kMmaWarp) {
     // ---------------------------------------------------------------- copies
-    const int t = tid - 128;
+    const int t = tid - G * 128;
     int page = -2, place = 0;
     static_assert(Sh::kCopy >= kTK, "a copying thread looks up a token at most");
     Cursor ld = c;        // the tile whose lookup is in the registers
@@ -730,7 +751,8 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
         page = P.S.table[(long long)ld.u.b * P.S.stride + slot];
       }
     };
-    auto store_lookup = [&](int ring) {
+    auto store_lookup = [&](int ring, bool end) {
+      if (t == 0) s_valid[ring * 4 + 2] = ld.tile + 1 == ld.u.tiles || end;  // the unit's last tile here
       if (t < kTK) {
         const bool ok = page >= 0 && page < P.C.n_pages;
         if (!ok && page != -2) set_status(P.status, SV_DATA_BAD_PAGE);
@@ -740,7 +762,7 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
       }
     };
     lookup();
-    store_lookup(0);
+    store_lookup(0, n_tiles == 1);
     if (n_tiles > 1) {
       if (++ld.tile == ld.u.tiles) next_unit<128>(P, ld);
       lookup();
@@ -791,7 +813,7 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
         if (t == 0) mbar_arrive(smem_addr(&bars.full[i % S]));  // releases the tile's s_valid, written before the last barrier
       }
       if (i + 1 < n_tiles) {
-        store_lookup((i + 1) % R);
+        store_lookup((i + 1) % R, i + 2 == n_tiles);
         if (i + 2 < n_tiles) {
           if (++ld.tile == ld.u.tiles) next_unit<128>(P, ld);
           lookup();
@@ -802,190 +824,243 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == Sh::kMmaWarp) {
     // -------------------------------------------------------------- products
-    if (lane == 0) {
-      bool alive = true;
-      int unit = -1;                      // of the S being issued
-      int pv_unit = 0;                    // of the P V being issued
-      bool pv_first = true;
-      auto issue_pv = [&](int i) {
-        alive = alive && wait(bars.p_ready[i & 1], (i >> 1) & 1);
-        if (alive && pv_first && pv_unit > 0) alive = wait(bars.o_free, (pv_unit - 1) & 1);
-        if (!alive) return;
-        tc_fence_after();
-        const uint32_t vb = kv_base + (i % S) * 2 * Sh::kTile + Sh::kTile, pa = tmem + D + (i & 1) * 64;
+    // What a tile needs to know of its unit is whether it ends it, which the copies left beside its lookups: this warp's steps are
+    // the chain that bounds short tiles, and a cursor of its own cost as much as the issue itself.
+    bool alive = true, first = true;       // the tile begins its unit
+    int unit = 0, pv_unit = 0;             // of the S being issued, of the P V
+    uint32_t begun = 0;                    // groups that have an O of that unit
+    uint32_t ends = 0;                     // of the tiles between their S and their P V: bit k of the tile k behind
+    const uint64_t q_desc = umma_desc(q_base, 16), k_desc = umma_desc(kv_base, 16), v_desc = umma_desc(kv_base + Sh::kTile, kTK * 128);
+    auto wait_all = [&](uint64_t& bar, int parity) { return __all_sync(kFull, wait(bar, parity)) != 0; };
+    auto issue_pv = [&](int i, bool end) {
+      const int g = i % G;
+      alive = alive && wait_all(bars.p_ready[i % NB], (i / NB) & 1);
+      if (alive && !begun && pv_unit > 0) alive = wait_all(bars.o_free, (pv_unit - 1) & 1);
+      if (!alive) return;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t vd = v_desc + (uint64_t)((i % S) * 2 * Sh::kTile / 16);
+        const bool add = begun >> g & 1u;
 #pragma unroll
         for (int k = 0; k < kTK / 16; ++k)
-          umma_ts(tmem, pa + k * 8, umma_desc(vb + k * 2048, kTK * 128), umma_idesc(D, true), !(pv_first && k == 0));
+          umma_ts(tmem + g * D, s_col + i % NB * kTK + k * 8, vd + k * (2048 / 16), umma_idesc(D, true), k > 0 || add);
         umma_commit(smem_addr(&bars.empty[i % S]));
-        umma_commit(smem_addr(&bars.o_done));
-      };
-      bool prev_last = false;  // tile i - 1 ends its unit
-      for (int i = 0; i < n_tiles && alive; ++i) {
-        if (i == 0 || c.tile == 0) {
-          ++unit;
-          alive = wait(bars.q_full[unit & 1], (unit >> 1) & 1);
-        }
-        alive = alive && wait(bars.full[i % S], (i / S) & 1);
-        if (!alive) break;
-        fence_proxy_async_smem();  // the copies wrote the tile through the generic proxy, the products read it through the other
-        tc_fence_after();
-        const uint32_t qb = q_base + (unit & 1) * Sh::kQ, kb = kv_base + (i % S) * 2 * Sh::kTile;
+        umma_commit(smem_addr(&bars.o_done[g]));
+      }
+      begun = end ? 0u : begun | 1u << g;
+      pv_unit += end;
+    };
+    for (int i = 0; i < n_tiles && alive; ++i) {
+      if (first) alive = wait_all(bars.q_full[unit & 1], (unit >> 1) & 1);
+      alive = alive && wait_all(bars.full[i % S], (i / S) & 1);
+      if (!alive) break;
+      const bool last = s_valid[(i % R) * 4 + 2] != 0;
+      fence_proxy_async_smem();  // the copies wrote the tile through the generic proxy, the products read it through the other
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t qd = q_desc + (uint64_t)((unit & 1) * Sh::kQ / 16), kd = k_desc + (uint64_t)((i % S) * 2 * Sh::kTile / 16);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          umma_ss(tmem + D + (i & 1) * 64, umma_desc(qb + (k >> 2) * (128 * 128) + (k & 3) * 32, 16),
-                  umma_desc(kb + (k >> 2) * (kTK * 128) + (k & 3) * 32, 16), umma_idesc(kTK, false), k > 0);
-        umma_commit(smem_addr(&bars.s_full[i & 1]));
-        const bool last = c.tile + 1 == c.u.tiles || i + 1 == n_tiles;
+          umma_ss(s_col + i % NB * kTK, qd + ((k >> 2) * (128 * 128) + (k & 3) * 32) / 16, kd + ((k >> 2) * (kTK * 128) + (k & 3) * 32) / 16,
+                  umma_idesc(kTK, false), k > 0);
+        umma_commit(smem_addr(&bars.s_full[i % NB]));
         if (last) umma_commit(smem_addr(&bars.q_empty[unit & 1]));
-        if (i > 0) {
-          issue_pv(i - 1);
-          pv_first = prev_last;
-          pv_unit += prev_last;
-        }
-        prev_last = last;
-        if (++c.tile == c.u.tiles && i + 1 < n_tiles) next_unit<128>(P, c);
       }
-      if (alive) issue_pv(n_tiles - 1);
-      umma_commit(smem_addr(&bars.end));
-      for (int it = 0; it < kSpinLimit && !mbar_try_wait(smem_addr(&bars.end), 0); ++it) {
-      }
+      ends = ends << 1 | (uint32_t)last;
+      first = last;
+      unit += last;
+      if (i >= NB - 1) issue_pv(i - (NB - 1), ends >> (NB - 1) & 1u);
     }
+    for (int i = max(0, n_tiles - (NB - 1)); i < n_tiles && alive; ++i) issue_pv(i, ends >> (n_tiles - 1 - i) & 1u);
+    if (elect_one()) umma_commit(smem_addr(&bars.end));
     __syncwarp();
+    for (int it = 0; it < kSpinLimit && !__all_sync(kFull, mbar_try_wait(smem_addr(&bars.end), 0)); ++it) {
+    }
   } else {
     // --------------------------------------------------- softmax and output
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    bool alive = true, from_start = false;
+    const int g = warp >> 2, r = tid & 127;  // the group, the row
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, o_addr = tmem + lanes + g * D;
+    int unit_begin = 0, parts[G];            // the unit's first tile; units in which each group had one
+#pragma unroll
+    for (int k = 0; k < G; ++k) parts[k] = 0;
+    bool from_start = c.tile == 0, fresh = true;
     int lo = 0, hi = 0;
     float m = -INFINITY, l = 0.f;
     for (int i = 0; i < n_tiles; ++i) {
+      const int rows = c.u.w.rows * P.group, row = c.u.mt * 128 + r;
+      const bool last = c.tile + 1 == c.u.tiles || i + 1 == n_tiles;  // of the unit, here
       if (i + 1 == n_tiles) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-      const int rows = c.u.w.rows * P.group, row = c.u.mt * 128 + tid;
-      if (i == 0 || c.tile == 0) {
-        from_start = c.tile == 0;
-        const int w = row < rows ? row / P.group : 0;
-        lo = row < rows ? candidate_start(P, c.u.w, w) : 0;
-        hi = row < rows ? w : -1 - c.u.ctx;  // rows past the window see nothing
-        m = -INFINITY;
-        l = 0.f;
-      }
-      alive = wait(bars.full[i % S], (i / S) & 1) && wait(bars.s_full[i & 1], (i >> 1) & 1);
-      if (__any_sync(kFull, !alive)) break;
-      tc_fence_after();
-      const uint32_t s_addr = tmem + lanes + D + (i & 1) * 64;
-      uint32_t s[2][32];
-      tc_ld32(s[0], s_addr);
-      tc_ld32(s[1], s_addr + 32);
-      tc_wait_ld();
-      const uint32_t valid[2] = {s_valid[(i % R) * 4], s_valid[(i % R) * 4 + 1]};
-      if ((c.tile + 1) * kTK > c.u.ctx || (valid[0] & valid[1]) != 0xffffffffu) {
-        const int at0 = c.tile * kTK - c.u.ctx;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int at = at0 + h * 32 + j;
-            const bool see = (at < 0 ? hi >= -c.u.ctx : at >= lo && at <= hi) && (valid[h] >> j & 1u);
-            if (!see) s[h][j] = 0xff800000u;
-          }
-      }
-      float most[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) most[j] = fmaxf(__uint_as_float(s[0][j]), __uint_as_float(s[1][j]));
-#pragma unroll
-      for (int j = 4; j < 32; ++j) most[j & 3] = fmaxf(most[j & 3], fmaxf(__uint_as_float(s[0][j]), __uint_as_float(s[1][j])));
-      const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-      // The reference moves where the maximum is 2^8 above it. Before a row's first token there is nothing to rescale.
-      float f = 1.f;
-      if (m == -INFINITY) {
-        m = top;
-      } else if ((top - m) * P.scale_log2 > 8.f) {
-        f = factor(m, top, P.scale_log2);
-        m = top;
-        l *= f;
-      }
-      // The last tile's P V: every phase is waited for in turn, so that its parity tells which one has ended.
-      alive = i < 1 || wait(bars.o_done, (i - 1) & 1);
-      if (__any_sync(kFull, !alive)) break;
-      if (__any_sync(kFull, f != 1.f)) {
-        tc_fence_after();
-#pragma unroll 1
-        for (int d = 0; d < D; d += 16) {
-          uint32_t o[16];
-          asm volatile(
-              "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-              : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]), "=r"(o[8]),
-                "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-              : "r"(tmem + lanes + d));
-          tc_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-          tc_st16(tmem + lanes + d, o);
+      if (i % G == g) {
+        if (fresh) {
+          fresh = false;
+          const int w = row < rows ? row / P.group : 0;
+          lo = row < rows ? candidate_start(P, c.u.w, w) : 0;
+          hi = row < rows ? w : -1 - c.u.ctx;  // rows past the window see nothing
+          m = -INFINITY;
+          l = 0.f;
         }
-        tc_wait_st();
-      }
-      const float off = m == -INFINITY ? 0.f : __fmul_rn(m, P.scale_log2);
-      const f2_t sl = f2_splat(P.scale_log2), neg = f2_splat(-off);
-      f2_t sum = 0ull;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t p[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const f2_t e = f2_ex2(f2_fma(f2_pack(__uint_as_float(s[h][2 * j]), __uint_as_float(s[h][2 * j + 1])), sl, neg));
-          sum = f2_add(sum, e);
-          float a, b;
-          f2_unpack(e, a, b);
-          p[j] = pack_bf16(a, b);
-        }
-        tc_st16(s_addr + h * 16, p);
-      }
-      float sa, sb;
-      f2_unpack(sum, sa, sb);
-      l += sa + sb;
-      tc_wait_st();
-      tc_fence_before();
-      mbar_arrive(smem_addr(&bars.p_ready[i & 1]));
-
-      const bool unit_end = c.tile + 1 == c.u.tiles;
-      if (unit_end || i + 1 == n_tiles) {
-        if (tid == 0 && i + 1 == n_tiles) tell_cut(L, sh, c, !unit_end && from_start);
-        alive = wait(bars.o_done, i & 1);
-        if (__any_sync(kFull, !alive)) break;
+        const uint32_t s_addr = s_col + lanes + i % NB * kTK;
+        const bool ok = wait(bars.full[i % S], (i / S) & 1) && wait(bars.s_full[i % NB], (i / NB) & 1);
+        if (__any_sync(kFull, !ok)) break;
         tc_fence_after();
-        const bool split = !from_start || !unit_end;
-        float* part = reinterpret_cast<float*>(L.part + (size_t)(blockIdx.x * 2 + (from_start ? 1 : 0)) * part_bytes<D, 128>());
-        const int w = row / P.group, h = c.u.head * P.group + (row - w * P.group);
-        char* dst = P.out + (long long)(c.u.w.r0 + w) * P.out_row_b + (long long)h * (D * 2);
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll 1
-        for (int d = 0; d < D; d += 32) {
-          uint32_t o[32];
-          tc_ld32(o, tmem + lanes + d);
+        const uint32_t valid[2] = {s_valid[(i % R) * 4], s_valid[(i % R) * 4 + 1]};
+        const bool masked = (c.tile + 1) * kTK > c.u.ctx || (valid[0] & valid[1]) != 0xffffffffu;
+        uint32_t s[32];
+        // Hidden tokens: behind the history all but the row's part of the window, and those without a page.
+        auto load = [&](int h) {
+          tc_ld32(s, s_addr + h * 32);
           tc_wait_ld();
-          if (split) {
-            uint4* to = reinterpret_cast<uint4*>(part + tid * D + d);
+          if (masked) {
+            const int at0 = c.tile * kTK - c.u.ctx + h * 32;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) to[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-          } else if (row < rows) {
-            uint4* to = reinterpret_cast<uint4*>(dst + d * 2);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t v[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                v[e] = pack_bf16(__uint_as_float(o[8 * j + 2 * e]) * inv, __uint_as_float(o[8 * j + 2 * e + 1]) * inv);
-              to[j] = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int j = 0; j < 32; ++j) {
+              const int at = at0 + j;
+              const bool see = (at < 0 ? hi >= -c.u.ctx : at >= lo && at <= hi) && (valid[h] >> j & 1u);
+              if (!see) s[j] = 0xff800000u;
             }
           }
+        };
+        float top = -INFINITY;
+#pragma unroll
+        for (int h = 1; h >= 0; --h) {
+          load(h);
+          float most[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) most[j] = fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 4]));
+#pragma unroll
+          for (int j = 8; j < 32; ++j) most[j & 3] = fmaxf(most[j & 3], __uint_as_float(s[j]));
+          top = fmaxf(top, fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])));
         }
-        if (split) {
-          part[128 * D + tid] = m;
-          part[128 * D + 128 + tid] = l;
-        } else if (row < rows && P.lse) {
-          P.lse[(long long)(c.u.w.r0 + w) * (P.C.n_heads * P.group) + h] = lse_of(m, l, P.scale_log2);
+        // The reference moves where the maximum is 2^8 above it. Before a row's first token there is nothing to rescale.
+        float f = 1.f;
+        if (m == -INFINITY) {
+          m = top;
+        } else if ((top - m) * P.scale_log2 > 8.f) {
+          f = factor(m, top, P.scale_log2);
+          m = top;
+          l *= f;
         }
+        // The group's last P V: every phase is waited for in turn, so that its parity tells which one has ended.
+        const bool done = i < G || wait(bars.o_done[g], (i / G - 1) & 1);
+        if (__any_sync(kFull, !done)) break;
+        const float off = m == -INFINITY ? 0.f : __fmul_rn(m, P.scale_log2);
+        const f2_t sl = f2_splat(P.scale_log2), neg = f2_splat(-off);
+        f2_t sum = 0ull;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h) load(h);
+          uint32_t p[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const f2_t e = f2_ex2(f2_fma(f2_pack(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), sl, neg));
+            sum = f2_add(sum, e);
+            float a, b;
+            f2_unpack(e, a, b);
+            p[j] = pack_bf16(a, b);
+          }
+          tc_st16(s_addr + h * 16, p);
+        }
+        float sa, sb;
+        f2_unpack(sum, sa, sb);
+        l += sa + sb;
+        if (__any_sync(kFull, f != 1.f)) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int d = 0; d < D; d += 16) {
+            uint32_t o[16];
+            tc_ld16(o, o_addr + d);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tc_st16(o_addr + d, o);
+          }
+        }
+        tc_wait_st();
         tc_fence_before();
-        mbar_arrive(smem_addr(&bars.o_free));
+        mbar_arrive(smem_addr(&bars.p_ready[i % NB]));
+      }
+      if (last) {
+        // The groups with a tile of this unit; the last of each hands its maxima and sums to the group of the unit's last tile.
+        const int count = i + 1 - unit_begin, fin = i % G;
+        const int behind = (i - g + G * 2) % G;  // how far the group's last tile lies behind the unit's
+        bool ok = true;
+        if (behind < count) {
+          ok = wait(bars.o_done[g], ((i - behind) / G) & 1);
+          if (ok && g != fin) {
+            s_ml[g][r] = make_float2(m, l);
+            mbar_arrive(smem_addr(&bars.ml[g]));
+          }
+        }
+        if (__any_sync(kFull, !ok)) break;
+        if (g == fin) {
+          float mg[G], fg[G];
+          float top = m;
+#pragma unroll
+          for (int k = 0; k < G; ++k) {
+            mg[k] = -INFINITY;
+            if (k != g && (i - k + G * 2) % G < count) {
+              ok = ok && wait(bars.ml[k], parts[k] & 1);
+              if (ok) mg[k] = s_ml[k][r].x;
+            }
+            if (k == g) mg[k] = m;
+            top = fmaxf(top, mg[k]);
+          }
+          if (__any_sync(kFull, !ok)) break;
+          tc_fence_after();
+          float sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < G; ++k) {
+            fg[k] = factor(mg[k], top, P.scale_log2);
+            if (mg[k] > -INFINITY) sum += fg[k] * (k == g ? l : s_ml[k][r].y);
+          }
+          const bool unit_end = c.tile + 1 == c.u.tiles, split = !from_start || !unit_end;
+          if (r == 0 && i + 1 == n_tiles) tell_cut(L, sh, c, !unit_end && from_start);
+          float* part = reinterpret_cast<float*>(L.part + (size_t)(blockIdx.x * 2 + (from_start ? 1 : 0)) * part_bytes<D, 128>());
+          const int w = row / P.group, h = c.u.head * P.group + (row - w * P.group);
+          char* dst = P.out + (long long)(c.u.w.r0 + w) * P.out_row_b + (long long)h * (D * 2);
+          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll 1
+          for (int d = 0; d < D; d += 16) {
+            float o[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = 0.f;
+#pragma unroll
+            for (int k = 0; k < G; ++k) {
+              if ((i - k + G * 2) % G >= count) continue;  // the same for the whole CTA
+              uint32_t x[16];
+              tc_ld16(x, tmem + lanes + k * D + d);
+              tc_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = fmaf(__uint_as_float(x[j]), fg[k], o[j]);
+            }
+            if (split) {
+              float4* to = reinterpret_cast<float4*>(part + r * D + d);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) to[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            } else if (row < rows) {
+              uint4* to = reinterpret_cast<uint4*>(dst + d * 2);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                uint32_t v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = pack_bf16(o[8 * j + 2 * e] * inv, o[8 * j + 2 * e + 1] * inv);
+                to[j] = make_uint4(v[0], v[1], v[2], v[3]);
+              }
+            }
+          }
+          if (split) {
+            part[128 * D + r] = top;
+            part[128 * D + 128 + r] = sum;
+          } else if (row < rows && P.lse) {
+            P.lse[(long long)(c.u.w.r0 + w) * (P.C.n_heads * P.group) + h] = lse_of(top, sum, P.scale_log2);
+          }
+          tc_fence_before();
+          mbar_arrive(smem_addr(&bars.o_free));
+        }
+#pragma unroll
+        for (int k = 0; k < G; ++k) parts[k] += k != fin && (i - k + G * 2) % G < count;
+        unit_begin = i + 1;
+        fresh = from_start = true;
       }
       if (++c.tile == c.u.tiles && i + 1 < n_tiles) next_unit<128>(P, c);
     }
