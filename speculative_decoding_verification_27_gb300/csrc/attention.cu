@@ -76,23 +76,37 @@ __device__ __forceinline__ void load_request(const Params& P, int b, Unit& u, bo
   u.n_mt = (int)(((long long)u.w.rows * P.group + MT - 1) / MT);
 }
 
+// The list's tiles in `grid` shares: the first `more` of them hold size + 1, the others size.
 struct Share {
-  long long t0, t1, total;  // this CTA's tiles of the list
-  int grid;                 // CTAs that have a share
+  long long t0, t1;  // this CTA's tiles of the list
+  long long size;
+  int more;
 };
 struct Cursor {
   Unit u;
   int tile;
 };
 
+// n / d and the rest, in 32 bits where that is enough.
+__device__ __forceinline__ long long div_small(long long n, int d, int& rest) {
+  if (n >> 32 == 0) {
+    const uint32_t q = (uint32_t)n / (uint32_t)d;
+    rest = (int)((uint32_t)n - q * (uint32_t)d);
+    return q;
+  }
+  const long long q = n / d;
+  rest = (int)(n - q * d);
+  return q;
+}
+
 // This CTA's share, and a cursor on its first tile; false for a CTA without
 // one. Thread i sums the tiles of its run of requests; a scan over the threads
 // gives the list's length, and the thread whose run holds the share's first
-// tile walks it.
+// tile walks it and tells the others the request.
 template <int MT, int kThr>
 __device__ __forceinline__ bool take_share(const Params& P, const Plan& L, Share& sh, Cursor& c) {
   __shared__ long long s_scan[kThr / 32];
-  __shared__ int s_start;
+  __shared__ Unit s_unit;
   __shared__ long long s_first;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (P.S.n + kThr - 1) / kThr;
@@ -109,36 +123,36 @@ __device__ __forceinline__ bool take_share(const Params& P, const Plan& L, Share
   }
   if (lane == 31) s_scan[warp] = incl;
   __syncthreads();
-  sh.total = 0;
+  long long total = 0;
+#pragma unroll
   for (int w = 0; w < kThr / 32; ++w) {
     if (w < warp) incl += s_scan[w];
-    sh.total += s_scan[w];
+    total += s_scan[w];
   }
-  sh.grid = (int)min((long long)gridDim.x, sh.total);  // shares of a tile at least
-  if (blockIdx.x >= sh.grid) {
-    if (tid == 0) L.cut[blockIdx.x * 4] = -1;
+  const int grid = (int)min((long long)gridDim.x, total), id = blockIdx.x;  // shares of a tile at least
+  if (id >= grid) {
+    if (tid == 0) L.cut[id * 4] = -1;
     return false;
   }
-  sh.t0 = sh.total * blockIdx.x / sh.grid;
-  sh.t1 = sh.total * (blockIdx.x + 1) / sh.grid;
+  sh.size = div_small(total, grid, sh.more);
+  sh.t0 = sh.size * id + min(id, sh.more);
+  sh.t1 = sh.t0 + sh.size + (id < sh.more);
   if (sh.t0 >= incl - mine && sh.t0 < incl) {
     long long at = incl - mine;
-    int b = tid * per;
-    for (;; ++b) {
-      load_request<MT>(P, b, c.u, false);
-      const long long n = (long long)c.u.tiles * c.u.n_mt * P.C.n_heads;
-      if (sh.t0 < at + n) break;
-      at += n;
-    }
-    s_start = b;
+    if (per > 1)
+      for (int b = tid * per;; ++b) {
+        load_request<MT>(P, b, c.u, false);
+        const long long n = (long long)c.u.tiles * c.u.n_mt * P.C.n_heads;
+        if (sh.t0 < at + n) break;
+        at += n;
+      }
+    s_unit = c.u;
     s_first = sh.t0 - at;  // first tile of the share within its request
   }
   __syncthreads();
-  load_request<MT>(P, s_start, c.u, false);
-  const long long unit = s_first / c.u.tiles;
-  c.tile = (int)(s_first - unit * c.u.tiles);
-  c.u.head = (int)(unit / c.u.n_mt);
-  c.u.mt = (int)(unit - (long long)c.u.head * c.u.n_mt);
+  c.u = s_unit;
+  const long long unit = div_small(s_first, c.u.tiles, c.tile);
+  c.u.head = (int)div_small(unit, c.u.n_mt, c.u.mt);
   return true;
 }
 
@@ -160,8 +174,9 @@ __device__ __forceinline__ void next_unit(const Params& P, Cursor& c) {
 // end, if it began here, and the last CTA that has a part of it.
 __device__ __forceinline__ void tell_cut(const Plan& L, const Share& sh, const Cursor& c, bool cuts) {
   const long long last = sh.t1 - 1 + (c.u.tiles - 1 - c.tile);  // the unit's last tile in the list
-  *reinterpret_cast<int4*>(L.cut + blockIdx.x * 4) =
-      make_int4(cuts ? c.u.b : -1, c.u.head, c.u.mt, (int)(((last + 1) * sh.grid - 1) / sh.total));  // the largest share that begins by then
+  const long long front = (sh.size + 1) * sh.more;               // tiles of the larger shares
+  const long long k = last < front ? last / (sh.size + 1) : sh.more + (last - front) / sh.size;
+  *reinterpret_cast<int4*>(L.cut + blockIdx.x * 4) = make_int4(cuts ? c.u.b : -1, c.u.head, c.u.mt, (int)k);
 }
 
 // The first row of the candidate that window row w lies in.
@@ -1080,8 +1095,8 @@ struct Shape32 {
   static constexpr int kT = 128;
   static constexpr int kPitch = D * 4 + 16;        // bytes of a row in shared memory: rows of one column lie in different banks
   static constexpr int kTile = kTK * kPitch;
-  static constexpr int kStages = D == 64 ? 3 : 2;
-  static constexpr int kCtas = D == 64 ? 2 : 1;    // an SM
+  static constexpr int kStages = 2;
+  static constexpr int kCtas = D == 64 ? 3 : 1;    // an SM
   static constexpr int SP = kTK + 4;               // row pitch of the scores, in floats
   static constexpr size_t smem = (size_t)kStages * 2 * kTile + (size_t)MT * D * 4 + (size_t)MT * SP * 4 + MT * 16 + kStages * kTK * 8;
 };
@@ -1110,19 +1125,24 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
   const int key = tid % kTK, half = tid / kTK;
   const int d_own = tid % D, kh = tid / D;
 
-  // The offsets of the loading cursor's tile, and the tile itself.
+  // A token of the loading cursor's tile: its page, looked up a tile ahead of the copy.
+  int page = -2, place = 0;
+  auto lookup = [&]() {
+    const int t = ld.tile * kTK + tid;
+    page = -2;
+    if (tid < kTK && t < ld.u.keys) {
+      const int slot = page_slot(P.C, t);
+      place = t - slot * P.C.page_size;
+      page = P.S.table[(long long)ld.u.b * P.S.stride + slot];
+    }
+  };
+  lookup();
+  // The offsets of the loading cursor's tile, the tile itself, and the next one's lookup.
   auto load_tile = [&](int n) {
     if (tid < kTK) {
-      const int t = ld.tile * kTK + tid;
-      long long off = -1;
-      if (t < ld.u.keys) {
-        const int slot = page_slot(P.C, t), page = P.S.table[(long long)ld.u.b * P.S.stride + slot];
-        if (page >= 0 && page < P.C.n_pages)
-          off = page * P.C.page_b + (t - slot * P.C.page_size) * P.C.token_b + ld.u.head * P.C.head_b;
-        else
-          set_status(P.status, SV_DATA_BAD_PAGE);
-      }
-      s_off[n % S * kTK + tid] = off;
+      const bool ok = page >= 0 && page < P.C.n_pages;
+      if (!ok && page != -2) set_status(P.status, SV_DATA_BAD_PAGE);
+      s_off[n % S * kTK + tid] = ok ? page * P.C.page_b + place * P.C.token_b + ld.u.head * P.C.head_b : -1;
     }
     __syncthreads();
     const uint32_t base = smem_addr(s_kv) + (n % S) * 2 * Sh::kTile;
@@ -1134,7 +1154,10 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
       cp16(base + Sh::kTile + r * Sh::kPitch + c * 16, P.C.v + at, off >= 0);
     }
     cp_commit();
-    if (++ld.tile == ld.u.tiles && n + 1 < n_tiles) next_unit<MT>(P, ld);
+    if (n + 1 < n_tiles) {
+      if (++ld.tile == ld.u.tiles) next_unit<MT>(P, ld);
+      lookup();
+    }
   };
   for (int i = 0; i < S - 1; ++i) {
     if (i < n_tiles)
@@ -1153,15 +1176,19 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
       begun = true;
       from_start = cp.tile == 0;
       __syncthreads();
-      for (int x = tid; x < MT * D; x += 128) {
-        const int r = cp.u.mt * MT + x / D;
-        float v = 0.f;
-        if (r < rows) {
+      float4 qv[(MT * D / 4 + 127) / 128];
+#pragma unroll
+      for (int j = 0; j < (MT * D / 4 + 127) / 128; ++j) {
+        const int x = tid + j * 128, r = cp.u.mt * MT + x / (D / 4);
+        qv[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (x < MT * D / 4 && r < rows) {
           const int w = r / P.group, h = cp.u.head * P.group + (r - w * P.group);
-          v = __ldg(reinterpret_cast<const float*>(P.q + (long long)(cp.u.w.r0 + w) * P.q_row_b + (long long)h * (D * 4)) + x % D);
+          qv[j] = __ldg(reinterpret_cast<const float4*>(P.q + (long long)(cp.u.w.r0 + w) * P.q_row_b + (long long)h * (D * 4)) + x % (D / 4));
         }
-        s_q[x] = v;
       }
+#pragma unroll
+      for (int j = 0; j < (MT * D / 4 + 127) / 128; ++j)
+        if (tid + j * 128 < MT * D / 4) reinterpret_cast<float4*>(s_q)[tid + j * 128] = qv[j];
       if (tid < MT) {
         s_m[tid] = -INFINITY;
         s_l[tid] = 0.f;
@@ -1471,7 +1498,7 @@ sv_status sv_window_attention(const void* q, int64_t q_stride, int32_t n_q_heads
   L.cut = static_cast<int*>(workspace);
   L.part = static_cast<char*>(workspace) + att::kGrid * 16;
   // Row tiles as high as the windows' mean number of stacked rows.
-  const long long rows = ((long long)R + P.S.n - 1) / P.S.n * P.group;
+  const long long rows = ((long long)R * P.group + P.S.n - 1) / P.S.n;
   cudaError_t e;
   if (es == 2) {
     P.q_mask = 0xffffffffu;
@@ -1494,9 +1521,9 @@ sv_status sv_window_attention(const void* q, int64_t q_stride, int32_t n_q_heads
           : rows <= 64 ? att::launch_mma<64, 4>(P, L, st)
                        : att::launch_tc<64>(P, L, st);
   } else if (D == 128) {
-    e = rows <= 4 ? att::launch_fma<128, 4>(P, L, st) : att::launch_fma<128, 16>(P, L, st);
+    e = rows <= 4 ? att::launch_fma<128, 4>(P, L, st) : rows <= 8 ? att::launch_fma<128, 8>(P, L, st) : att::launch_fma<128, 16>(P, L, st);
   } else {
-    e = rows <= 4 ? att::launch_fma<64, 4>(P, L, st) : att::launch_fma<64, 16>(P, L, st);
+    e = rows <= 4 ? att::launch_fma<64, 4>(P, L, st) : rows <= 8 ? att::launch_fma<64, 8>(P, L, st) : att::launch_fma<64, 16>(P, L, st);
   }
   return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
