@@ -580,17 +580,17 @@ struct TcShape {
   static constexpr int MT = 128;
   static constexpr int G = D == 64 ? 1 : 2;         // softmax groups
   static constexpr int NB = 2;                      // S tiles
-  static constexpr int kCopy = D == 64 ? 64 : 128;  // threads that copy
-  static constexpr int kMmaWarp = G * 4 + kCopy / 32;
+  static constexpr int NW = D == 64 ? 2 : 4;        // warps that copy
+  static constexpr int kMmaWarp = G * 4 + NW;
   static constexpr int kT = (kMmaWarp + 1) * 32;
   static constexpr int kCtas = D == 64 ? 2 : 1;     // an SM
   static constexpr int kStages = 4;
   static constexpr int kRing = kStages + 2;         // tiles whose page lookups are kept
   static constexpr int kTile = kTK * D * 2;         // bytes of K (or V) of a tile
   static constexpr int kQ = MT * D * 2;             // bytes of a Q tile
-  static constexpr size_t smem = 1024 + 2 * kQ + (size_t)kStages * 2 * kTile + kRing * (kTK * 8 + 16);
+  static constexpr size_t smem = 1024 + 2 * kQ + (size_t)kStages * 2 * kTile;
   static constexpr int kCols = 512 / kCtas;         // TMEM columns: G times O (D), then the S tiles (64 each, P in their first half)
-  static_assert(G * D + NB * kTK <= kCols && kStages > NB && NB >= G && NB % G == 0, "");
+  static_assert(G * D + NB * kTK <= kCols && kStages > NB && NB >= G && NB % G == 0 && kStages % NW == 0, "");
 };
 
 __device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lead_bytes) {
@@ -653,19 +653,6 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) 
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// A barrier of the N copying threads; true where all of them are alive, so
-// that all of them go on or leave.
-template <int N>
-__device__ __forceinline__ bool copies_sync(bool alive) {
-  uint32_t all;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(all)
-      : "r"((uint32_t)alive), "n"(N)
-      : "memory");
-  return all != 0;
-}
 // Arrives on the mbarrier when this thread's copies so far have landed.
 __device__ __forceinline__ void cp_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -700,6 +687,8 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
   extern __shared__ char smem_raw[];
   __shared__ TcBars<S, G, NB> bars;
   __shared__ float2 s_ml[G][128];  // a group's (maximum, sum) of a row, at a unit's end
+  __shared__ long long s_off[Sh::NW][kTK];  // a copying warp's tile: the tokens' byte offsets
+  __shared__ uint32_t s_valid[R][4];        // a tile's tokens that have a page, and whether it is the unit's last here
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -711,11 +700,9 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
 
   char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const uint32_t q_base = smem_addr(smem), kv_base = q_base + 2 * Sh::kQ;
-  long long* s_off = reinterpret_cast<long long*>(smem + 2 * Sh::kQ + S * 2 * Sh::kTile);  // [R][kTK]
-  uint32_t* s_valid = reinterpret_cast<uint32_t*>(s_off + R * kTK);                        // [R][4]
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(smem_addr(&bars.full[i]), Sh::kCopy + 1);
+      mbar_init(smem_addr(&bars.full[i]), 32 + 1);
       mbar_init(smem_addr(&bars.empty[i]), 1);
     }
     for (int i = 0; i < NB; ++i) {
@@ -727,7 +714,7 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
       mbar_init(smem_addr(&bars.ml[i]), 128);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_addr(&bars.q_full[i]), Sh::kCopy);
+      mbar_init(smem_addr(&bars.q_full[i]), Sh::NW * 32);
       mbar_init(smem_addr(&bars.q_empty[i]), 1);
     }
     mbar_init(smem_addr(&bars.o_free), 128);
@@ -751,88 +738,108 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
   const uint32_t s_col = tmem + G * D;  // the first S
   if (warp >= G * 4 && warp < Sh::kMmaWarp) {
     // ---------------------------------------------------------------- copies
-    const int t = tid - G * 128;
-    int page = -2, place = 0;
-    static_assert(Sh::kCopy >= kTK, "a copying thread looks up a token at most");
-    Cursor ld = c;        // the tile whose lookup is in the registers
+    // Copying warp j takes every NW-th tile whole, with nothing shared between the warps but Q, of which each brings its rows.
+    const int j = warp - G * 4;
+    constexpr int NW = Sh::NW, CPR = D / 8, RPP = 32 / CPR;  // 16-byte chunks of a row; rows that a warp copies at once
+    const int ch = lane % CPR, r0 = lane / CPR;
+    const uint32_t to = (uint32_t)((ch >> 3) * (kTK * 128) + r0 * 128), x0 = (uint32_t)(((ch & 7) ^ r0) << 4);
+    const char* k_ch = P.C.k + ch * 16;
+    const long long v_k = P.C.v - P.C.k;
+    // The pages of the warp's next tile, two tokens a lane, looked up while the one before it is copied.
+    Cursor ld = c;
+    int ld_at = 0, page[2], place[2];
+    auto lookup = [&](int i) {
+      for (; ld_at < i; ++ld_at)
+        if (++ld.tile == ld.u.tiles) next_unit<128>(P, ld);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = ld.tile * kTK + h * 32 + lane;
+        page[h] = -2;
+        if (k < ld.u.keys) {
+          const int slot = page_slot(P.C, k);
+          place[h] = k - slot * P.C.page_size;
+          page[h] = P.S.table[(long long)ld.u.b * P.S.stride + slot];
+        }
+      }
+    };
+    if (j < n_tiles) lookup(j);
+    bool alive = true;
     int unit = 0;
-    auto lookup = [&]() {
-      const int k = ld.tile * kTK + t;
-      page = -2;
-      place = 0;
-      if (t < kTK && k < ld.u.keys) {
-        const int slot = page_slot(P.C, k);
-        place = k - slot * P.C.page_size;
-        page = P.S.table[(long long)ld.u.b * P.S.stride + slot];
-      }
-    };
-    auto store_lookup = [&](int ring, bool end) {
-      if (t == 0) s_valid[ring * 4 + 2] = ld.tile + 1 == ld.u.tiles || end;  // the unit's last tile here
-      if (t < kTK) {
-        const bool ok = page >= 0 && page < P.C.n_pages;
-        if (!ok && page != -2) set_status(P.status, SV_DATA_BAD_PAGE);
-        s_off[ring * kTK + t] = ok ? page * P.C.page_b + place * P.C.token_b + ld.u.head * P.C.head_b : -1;
-        const unsigned m = __ballot_sync(kFull, ok);
-        if (lane == 0) s_valid[ring * 4 + (t >> 5)] = m;
-      }
-    };
-    lookup();
-    store_lookup(0, n_tiles == 1);
-    if (n_tiles > 1) {
-      if (++ld.tile == ld.u.tiles) next_unit<128>(P, ld);
-      lookup();
-    }
-    for (int i = 0; i < n_tiles; ++i) {
-      bool alive = true;
-      const bool new_unit = i == 0 || c.tile == 0;
-      if (new_unit && unit >= 2) alive = wait(bars.q_empty[unit & 1], ((unit >> 1) - 1) & 1);
-      if (i >= S) alive = alive && wait(bars.empty[i % S], (i / S - 1) & 1);
-      if (!copies_sync<Sh::kCopy>(alive)) break;  // tile i's offsets are there, too
-      if (new_unit) {  // a unit's rows
-        const uint32_t qb = q_base + (unit & 1) * Sh::kQ;
-        const int rows = c.u.w.rows * P.group;
-        for (int x = t; x < 128 * (D / 8); x += Sh::kCopy) {
-          const int r = x / (D / 8), ch = x % (D / 8), row = c.u.mt * 128 + r;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (row < rows) {
-            const int w = row / P.group, h = row - w * P.group;
-            v = *reinterpret_cast<const uint4*>(P.q + (long long)(c.u.w.r0 + w) * P.q_row_b +
-                                                (long long)(c.u.head * P.group + h) * (D * 2) + ch * 16);
-            v.x = (v.x & P.q_mask) ^ P.q_sign;
-            v.y = (v.y & P.q_mask) ^ P.q_sign;
-            v.z = (v.z & P.q_mask) ^ P.q_sign;
-            v.w = (v.w & P.q_mask) ^ P.q_sign;
+    for (int i = 0; i < n_tiles && alive; ++i) {
+      if (i == 0 || c.tile == 0) {  // a unit's rows: this warp's 128 / NW of them
+        if (unit >= 2) alive = __all_sync(kFull, wait(bars.q_empty[unit & 1], ((unit >> 1) - 1) & 1));
+        if (!alive) break;
+        const uint32_t qb = q_base + (unit & 1) * Sh::kQ + (uint32_t)((ch >> 3) * (128 * 128));
+        const int rows = c.u.w.rows * P.group, first = j * (128 / NW) + r0;
+        int row = c.u.mt * 128 + first, w = row / P.group, h = row - w * P.group;
+        const char* q = P.q + (long long)c.u.w.r0 * P.q_row_b + (long long)c.u.head * P.group * (D * 2) + ch * 16;
+        constexpr int N = 128 / NW / RPP, U = 8;  // rows of a lane, of which U are in flight
+#pragma unroll 1
+        for (int n = 0; n < N; n += U) {
+          uint4 v[U];
+#pragma unroll
+          for (int e = 0; e < U; ++e) {
+            v[e] = row < rows ? *reinterpret_cast<const uint4*>(q + w * P.q_row_b + h * (D * 2)) : make_uint4(0u, 0u, 0u, 0u);
+            row += RPP;
+            h += RPP;
+            while (h >= P.group) {
+              h -= P.group;
+              ++w;
+            }
           }
-          const uint32_t a = qb + (ch >> 3) * (128 * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+#pragma unroll
+          for (int e = 0; e < U; ++e) {
+            const int r = first + (n + e) * RPP;
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(qb + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
+                         "r"((v[e].x & P.q_mask) ^ P.q_sign), "r"((v[e].y & P.q_mask) ^ P.q_sign),
+                         "r"((v[e].z & P.q_mask) ^ P.q_sign), "r"((v[e].w & P.q_mask) ^ P.q_sign)
+                         : "memory");
+          }
         }
         fence_proxy_async_smem();
         mbar_arrive(smem_addr(&bars.q_full[unit & 1]));
         ++unit;
       }
-      {
-        const uint32_t base = kv_base + (i % S) * 2 * Sh::kTile;
-        constexpr int CPR = D / 8, RPP = Sh::kCopy / CPR;
-        const int ch = t % CPR;
+      if (i % NW == j) {
+        if (i >= S) alive = __all_sync(kFull, wait(bars.empty[i % S], (i / S - 1) & 1));
+        if (!alive) break;
+        uint32_t valid[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bool ok = page[h] >= 0 && page[h] < P.C.n_pages;
+          if (!ok && page[h] != -2) set_status(P.status, SV_DATA_BAD_PAGE);
+          s_off[j][h * 32 + lane] = ok ? page[h] * P.C.page_b + place[h] * P.C.token_b + ld.u.head * P.C.head_b : -1;
+          valid[h] = __ballot_sync(kFull, ok);
+        }
+        if (lane == 0) {
+          s_valid[i % R][0] = valid[0];
+          s_valid[i % R][1] = valid[1];
+          s_valid[i % R][2] = ld.tile + 1 == ld.u.tiles || i + 1 == n_tiles;
+        }
+        if (i + NW < n_tiles) lookup(i + NW);
+        __syncwarp();
+        const uint32_t base = kv_base + (i % S) * 2 * Sh::kTile + to;
+        if ((valid[0] & valid[1]) == 0xffffffffu) {
 #pragma unroll 8
-        for (int j = 0; j < kTK / RPP; ++j) {
-          const int r = t / CPR + j * RPP;
-          const long long off = s_off[(i % R) * kTK + r];
-          const bool ok = off >= 0;
-          const long long at = (ok ? off : 0) + ch * 16;
-          const uint32_t dst = base + (ch >> 3) * (kTK * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-          cp16(dst, P.C.k + at, ok);
-          cp16(dst + Sh::kTile, P.C.v + at, ok);
+          for (int n = 0; n < kTK / RPP; ++n) {
+            const char* src = k_ch + s_off[j][n * RPP + r0];
+            const uint32_t dst = base + n * RPP * 128 + (x0 ^ ((n * RPP & 7) << 4));
+            cp16(dst, src, true);
+            cp16(dst + Sh::kTile, src + v_k, true);
+          }
+        } else {  // zeros where there is no page, and behind the sequence
+#pragma unroll 1
+          for (int n = 0; n < kTK / RPP; ++n) {
+            const long long off = s_off[j][n * RPP + r0];
+            const char* src = k_ch + (off < 0 ? 0 : off);
+            const uint32_t dst = base + n * RPP * 128 + (x0 ^ ((n * RPP & 7) << 4));
+            cp16(dst, src, off >= 0);
+            cp16(dst + Sh::kTile, src + v_k, off >= 0);
+          }
         }
         cp_arrive(smem_addr(&bars.full[i % S]));
-        if (t == 0) mbar_arrive(smem_addr(&bars.full[i % S]));  // releases the tile's s_valid, written before the last barrier
-      }
-      if (i + 1 < n_tiles) {
-        store_lookup((i + 1) % R, i + 2 == n_tiles);
-        if (i + 2 < n_tiles) {
-          if (++ld.tile == ld.u.tiles) next_unit<128>(P, ld);
-          lookup();
-        }
+        if (lane == 0) mbar_arrive(smem_addr(&bars.full[i % S]));  // releases what lane 0 wrote to s_valid
+        __syncwarp();
       }
       if (++c.tile == c.u.tiles && i + 1 < n_tiles) next_unit<128>(P, c);
     }
@@ -869,7 +876,7 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
       if (first) alive = wait_all(bars.q_full[unit & 1], (unit >> 1) & 1);
       alive = alive && wait_all(bars.full[i % S], (i / S) & 1);
       if (!alive) break;
-      const bool last = s_valid[(i % R) * 4 + 2] != 0;
+      const bool last = s_valid[i % R][2] != 0;
       fence_proxy_async_smem();  // the copies wrote the tile through the generic proxy, the products read it through the other
       tc_fence_after();
       if (elect_one()) {
@@ -918,21 +925,24 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
         const bool ok = wait(bars.full[i % S], (i / S) & 1) && wait(bars.s_full[i % NB], (i / NB) & 1);
         if (__any_sync(kFull, !ok)) break;
         tc_fence_after();
-        const uint32_t valid[2] = {s_valid[(i % R) * 4], s_valid[(i % R) * 4 + 1]};
-        const bool masked = (c.tile + 1) * kTK > c.u.ctx || (valid[0] & valid[1]) != 0xffffffffu;
+        // Hidden tokens: behind the history all but the row's part of the window, and those without a page. Bit k of `see` is
+        // token k of the tile.
+        uint64_t see = (uint64_t)s_valid[i % R][1] << 32 | s_valid[i % R][0];
+        const bool masked = (c.tile + 1) * kTK > c.u.ctx || see != ~0ull;
+        if (masked) {
+          const int at0 = c.tile * kTK - c.u.ctx;  // of the tile's first token in the window
+          auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; };
+          see &= hi < -c.u.ctx ? 0ull : below(-at0) | (below(hi + 1 - at0) & ~below(max(lo, 0) - at0));
+        }
         uint32_t s[32];
-        // Hidden tokens: behind the history all but the row's part of the window, and those without a page.
         auto load = [&](int h) {
           tc_ld32(s, s_addr + h * 32);
           tc_wait_ld();
           if (masked) {
-            const int at0 = c.tile * kTK - c.u.ctx + h * 32;
+            const uint32_t bits = (uint32_t)(see >> (h * 32));
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int at = at0 + j;
-              const bool see = (at < 0 ? hi >= -c.u.ctx : at >= lo && at <= hi) && (valid[h] >> j & 1u);
-              if (!see) s[j] = 0xff800000u;
-            }
+            for (int j = 0; j < 32; ++j)
+              if (!(bits & 1u << j)) s[j] = 0xff800000u;
           }
         };
         float top = -INFINITY;
