@@ -764,41 +764,55 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
     };
     if (j < n_tiles) lookup(j);
     bool alive = true;
-    int unit = 0;
-    for (int i = 0; i < n_tiles && alive; ++i) {
-      if (i == 0 || c.tile == 0) {  // a unit's rows: this warp's 128 / NW of them
-        if (unit >= 2) alive = __all_sync(kFull, wait(bars.q_empty[unit & 1], ((unit >> 1) - 1) & 1));
-        if (!alive) break;
-        const uint32_t qb = q_base + (unit & 1) * Sh::kQ + (uint32_t)((ch >> 3) * (128 * 128));
-        const int rows = c.u.w.rows * P.group, first = j * (128 / NW) + r0;
-        int row = c.u.mt * 128 + first, w = row / P.group, h = row - w * P.group;
-        const char* q = P.q + (long long)c.u.w.r0 * P.q_row_b + (long long)c.u.head * P.group * (D * 2) + ch * 16;
-        constexpr int N = 128 / NW / RPP, U = 8;  // rows of a lane, of which U are in flight
+    int unit = 0;  // units whose rows are loaded
+    // A unit's rows: this warp's 128 / NW of them.
+    auto load_q = [&](const Cursor& u) {
+      if (unit >= 2) alive = __all_sync(kFull, wait(bars.q_empty[unit & 1], ((unit >> 1) - 1) & 1));
+      if (!alive) return;
+      const uint32_t qb = q_base + (unit & 1) * Sh::kQ + (uint32_t)((ch >> 3) * (128 * 128));
+      const int rows = u.u.w.rows * P.group, first = j * (128 / NW) + r0;
+      int row = u.u.mt * 128 + first, w = row / P.group, h = row - w * P.group;
+      const char* q = P.q + (long long)u.u.w.r0 * P.q_row_b + (long long)u.u.head * P.group * (D * 2) + ch * 16;
+      constexpr int N = 128 / NW / RPP, U = 8;  // rows of a lane, of which U are in flight
 #pragma unroll 1
-        for (int n = 0; n < N; n += U) {
-          uint4 v[U];
+      for (int n = 0; n < N; n += U) {
+        uint4 v[U];
 #pragma unroll
-          for (int e = 0; e < U; ++e) {
-            v[e] = row < rows ? *reinterpret_cast<const uint4*>(q + w * P.q_row_b + h * (D * 2)) : make_uint4(0u, 0u, 0u, 0u);
-            row += RPP;
-            h += RPP;
-            while (h >= P.group) {
-              h -= P.group;
-              ++w;
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < U; ++e) {
-            const int r = first + (n + e) * RPP;
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(qb + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
-                         "r"((v[e].x & P.q_mask) ^ P.q_sign), "r"((v[e].y & P.q_mask) ^ P.q_sign),
-                         "r"((v[e].z & P.q_mask) ^ P.q_sign), "r"((v[e].w & P.q_mask) ^ P.q_sign)
-                         : "memory");
+        for (int e = 0; e < U; ++e) {
+          v[e] = row < rows ? *reinterpret_cast<const uint4*>(q + w * P.q_row_b + h * (D * 2)) : make_uint4(0u, 0u, 0u, 0u);
+          row += RPP;
+          h += RPP;
+          while (h >= P.group) {
+            h -= P.group;
+            ++w;
           }
         }
-        fence_proxy_async_smem();
-        mbar_arrive(smem_addr(&bars.q_full[unit & 1]));
-        ++unit;
+#pragma unroll
+        for (int e = 0; e < U; ++e) {
+          const int r = first + (n + e) * RPP;
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(qb + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
+                       "r"((v[e].x & P.q_mask) ^ P.q_sign), "r"((v[e].y & P.q_mask) ^ P.q_sign),
+                       "r"((v[e].z & P.q_mask) ^ P.q_sign), "r"((v[e].w & P.q_mask) ^ P.q_sign)
+                       : "memory");
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(smem_addr(&bars.q_full[unit & 1]));
+      ++unit;
+    };
+    // The first unit's rows at once, the next one's S tiles into a unit, when the buffer has long been free (or at the unit's
+    // end): a new unit then does not wait for its rows.
+    load_q(c);
+    bool next_loaded = false;
+    int into = 0;  // tiles into the unit
+    for (int i = 0; i < n_tiles && alive; ++i) {
+      const int left = c.u.tiles - c.tile;  // tiles of the unit from here on
+      if (!next_loaded && i + left < n_tiles && (into == S || left == 1)) {
+        Cursor q = c;
+        next_unit<128>(P, q);
+        load_q(q);
+        next_loaded = true;
+        if (!alive) break;
       }
       if (i % NW == j) {
         if (i >= S) alive = __all_sync(kFull, wait(bars.empty[i % S], (i / S - 1) & 1));
@@ -841,7 +855,12 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
         if (lane == 0) mbar_arrive(smem_addr(&bars.full[i % S]));  // releases what lane 0 wrote to s_valid
         __syncwarp();
       }
-      if (++c.tile == c.u.tiles && i + 1 < n_tiles) next_unit<128>(P, c);
+      ++into;
+      if (++c.tile == c.u.tiles && i + 1 < n_tiles) {
+        next_unit<128>(P, c);
+        next_loaded = false;
+        into = 0;
+      }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == Sh::kMmaWarp) {
