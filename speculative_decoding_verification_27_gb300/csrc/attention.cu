@@ -9,6 +9,7 @@
 // One warp a (row, query head): the lanes hold the head's elements, one token
 // at a time.
 #include "sv_cache.cuh"
+#include "sv_launch.cuh"
 
 #include <cmath>
 #include <cuda_bf16.h>
@@ -105,6 +106,7 @@ __device__ __forceinline__ long long div_small(long long n, int d, int& rest) {
 // tile walks it and tells the others the request.
 template <int MT, int kThr>
 __device__ __forceinline__ bool take_share(const Params& P, const Plan& L, Share& sh, Cursor& c) {
+  wait_for_stream();
   __shared__ long long s_scan[kThr / 32];
   __shared__ Unit s_unit;
   __shared__ long long s_first;
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(Shape<D, WM>::kT, Shape<D, WM>::kCtas) window_
 
   if (S < n_tiles) lookup(ld, page, place);  // tile S, stored in the first round
   for (int i = 0; i < n_tiles; ++i) {
-    if (i + 1 == n_tiles) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may take its place
+    if (i + 1 == n_tiles) release_stream();  // the join may take its place
     if (!begun) {  // a new unit: its rows
       begun = true;
       from_start = cp.tile == 0;
@@ -930,7 +932,7 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
     for (int i = 0; i < n_tiles; ++i) {
       const int rows = c.u.w.rows * P.group, row = c.u.mt * 128 + r;
       const bool last = c.tile + 1 == c.u.tiles || i + 1 == n_tiles;  // of the unit, here
-      if (i + 1 == n_tiles) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      if (i + 1 == n_tiles) release_stream();
       if (i % G == g) {
         if (fresh) {
           fresh = false;
@@ -1119,8 +1121,9 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
 // ---------------------------------------------------------------------------
 // fp32: the same shares, on the fp32 pipes
 // ---------------------------------------------------------------------------
-template <int D, int MT>
+template <int D, int M>
 struct Shape32 {
+  static constexpr int MT = M;
   static constexpr int kT = 128;
   static constexpr int kPitch = D * 4 + 16;        // bytes of a row in shared memory: rows of one column lie in different banks
   static constexpr int kTile = kTK * kPitch;
@@ -1199,7 +1202,7 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
   int lo[RH], hi[RH];
   bool begun = false, from_start = false;
   for (int i = 0; i < n_tiles; ++i) {
-    if (i + 1 == n_tiles) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (i + 1 == n_tiles) release_stream();
     const int rows = cp.u.w.rows * P.group;
     if (!begun) {
       begun = true;
@@ -1355,7 +1358,8 @@ __global__ void __launch_bounds__(kJoinT) join_kernel(Params P, Plan L, int grid
   constexpr int TPR = D / 4, kG = kJoinT / TPR;
   __shared__ float4 s_o[kG][TPR];
   __shared__ float2 s_ml[kG];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  release_stream();
+  wait_for_stream();
   const int c = blockIdx.x;
   const int4 cut = *reinterpret_cast<const int4*>(L.cut + c * 4);
   if (cut.x < 0) return;
@@ -1430,54 +1434,32 @@ __global__ void __launch_bounds__(kJoinT) join_kernel(Params P, Plan L, int grid
 
 constexpr int kGrid = 152 * 4;  // CTAs of the pipeline, at most
 
-// The join starts while the shares are computed: its launch is hidden, and it waits for their end.
-template <int DT, int D, int MT>
-cudaError_t launch_join(const Params& P, const Plan& L, int grid, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, MT < 16 ? MT : 16);
-  cfg.blockDim = dim3(kJoinT);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel<DT, D, MT>, P, L, grid);
-  return e == cudaSuccess ? cudaGetLastError() : e;
+// A kernel over the shares, then the join: it is brought up while the shares are computed, and waits for their end.
+template <int DT, int D, typename Sh>
+cudaError_t launch_shares(void (*kernel)(Params, Plan), const Params& P, const Plan& L, cudaStream_t st,
+                          std::atomic<unsigned long long>& allowed) {
+  static_assert(Sh::kCtas * Sh::MT <= 256, "the workspace has room for the partial results");
+  const int grid = 152 * Sh::kCtas;
+  cudaError_t e = allow_smem(kernel, Sh::smem, allowed);
+  if (e == cudaSuccess) e = launch_overlapped(kernel, dim3(grid), Sh::kT, Sh::smem, 1, st, P, L);
+  if (e == cudaSuccess)
+    e = launch_overlapped(join_kernel<DT, D, Sh::MT>, dim3(grid, Sh::MT < 16 ? Sh::MT : 16), kJoinT, 0, 1, st, P, L, grid);
+  return e;
 }
-
 template <int D, int WM>
 cudaError_t launch_mma(const Params& P, const Plan& L, cudaStream_t st) {
-  using Sh = Shape<D, WM>;
-  cudaError_t e = cudaFuncSetAttribute(window_mma_kernel<D, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::smem);
-  if (e != cudaSuccess) return e;
-  const int grid = 152 * Sh::kCtas;
-  window_mma_kernel<D, WM><<<grid, Sh::kT, Sh::smem, st>>>(P, L);
-  e = cudaGetLastError();
-  return e == cudaSuccess ? launch_join<1, D, Sh::MT>(P, L, grid, st) : e;
+  static std::atomic<unsigned long long> allowed{0};
+  return launch_shares<1, D, Shape<D, WM>>(window_mma_kernel<D, WM>, P, L, st, allowed);
 }
-
 template <int D>
 cudaError_t launch_tc(const Params& P, const Plan& L, cudaStream_t st) {
-  using Sh = TcShape<D>;
-  static_assert(Sh::kCtas * Sh::MT <= 256, "the workspace has room for the partial results");
-  cudaError_t e = cudaFuncSetAttribute(window_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::smem);
-  if (e != cudaSuccess) return e;
-  const int grid = 152 * Sh::kCtas;
-  window_tc_kernel<D><<<grid, Sh::kT, Sh::smem, st>>>(P, L);
-  e = cudaGetLastError();
-  return e == cudaSuccess ? launch_join<1, D, Sh::MT>(P, L, grid, st) : e;
+  static std::atomic<unsigned long long> allowed{0};
+  return launch_shares<1, D, TcShape<D>>(window_tc_kernel<D>, P, L, st, allowed);
 }
-
-template <int D, int MT>
+template <int D, int M>
 cudaError_t launch_fma(const Params& P, const Plan& L, cudaStream_t st) {
-  using Sh = Shape32<D, MT>;
-  cudaError_t e = cudaFuncSetAttribute(window_fma_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::smem);
-  if (e != cudaSuccess) return e;
-  const int grid = 152 * Sh::kCtas;
-  window_fma_kernel<D, MT><<<grid, Sh::kT, Sh::smem, st>>>(P, L);
-  e = cudaGetLastError();
-  return e == cudaSuccess ? launch_join<0, D, MT>(P, L, grid, st) : e;
+  static std::atomic<unsigned long long> allowed{0};
+  return launch_shares<0, D, Shape32<D, M>>(window_fma_kernel<D, M>, P, L, st, allowed);
 }
 
 }  // namespace att

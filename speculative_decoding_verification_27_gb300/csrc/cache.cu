@@ -6,6 +6,7 @@
 // bits in the order of the sequences. Both are independent of timing, so the
 // page tables are the same from run to run.
 #include "sv_cache.cuh"
+#include "sv_launch.cuh"
 
 #include <climits>
 
@@ -55,6 +56,8 @@ __device__ __forceinline__ void release_from(const CacheView& C, const SeqView& 
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kT) fork_kernel(CacheView C, SeqView S, int N, const int32_t* src, const int32_t* dst,
                                                   uint32_t* status) {
+  release_stream();
+  wait_for_stream();
   const int i = blockIdx.x * (kT / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (i >= N) return;
   const int s = src[i], d = dst[i];
@@ -93,6 +96,8 @@ __global__ void __launch_bounds__(kT) fork_kernel(CacheView C, SeqView S, int N,
 }
 
 __global__ void __launch_bounds__(kT) free_kernel(CacheView C, SeqView S, int N, const int32_t* which, uint32_t* status) {
+  release_stream();
+  wait_for_stream();
   const int i = blockIdx.x * (kT / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (i >= N) return;
   const int s = which[i];
@@ -180,7 +185,8 @@ __device__ __forceinline__ int last_at_most(const int* first, int n, int k) {
 // launch and the first loads are half).
 __global__ void __launch_bounds__(kR) reserve_kernel(CacheView C, SeqView S, WindowView W, int32_t* granted, ReserveWs* ws,
                                                      uint32_t* status) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  release_stream();
+  wait_for_stream();
   extern __shared__ __align__(16) int s_mem[];
   const int n_pad = (S.n + 4) & ~3;
   int* s_part = s_mem;             // the shared partial page, or -1
@@ -330,7 +336,8 @@ __global__ void __launch_bounds__(kR) reserve_kernel(CacheView C, SeqView S, Win
 // The copies that reserve asked for: a CTA a (job, layer, K or V), 16-byte
 // vectors of whole tokens, four a thread in flight.
 __global__ void __launch_bounds__(kT) copy_kernel(CacheView C, const ReserveWs* ws) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  release_stream();
+  wait_for_stream();
   const int vecs = C.head_bytes / 16, n_vec = C.n_heads * vecs;
   const bool whole = C.head_b == C.head_bytes && C.token_b == (long long)C.n_heads * C.head_b;  // tokens lie one after another
   const long long n = (long long)ws->n_jobs * C.n_layers * 2;
@@ -375,6 +382,8 @@ constexpr int kIn = 4;
 __global__ void __launch_bounds__(kT) append_kernel(CacheView C, SeqView S, WindowView W, int layer, int n_layers,
                                                     const char* k_new, const char* v_new, long long new_layer_b,
                                                     long long new_row_b, uint32_t* status) {
+  release_stream();
+  wait_for_stream();
   const int lane = threadIdx.x & 31, vecs = C.head_bytes / 16, n_vec = C.n_heads * vecs;
   const int warp0 = blockIdx.x * (kT / 32) + (threadIdx.x >> 5), step = gridDim.x * (kT / 32);
   const bool whole = C.head_b == C.head_bytes;  // a token's heads lie together
@@ -486,7 +495,8 @@ __device__ __forceinline__ Kept kept_rows(const CacheView& C, const SeqView& S, 
 constexpr int kMove = 8;
 __global__ void __launch_bounds__(kT) move_kernel(CacheView C, SeqView S, WindowView W, const int32_t* best,
                                                   const int32_t* out_len) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  release_stream();
+  wait_for_stream();
   __shared__ long long s_from[kMove], s_to[kMove];
   const int vecs = C.head_bytes / 16;
   const long long cols = 2ll * C.n_layers * C.n_heads * vecs;
@@ -523,7 +533,8 @@ __global__ void __launch_bounds__(kT) move_kernel(CacheView C, SeqView S, Window
 // The new length, and the pages behind it released: one warp a request.
 __global__ void __launch_bounds__(kT) trim_kernel(CacheView C, SeqView S, WindowView W, const int32_t* best,
                                                   const int32_t* out_len, uint32_t* status) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  release_stream();
+  wait_for_stream();
   const int b = blockIdx.x * (kT / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (b >= S.n) return;
   const Kept kept = kept_rows(C, S, W, best, out_len, b);
@@ -538,25 +549,13 @@ __global__ void __launch_bounds__(kT) trim_kernel(CacheView C, SeqView S, Window
 }
 
 inline bool aligned4(const void* p) { return (uintptr_t)p % 4 == 0; }
-inline sv_status launched() { return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
 inline int warps_grid(long long n) {
   const long long g = (n + kT / 32 - 1) / (kT / 32);
   return (int)(g > (1 << 30) ? (1 << 30) : g);
 }
-// Launches a kernel that waits for the one before it in the stream by itself (griddepcontrol.wait): the launches overlap.
-template <typename... A>
-sv_status launch_after(void (*kernel)(A...), dim3 grid, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kT);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  return e == cudaSuccess ? launched() : SV_ERR_CUDA;
+template <typename... K, typename... A>
+sv_status launch(void (*kernel)(K...), dim3 grid, cudaStream_t st, A... args) {
+  return launch_overlapped(kernel, grid, kT, 0, 1, st, args...) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 inline int y_grid(int n) { return n > 32768 ? 32768 : n; }
 
@@ -573,9 +572,8 @@ sv_status sv_cache_fork(const sv_kv_cache* cache, const sv_sequences* seqs, int3
   if (!cache_view(cache, &C) || !seq_view(seqs, &S) || N < 0 || !cache::aligned4(status)) return SV_ERR_INVALID_ARG;
   if (N == 0) return SV_OK;
   if (!src || !dst || !cache::aligned4(src) || !cache::aligned4(dst)) return SV_ERR_INVALID_ARG;
-  cache::fork_kernel<<<cache::warps_grid(N), cache::kT, 0, static_cast<cudaStream_t>(cuda_stream)>>>(C, S, N, src, dst,
-                                                                                                    status);
-  return cache::launched();
+  return cache::launch(cache::fork_kernel, dim3((unsigned)cache::warps_grid(N)), static_cast<cudaStream_t>(cuda_stream), C, S, N, src,
+                       dst, status);
 }
 
 sv_status sv_cache_free(const sv_kv_cache* cache, const sv_sequences* seqs, int32_t N, const int32_t* which,
@@ -586,9 +584,8 @@ sv_status sv_cache_free(const sv_kv_cache* cache, const sv_sequences* seqs, int3
   if (!cache_view(cache, &C) || !seq_view(seqs, &S) || N < 0 || !cache::aligned4(status)) return SV_ERR_INVALID_ARG;
   if (N == 0) return SV_OK;
   if (!which || !cache::aligned4(which)) return SV_ERR_INVALID_ARG;
-  cache::free_kernel<<<cache::warps_grid(N), cache::kT, 0, static_cast<cudaStream_t>(cuda_stream)>>>(C, S, N, which,
-                                                                                                    status);
-  return cache::launched();
+  return cache::launch(cache::free_kernel, dim3((unsigned)cache::warps_grid(N)), static_cast<cudaStream_t>(cuda_stream), C, S, N, which,
+                       status);
 }
 
 size_t sv_cache_reserve_workspace_size(int32_t n) {
@@ -612,14 +609,15 @@ sv_status sv_cache_reserve(const sv_kv_cache* cache, const sv_sequences* seqs, i
   W.R = -1;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const int smem = 3 * ((S.n + 4) & ~3) * 4;
+  static std::atomic<unsigned long long> allowed{0};
   if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(cache::reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      allow_smem(cache::reserve_kernel, 3 * 4 * (SV_CACHE_MAX_SEQS + 4), allowed) != cudaSuccess)
     return SV_ERR_CUDA;
   cache::ReserveWs* ws = static_cast<cache::ReserveWs*>(workspace);
-  cache::reserve_kernel<<<1, cache::kR, smem, st>>>(C, S, W, granted, ws, status);
-  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  if (launch_overlapped(cache::reserve_kernel, dim3(1), cache::kR, smem, 1, st, C, S, W, granted, ws, status) != cudaSuccess)
+    return SV_ERR_CUDA;
   const long long most = (long long)S.n * C.n_layers * 2;
-  return cache::launch_after(cache::copy_kernel, dim3((unsigned)(most < 152 * 8 ? most : 152 * 8)), st, C,
+  return cache::launch(cache::copy_kernel, dim3((unsigned)(most < 152 * 8 ? most : 152 * 8)), st, C,
                              static_cast<const cache::ReserveWs*>(ws));
 }
 
@@ -645,10 +643,9 @@ sv_status sv_cache_append(const sv_kv_cache* cache, int32_t layer, int32_t n_lay
   const int gy = cache::y_grid(S.n), gz = n_layers < 64 ? n_layers : 64;
   const long long gx = ((R + gy - 1) / gy + cache::kT / 32 - 1) / (cache::kT / 32);
   const long long most = (152 * 8 + (long long)gy * gz - 1) / ((long long)gy * gz);
-  cache::append_kernel<<<dim3((unsigned)(gx < most ? gx : most), gy, gz), cache::kT, 0, static_cast<cudaStream_t>(cuda_stream)>>>(
+  return cache::launch(cache::append_kernel, dim3((unsigned)(gx < most ? gx : most), gy, gz), static_cast<cudaStream_t>(cuda_stream),
       C, S, W, layer, n_layers, static_cast<const char*>(k_new), static_cast<const char*>(v_new), new_layer_stride * es,
       new_row_stride * es, status);
-  return cache::launched();
 }
 
 sv_status sv_cache_commit(const sv_kv_cache* cache, const sv_sequences* seqs, int32_t n_cand, const int32_t* cu_draft,
@@ -668,15 +665,14 @@ sv_status sv_cache_commit(const sv_kv_cache* cache, const sv_sequences* seqs, in
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const dim3 trim((unsigned)cache::warps_grid(S.n));
   if (!cu_cand) {  // without candidates the kept rows are in place
-    cache::trim_kernel<<<trim, cache::kT, 0, st>>>(C, S, W, best, out_len, status);
-    return cache::launched();
+    return cache::launch(cache::trim_kernel, trim, st, C, S, W, best, out_len, status);
   }
   const long long cols = 2ll * C.n_layers * C.n_heads * (C.head_bytes / 16);
   const int gy = cache::y_grid(S.n);
   const long long gx = (cols + cache::kT - 1) / cache::kT, most = (152 * 8 + gy - 1) / gy;
-  cache::move_kernel<<<dim3((unsigned)(gx < most ? gx : most), gy), cache::kT, 0, st>>>(C, S, W, best, out_len);
-  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
-  return cache::launch_after(cache::trim_kernel, trim, st, C, S, W, best, out_len, status);
+  const sv_status moved = cache::launch(cache::move_kernel, dim3((unsigned)(gx < most ? gx : most), gy), st, C, S, W, best, out_len);
+  if (moved != SV_OK) return moved;
+  return cache::launch(cache::trim_kernel, trim, st, C, S, W, best, out_len, status);
 }
 
 }  // extern "C"

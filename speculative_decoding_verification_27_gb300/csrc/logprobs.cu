@@ -21,6 +21,7 @@
 // about 70% of the special-function rate at the copy rate for bf16).
 #include "../../include/spec_verify.h"
 #include "sv_device.cuh"
+#include "sv_launch.cuh"
 
 #include <cfloat>
 #include <climits>
@@ -388,6 +389,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = cl > 1 ? (int)cluster_rank() : 0;
   const int r = cl > 1 ? blockIdx.x / cl : blockIdx.x;
+  release_stream();
+  wait_for_stream();
   if (blockIdx.x == 0) check_offsets(P, tid);
   if (P.cu && !row_wanted(P, r, find_request(P.cu, P.B, r))) return;  // all CTAs of the row alike
   const int V = P.V, n_top = P.n_top;
@@ -706,17 +709,8 @@ extern "C" sv_status sv_token_logprobs(const void* logits, sv_dtype dtype, int32
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const int cl = lp::cluster_size(R, (long long)V * es);
   if ((long long)R * cl > INT32_MAX) return SV_ERR_INVALID_ARG;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(R * cl));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)cl;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = cl > 1 ? 1 : 0;
-  const cudaError_t e = dtype == SV_BF16 ? cudaLaunchKernelEx(&cfg, lp::logprobs_kernel<1>, P, cl)
-                                         : cudaLaunchKernelEx(&cfg, lp::logprobs_kernel<0>, P, cl);
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  const cudaError_t e =
+      dtype == SV_BF16 ? launch_overlapped(lp::logprobs_kernel<1>, dim3((unsigned)(R * cl)), kThreads, 0, (unsigned)cl, st, P, cl)
+                       : launch_overlapped(lp::logprobs_kernel<0>, dim3((unsigned)(R * cl)), kThreads, 0, (unsigned)cl, st, P, cl);
+  return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }

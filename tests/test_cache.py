@@ -446,7 +446,10 @@ def test_a_captured_step(cuda_lib):
     twice = new * 2
     cu, n = r.i32([0, 2, 4, 6]), r.i32([0, 0, 0])
 
+    from_host = torch.zeros_like(n)
+
     def step():
+        n.copy_(from_host)  # a copy node before the kernels
         api.sv_cache_reserve(*r.args(), cu)
         api.sv_cache_append(r.cache, 0, new, twice, r.table, r.ctx, cu)
         api.sv_cache_commit(*r.args(), cu, n)
@@ -462,7 +465,7 @@ def test_a_captured_step(cuda_lib):
         r.names += 9
         new.copy_(torch.stack([_value(x, r.L, r.H, r.D, r.dtype) for y in names for x in y], 1))
         twice.copy_(new * 2)
-        n.copy_(r.i32(keep))
+        from_host.copy_(r.i32(keep))
         graph.replay()
         granted, _, _ = r.m.reserve([3] * 3)
         r.m.append(names, granted)

@@ -251,11 +251,15 @@ def test_streams_graphs_and_repeats(cuda_lib):
     small, st = zc[:5].clone(), tc[:5].clone()
     api.sv_token_logprobs(small, st, n_top=20)
     graph = torch.cuda.CUDAGraph()
+    src = zc[300:305].clone()
     with torch.cuda.graph(graph):
+        small.copy_(src)  # a copy before the kernel, and one behind it
         out = api.sv_token_logprobs(small, st, n_top=20)
-    small.copy_(zc[300:305])
+        after = out.logprob.clone()
     st.copy_(tc[300:305])
     graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(after, out.logprob)
     torch.cuda.synchronize()
     _check(z[300:305], tok[300:305], 1.0, 20, out)
 
