@@ -7,6 +7,7 @@ error, not a fallback. PyTorch supplies device memory and the current stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import struct
@@ -630,6 +631,26 @@ class KVCache:
         self._c = _Cache(k.data_ptr(), v.data_ptr(), _dtype(k), *k.shape, *steps[:4],
                          _vec(page_ref, "page_ref", torch.int32, (n,)), _vec(free_bits, "free_bits", torch.int32, (words,)))
         self._ref = ctypes.byref(self._c)
+        self._attention_bytes = load().sv_window_attention_workspace_size(self._ref, self.n_kv_heads, 0)
+        self._workspaces: dict = {}
+
+    def _workspace(self, nbytes: int, stream) -> torch.Tensor:
+        """Scratch of at least nbytes for a call on `stream`: one block a
+        stream, whose calls run in order. A call that is being captured gets
+        a block of its graph's own."""
+        if stream is None:
+            key = _raw_stream(self.k.get_device())
+            capturing = torch.cuda.is_current_stream_capturing()
+        else:
+            key = stream.cuda_stream
+            with torch.cuda.stream(stream):
+                capturing = torch.cuda.is_current_stream_capturing()
+        if capturing:
+            return _new(torch.empty, nbytes, torch.uint8, self.k, stream)
+        ws = self._workspaces.get(key)
+        if ws is None or ws.numel() < nbytes:
+            ws = self._workspaces[key] = _new(torch.empty, max(nbytes, self._attention_bytes), torch.uint8, self.k, stream)
+        return ws
 
 
 def _seqs(page_table: torch.Tensor, ctx_len: torch.Tensor) -> bytes:
@@ -653,10 +674,6 @@ def _windows(n: int, cu_draft, cu_cand):
     return n_cand, _vec(cu_draft, "cu_draft", torch.int32, (n_cand + 1,)), _vec(cu_cand, "cu_cand", torch.int32, (n + 1,))
 
 
-def _scratch(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
-    return _new(torch.empty, max(nbytes, 16), torch.uint8, like, stream)
-
-
 def sv_cache_fork(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, *,
                   status=None, stream=None) -> None:
     """Sequences dst[i] (empty) become copies of src[i] that share its pages."""
@@ -673,6 +690,11 @@ def sv_cache_free(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Tenso
             _vec(which, "which", torch.int32, (N,)), _vec(status, "status", torch.int32, (1,)))
 
 
+@functools.lru_cache(maxsize=1024)
+def _reserve_bytes(n: int) -> int:
+    return max(int(load().sv_cache_reserve_workspace_size(n)), 16)
+
+
 def sv_cache_reserve(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Tensor, cu_draft=None, cu_cand=None, *,
                      granted=None, workspace=None, status=None, stream=None) -> torch.Tensor:
     """Pages for every sequence's window. Returns `granted` [n]: the window's
@@ -681,7 +703,7 @@ def sv_cache_reserve(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Te
     if granted is None:
         granted = _new(torch.empty, n, torch.int32, page_table, stream)
     if workspace is None:
-        workspace = _scratch((_lib or load()).sv_cache_reserve_workspace_size(n), page_table, stream)
+        workspace = cache._workspace(_reserve_bytes(n), stream)
     _launch("sv_cache_reserve", cache.k, stream, cache._ref, _seqs(page_table, ctx_len), *_windows(n, cu_draft, cu_cand),
             _vec(granted, "granted", torch.int32, (n,)), _ptr(workspace), workspace.numel(),
             _vec(status, "status", torch.int32, (1,)))
@@ -738,7 +760,7 @@ def sv_window_attention(q: torch.Tensor, cache: KVCache, layer: int, page_table:
     if out_lse is None and want_lse:
         out_lse = _new(torch.zeros, (R, heads), torch.float32, q, stream)
     if workspace is None:
-        workspace = _scratch((_lib or load()).sv_window_attention_workspace_size(cache._ref, heads, R), q, stream)
+        workspace = cache._workspace(cache._attention_bytes, stream)
     _launch("sv_window_attention", q, stream, q.data_ptr(), q.stride(0) if R > 1 else heads * D, heads, R, cache._ref,
             int(layer), _seqs(page_table, ctx_len), *_windows(page_table.shape[0], cu_draft, cu_cand),
             D ** -0.5 if scale is None else float(scale), out.data_ptr(), out.stride(0) if R > 1 else heads * D,
