@@ -72,8 +72,14 @@ __device__ __forceinline__ void check_offsets(const Params& P, int tid) {
   if (bad) flag(P, SV_DATA_BAD_OFFSETS);
 }
 
-constexpr int kU = 4;            // 16-byte loads of a batch, per thread; the next batch's are in flight meanwhile
-constexpr int kVecs = 1024;      // vectors that a CTA buffers because one of their elements may be an alternative
+#ifndef SV_LP_LOADS
+#define SV_LP_LOADS 4
+#endif
+#ifndef SV_LP_CTAS
+#define SV_LP_CTAS 4
+#endif
+constexpr int kU = SV_LP_LOADS;  // 16-byte loads of a batch, per thread; the next batch's are in flight meanwhile
+constexpr int kVecs = 256 * SV_LP_LOADS;      // vectors that a CTA buffers because one of their elements may be an alternative
 constexpr int kCap = 1024;       // elements that reached the last floor
 constexpr int kMaxCluster = 8;   // CTAs to a row, at most
 constexpr float kFar = 200.f;    // 2^-kFar is zero in fp32: exponents are cut off there
@@ -315,6 +321,20 @@ struct Smem {
   int n, n2;
 };
 
+// Places for n entries a lane in a list of *count entries: the lane's first.
+__device__ __forceinline__ int warp_place(int n, int* count) {
+  const int lane = threadIdx.x & 31;
+  int x = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  int first = 0;
+  if (lane == 31 && x) first = atomicAdd(count, x);
+  return __shfl_sync(kFull, first, 31) + x - n;
+}
+
 // n elements of the row reach the least of the warps' floors.
 __device__ __forceinline__ float shared_floor(const Smem& sm) {
   float f = sm.floor_w[0];
@@ -383,7 +403,7 @@ __device__ __forceinline__ void to_leader(u64* p, u64 v) {
 
 // A cluster of `cl` CTAs takes a row, each a contiguous slice of its vectors.
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl) {
+__global__ void __launch_bounds__(kThreads, SV_LP_CTAS) logprobs_kernel(Params P, int cl) {
   constexpr int EPV = Elem<DT>::kEPV;
   __shared__ Smem sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -475,17 +495,20 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
           floor = fmaxf(floor, warp_nth_largest(m, n_top));
           hit = hit && bm >= floor;
         }
-        if (hit) {
+        // The warp's vectors that reach it, one addition to the count for all of them.
+        uint32_t mine = 0;
 #pragma unroll
-          for (int u = 0; u < kU; ++u)
-            if (max_value<DT>(vm[u]) >= floor) {
-              const int k = atomicAdd(&sm.n, 1);
-              if (k < kVecs) {
-                sm.vec[k] = cur[u];
-                sm.vec_at[k] = at + u * kThreads + tid;
-              }
+        for (int u = 0; u < kU; ++u) mine |= (uint32_t)(hit && max_value<DT>(vm[u]) >= floor) << u;
+        int k = warp_place(__popc(mine), &sm.n);
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          if (mine >> u & 1u) {
+            if (k < kVecs) {
+              sm.vec[k] = cur[u];
+              sm.vec_at[k] = at + u * kThreads + tid;
             }
-        }
+            ++k;
+          }
         __syncwarp();
         if (!first) {
           const float w = warp_nth_largest(m, q);
@@ -538,16 +561,25 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Params P, int cl)
     const int c = sm.n;
     if (c <= kVecs) {
       // What reached the last floor, in any order: the sort below does not depend on it.
-      for (int i = tid; i < c; i += kThreads) {
+      for (int i0 = warp * 32; i0 < c; i0 += kThreads) {
+        const int i = i0 + lane;
         float f[EPV];
-        Elem<DT>::unpack(sm.vec[i], f);
-        const int x0 = sm.vec_at[i] * EPV - off;
+        uint32_t mine = 0;
+        if (i < c) {
+          Elem<DT>::unpack(sm.vec[i], f);
 #pragma unroll
-        for (int j = 0; j < EPV; ++j)
-          if (f[j] >= floor && f[j] > -INFINITY) {
-            const int k = atomicAdd(&sm.n2, 1);
-            if (k < kCap - 1) sm.cand[k] = make_key(f[j], x0 + j);
-          }
+          for (int j = 0; j < EPV; ++j) mine |= (uint32_t)(f[j] >= floor && f[j] > -INFINITY) << j;
+        }
+        int k = warp_place(__popc(mine), &sm.n2);
+        if (mine) {
+          const int x0 = sm.vec_at[i] * EPV - off;
+#pragma unroll
+          for (int j = 0; j < EPV; ++j)
+            if (mine >> j & 1u) {
+              if (k < kCap - 1) sm.cand[k] = make_key(f[j], x0 + j);
+              ++k;
+            }
+        }
       }
       __syncthreads();
     }
