@@ -6,8 +6,21 @@
 //   m' = max(m, s), l' = l e^(m - m') + e^(s - m'), o' = o e^(m - m') + e^(s - m') v
 // and out = o / l, lse = m + ln l.
 //
-// One warp a (row, query head): the lanes hold the head's elements, one token
-// at a time.
+// The query heads that share a key-value head, over all rows of the window,
+// are stacked: a tile of stacked rows reads each key and value once. Four
+// kernels, all over equal shares of one list of key tiles (see Plan), chosen
+// by the type and by the windows' mean number of stacked rows (64 requests of
+// 4096 tokens, 8 key-value heads, one token to 32 of them; the copy rate would
+// read heads of 128 in 159 us, of 64 in 79):
+//   bf16, up to 16, 32, 64 rows   window_mma_kernel: 191-200 us for heads of
+//     128 (5.3 - 5.6 TB/s) up to 32 rows, 265 us for 64; heads of 64: 118-128
+//     and 172 us;
+//   bf16, more rows               window_tc_kernel, tiles of 128 rows: 280 us
+//     (heads of 128) and 170 us (of 64) for 128 rows, where the other took
+//     476 and 293 us. At 64 rows its tiles would be half empty and it takes
+//     as long as for 128: no gain;
+//   fp32, up to 4, 8, 16 rows     window_fma_kernel.
+// Sums of a split request are joined by join_kernel.
 #include "sv_cache.cuh"
 #include "sv_launch.cuh"
 
@@ -33,7 +46,7 @@ struct Params {
 };
 
 // ---------------------------------------------------------------------------
-// bf16: tensor cores over a paged pipeline
+// The list of key tiles and its shares
 // ---------------------------------------------------------------------------
 constexpr int kTK = 64;    // tokens of a key tile
 
@@ -239,6 +252,16 @@ constexpr size_t part_bytes() {
   return (size_t)MT * (D + 2) * 4;
 }
 
+// ---------------------------------------------------------------------------
+// bf16, few stacked rows: mma.sync over a paged pipeline
+// ---------------------------------------------------------------------------
+// Bound by the bytes up to 32 rows. K and V tiles are gathered by 16-byte
+// asynchronous copies through a ring of swizzled stages (any page size and
+// layout; pages of 1, 16 and 64 tokens take the same time), the page table
+// looked up a tile ahead of them. With few rows the warps split a tile's
+// tokens (WK), with 64 its rows. Two CTAs an SM with three stages for heads of
+// 128 (three CTAs with two stages: 7% slower), four with three for heads of 64
+// (two with six: 5% slower).
 template <int D, int WM>
 struct Shape {
   static constexpr int MT = 16 * WM;            // stacked rows of a unit
@@ -1133,6 +1156,9 @@ struct Shape32 {
   static constexpr size_t smem = (size_t)kStages * 2 * kTile + (size_t)MT * D * 4 + (size_t)MT * SP * 4 + MT * 16 + kStages * kTK * 8;
 };
 
+// Bound by its instructions and latencies, not by its bytes: 64 requests of
+// 1000 tokens, 8 heads of 64, windows of 4 rows take 70 us (39 us of bytes),
+// 37 ragged windows over 0 - 1000 tokens 33 us a call. Row tiles of 4, 8 or 16.
 // A tile's scores: thread (token, half of the rows) walks d. Its softmax: a
 // warp takes every fourth row. Its product with V: thread (d, share of the
 // tokens) holds every row's sum.
