@@ -597,7 +597,8 @@ sv_status sv_cache_commit(const sv_kv_cache* cache, const sv_sequences* seqs, in
  * not. Keys and values of the tokens a window holds must be finite; what lies
  * in the pages behind it may be anything. A page out of range in a
  * sequence's table hides its tokens (SV_DATA_BAD_PAGE); a row that sees no
- * token gives out = 0 and lse = -inf.
+ * token gives out = 0 and lse = -inf. SV_DEV_COPY_TIMEOUT in status: a bounded
+ * wait inside the call gave up (never expected) and its outputs are invalid.
  */
 size_t sv_window_attention_workspace_size(const sv_kv_cache* cache, int32_t n_q_heads, int32_t R);
 sv_status sv_window_attention(const void* q, int64_t q_stride, int32_t n_q_heads, int32_t R,

@@ -164,6 +164,7 @@ __device__ __forceinline__ bool take_share(const Params& P, const Plan& L, Share
     s_unit = c.u;
     s_first = sh.t0 - at;  // first tile of the share within its request
   }
+  if (tid == 0) L.cut[id * 4] = -1;  // until the share's end is reached
   __syncthreads();
   c.u = s_unit;
   const long long unit = div_small(s_first, c.u.tiles, c.tile);
@@ -1388,7 +1389,7 @@ __global__ void __launch_bounds__(kJoinT) join_kernel(Params P, Plan L, int grid
   wait_for_stream();
   const int c = blockIdx.x;
   const int4 cut = *reinterpret_cast<const int4*>(L.cut + c * 4);
-  if (cut.x < 0) return;
+  if (cut.x < 0 || cut.x >= P.S.n) return;
   const int head = cut.y, mt = cut.z, last = min(cut.w, grid - 1);
   const Window w = find_window(P.W, cut.x);
   const int rows = w.rows * P.group;
@@ -1494,7 +1495,7 @@ cudaError_t launch_fma(const Params& P, const Plan& L, cudaStream_t st) {
 extern "C" {
 
 size_t sv_window_attention_workspace_size(const sv_kv_cache* cache, int32_t n_q_heads, int32_t R) {
-  if (!cache || n_q_heads < 1 || R < 0) return 0;
+  if (!cache || (cache->head_dim != 64 && cache->head_dim != 128) || n_q_heads < 1 || R < 0) return 0;
   // The cuts, then two partial results a CTA: of any kernel, 256 rows an SM at most.
   return (size_t)sv::att::kGrid * 16 + 2 * (size_t)152 * 256 * ((size_t)cache->head_dim + 2) * 4;
 }

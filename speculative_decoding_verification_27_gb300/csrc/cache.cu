@@ -202,7 +202,10 @@ __global__ void __launch_bounds__(kR) reserve_kernel(CacheView C, SeqView S, Win
   __shared__ uint32_t s_bits[kR];
   __shared__ int s_jobs, s_end, s_shared;
   const int tid = threadIdx.x, n_words = (C.n_pages + 31) / 32;
-  uint32_t bits0 = tid < n_words ? C.free_bits[tid] : 0u;  // early: needed last
+  // Free pages of word w; what a caller left in the bits past the last page does not count.
+  const uint32_t tail = C.n_pages & 31 ? (1u << (C.n_pages & 31)) - 1u : ~0u;
+  auto free_word = [&](int w) { return w < n_words ? C.free_bits[w] & (w + 1 == n_words ? tail : ~0u) : 0u; };
+  const uint32_t bits0 = free_word(tid);  // early: needed last
   if (tid == 0) {
     s_jobs = s_shared = 0;
     s_end = INT_MAX;
@@ -284,7 +287,7 @@ __global__ void __launch_bounds__(kR) reserve_kernel(CacheView C, SeqView S, Win
   for (int w0 = 0; w0 < n_words && avail < total; w0 += kR) {
     const int w = w0 + tid;
     int sum;
-    word_first = block_excl_scan(w0 == 0 ? __popc(bits0) : w < n_words ? __popc(C.free_bits[w]) : 0, s_warp, sum);
+    word_first = block_excl_scan(__popc(w0 == 0 ? bits0 : free_word(w)), s_warp, sum);
     avail += sum;
   }
   __syncthreads();
@@ -304,7 +307,7 @@ __global__ void __launch_bounds__(kR) reserve_kernel(CacheView C, SeqView S, Win
   int taken = 0;
   for (int w0 = 0; w0 < n_words && taken < total; w0 += kR) {
     const int w = w0 + tid;
-    const uint32_t bits = w0 == 0 ? bits0 : w < n_words ? C.free_bits[w] : 0u;
+    const uint32_t bits = w0 == 0 ? bits0 : free_word(w);
     const int mine = __popc(bits);
     int sum = min(avail, INT_MAX), first = word_first;
     if (n_words > kR) first = block_excl_scan(mine, s_warp, sum);

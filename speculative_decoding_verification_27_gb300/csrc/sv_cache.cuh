@@ -54,6 +54,9 @@ inline bool cache_view(const sv_kv_cache* c, CacheView* out) {
   if ((int64_t)c->n_kv_heads * (c->head_dim * es / 16) * c->page_size > (1 << 30)) return false;
   *out = CacheView{static_cast<char*>(c->k), static_cast<char*>(c->v), s[0] * es, s[1] * es, s[2] * es, s[3] * es,
                    c->n_layers, c->n_pages, c->page_size, c->n_kv_heads, c->head_dim * es, c->page_ref, c->free_bits, 0, 0};
+  // A dimension of one element takes no step: give it the one that lets copies run through.
+  if (out->n_heads == 1) out->head_b = out->head_bytes;
+  if (out->page_size == 1) out->token_b = out->n_heads * out->head_b;
   // For t < 2^31: with 2^s the next power of two, m = ceil(2^(31 + s) / page_size) errs by less than 2^s, so that t m / 2^(31 + s)
   // is less than 1 / page_size too large.
   int log2 = 0;

@@ -208,6 +208,68 @@ def test_peaked_rows_and_scales(cuda_lib, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("scale,heavy", [(None, True), (0.0, False), (-0.2, False), (2.0, False)])
+def test_high_tiles_peaked_rows_and_scales(cuda_lib, D, scale, heavy):
+    """Row tiles of 128: maxima that move by hundreds from tile to tile, a scale of zero and negative ones."""
+    c = Case([700, 20, 333], [[3, 2], [4], [30]], 32, 1, D, 16, BF, seed=30 + D, heavy=heavy)
+    # Scores that rise along the history, so that the running maximum moves at every tile.
+    rise = torch.linspace(0.2, 4.0, 64)
+    for b, n in enumerate((705, 24, 363)):
+        for t in range(n):
+            p, i = int(c.table[b, t // 16]), t % 16
+            c.k[0, p, i] = (c.k[0, p, i].float() * rise[min(63, t // 12)]).to(BF)
+    c.check(**({} if scale is None else {"scale": scale}))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("layout,q_pad,page", [("hnd", 0, 16), ("both", 64, 7), ("nhd", 0, 1), ("nhd", 0, 1000)])
+def test_high_tiles_layouts(cuda_lib, D, layout, q_pad, page):
+    Case([300, 0, 64, 129], [[9], [5, 4], [3, 1, 20], [17]], 48, 3, D, page, BF, seed=D + page, layout=layout, q_pad=q_pad).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_high_tiles_split_repeats_and_bad_pages(cuda_lib, D):
+    """Long requests of many stacked rows, split over the machine: the same bits every time, from a graph too; hidden pages."""
+    c = Case([9000, 4000, 10], [[5], [3, 3], [2]], 64, 2, D, 16, BF, seed=40 + D)
+    c.check()
+    q, cache, layer, table, ctx, cu, cand = c.args
+    want = api.sv_window_attention(*c.args, want_lse=True)
+    for _ in range(3):
+        got = api.sv_window_attention(*c.args, want_lse=True)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = api.sv_window_attention(*c.args, want_lse=True)
+    other = api.sv_window_attention(q * 0.5, *c.args[1:], want_lse=True)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1]) and not torch.equal(other[0], want[0])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    broken = table.clone()
+    broken[1, :200] = 1 << 20
+    broken[2] = -1
+    got = api.sv_window_attention(q, cache, layer, broken, ctx, cu, cand, want_lse=True, status=status)
+    assert int(status) == api.SV_DATA_BAD_PAGE
+    assert torch.equal(got[0][:5], want[0][:5])
+    assert bool((got[0][11:13] == 0).all()) and bool((got[1][11:13] == -INF).all())
+    keep = torch.arange(3200, 4001)
+    k = c.k[0][c.table[1].long()[keep // 16], keep % 16].double().repeat_interleave(32, 1)
+    s = torch.einsum("hd,thd->ht", c.q[5].double(), k) * D ** -0.5
+    assert (torch.logsumexp(s, 1) - got[1][5].cpu().double()).abs().max() < 1e-4
+
+
+@pytest.mark.gpu
+def test_thousands_of_sequences(cuda_lib):
+    """More sequences than a CTA has threads: every thread walks several of them."""
+    gen = torch.Generator().manual_seed(3)
+    ctx = torch.randint(0, 20, (3001,), generator=gen).tolist()
+    Case(ctx, [[1]] * 3001, 2, 1, 64, 16, BF, seed=3, cands=False).check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_many_requests(cuda_lib, dtype):
     """More requests than the machine has processors, most of them short."""

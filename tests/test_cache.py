@@ -423,6 +423,52 @@ def test_offsets_past_32_bits(cuda_lib):
 
 
 @pytest.mark.gpu
+def test_free_pages_far_into_a_large_pool(cuda_lib):
+    """More pages than one sweep of the allocator covers, free ones here and there; bits past the last page do not count."""
+    P = 100003
+    k = torch.zeros(1, P, 1, 1, 8, device="cuda")
+    free = sorted(random.Random(2).sample(range(40000, P), 50)) + [P - 1]
+    ref = torch.ones(P, dtype=torch.int32)
+    words = [0] * -(-P // 32)
+    for p in free:
+        ref[p] = 0
+        words[p // 32] |= 1 << p % 32
+    bits = torch.tensor([w - (1 << 32) if w >> 31 else w for w in words], dtype=torch.int32, device="cuda")
+    bits[-1] |= 1 << 30  # stray bits behind the last page
+    assert P % 32 < 30
+    cache = api.KVCache(k, k.clone(), ref.cuda(), bits)
+    table = torch.full((60, 3), -1, dtype=torch.int32, device="cuda")
+    ctx = torch.zeros(60, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = api.sv_cache_reserve(cache, table, ctx, status=status).cpu()
+    assert int(status) == api.SV_DATA_NO_PAGES and got.tolist() == [1] * 51 + [0] * 9
+    assert table[:51, 0].cpu().tolist() == sorted(set(free)) and int((cache.page_ref != 1).sum()) == 0
+
+
+@pytest.mark.gpu
+def test_append_from_a_wider_projection(cuda_lib):
+    """k_new and v_new as slices of one projection's output: rows with a stride."""
+    r = Rig(page=4, n=3, n_pages=20, H=2, D=64)
+    cu = r.i32([0, 2, 2, 5])
+    api.sv_cache_reserve(*r.args(), cu)
+    qkv = torch.randn(8, 3, 2, 64, device="cuda").to(r.dtype)
+    for layer in range(r.L):
+        api.sv_cache_append(r.cache, layer, qkv[:, 1], qkv[:, 2], r.table, r.ctx, cu, status=r.status)
+    assert r.bits() == 0
+    row = 0
+    for b, n in enumerate((3, 1, 4)):
+        for t in range(n):
+            p = int(r.table[b, t // 4])
+            for layer in range(r.L):
+                assert torch.equal(r.cache.k[layer, p, t % 4], qkv[row, 1]) and torch.equal(r.cache.v[layer, p, t % 4], qkv[row, 2])
+            row += 1
+    with pytest.raises(ValueError):
+        api.sv_cache_append(r.cache, 0, qkv[:, 1], qkv[:, 2].contiguous(), r.table, r.ctx, cu)
+    with pytest.raises(ValueError):
+        api.sv_cache_append(r.cache, 0, qkv[:, 1].float(), qkv[:, 2].float(), r.table, r.ctx, cu)
+
+
+@pytest.mark.gpu
 def test_largest_batch_of_reserve(cuda_lib):
     n = api.SV_CACHE_MAX_SEQS
     k = torch.zeros(1, n + 40, 2, 1, 8, device="cuda")
