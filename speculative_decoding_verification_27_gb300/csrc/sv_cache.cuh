@@ -104,9 +104,9 @@ __device__ __forceinline__ int page_slot(const CacheView& C, int t) {
   return (int)(((unsigned long long)(uint32_t)t * C.div_mul) >> C.div_shift);
 }
 
-// A length that fits its table (and 31 bits with the window).
+// A length that fits its table, and 31 bits with the rest of a tile.
 __device__ __forceinline__ bool length_ok(const CacheView& C, const SeqView& S, long long len) {
-  return len >= 0 && len <= (long long)S.width * C.page_size && len <= 0x7fffffffll;
+  return len >= 0 && len <= (long long)S.width * C.page_size && len <= 0x7fff0000ll;
 }
 
 }  // namespace sv
