@@ -390,8 +390,8 @@ __global__ void __launch_bounds__(Shape<D, WM>::kT, Shape<D, WM>::kCtas) window_
                                                                 (long long)(cp.u.head * P.group + h) * (D * 2)) + (lane & 3);
 #pragma unroll
         for (int k = 0; k < KD; ++k) {
-          q[k][e] = ok ? (__ldg(src + k * 8) & P.q_mask) ^ P.q_sign : 0u;
-          q[k][e + 2] = ok ? (__ldg(src + k * 8 + 4) & P.q_mask) ^ P.q_sign : 0u;
+          q[k][e] = ok ? (src[k * 8] & P.q_mask) ^ P.q_sign : 0u;
+          q[k][e + 2] = ok ? (src[k * 8 + 4] & P.q_mask) ^ P.q_sign : 0u;
         }
         m_run[e] = -INFINITY;
         l_run[e] = 0.f;
@@ -1242,7 +1242,7 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
         qv[j] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (x < MT * D / 4 && r < rows) {
           const int w = r / P.group, h = cp.u.head * P.group + (r - w * P.group);
-          qv[j] = __ldg(reinterpret_cast<const float4*>(P.q + (long long)(cp.u.w.r0 + w) * P.q_row_b + (long long)h * (D * 4)) + x % (D / 4));
+          qv[j] = reinterpret_cast<const float4*>(P.q + (long long)(cp.u.w.r0 + w) * P.q_row_b + (long long)h * (D * 4))[x % (D / 4)];
         }
       }
 #pragma unroll

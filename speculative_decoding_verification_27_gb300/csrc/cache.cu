@@ -393,6 +393,8 @@ __global__ void __launch_bounds__(kT) append_kernel(CacheView C, SeqView S, Wind
                                                     long long new_row_b, uint32_t* status) {
   release_stream();
   wait_for_stream();
+  k_new = behind_wait(k_new);
+  v_new = behind_wait(v_new);
   const int lane = threadIdx.x & 31, vecs = C.head_bytes / 16, n_vec = C.n_heads * vecs;
   const int warp0 = blockIdx.x * (kT / 32) + (threadIdx.x >> 5), step = gridDim.x * (kT / 32);
   const bool whole = C.head_b == C.head_bytes;  // a token's heads lie together
@@ -414,8 +416,8 @@ __global__ void __launch_bounds__(kT) append_kernel(CacheView C, SeqView S, Wind
 #pragma unroll
         for (int j = 0; j < kIn; ++j) {
           if (x0 + j * 32 + lane >= n_vec) break;
-          kv[0][j] = ld_stream16(k_from + from + j * 512);
-          kv[1][j] = ld_stream16(v_from + from + j * 512);
+          kv[0][j] = ld_once16(k_from + from + j * 512);
+          kv[1][j] = ld_once16(v_from + from + j * 512);
         }
       };
       for (long long r0 = warp0; r0 < w.rows; r0 += 32ll * step) {

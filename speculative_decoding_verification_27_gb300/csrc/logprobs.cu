@@ -22,15 +22,14 @@
 // the hits and cost more than they did, and raising it less often did too.
 //
 // Bound by the bytes for long rows: 2048 rows of V = 151936 bf16 without
-// alternatives take 113 us (81% of the copy rate), with 20 of them 148; the
-// benchmark batch's 1150 committed rows with rank and 20 alternatives 89 us
+// alternatives take 113 us (81% of the copy rate), with 20 of them 140; the
+// benchmark batch's 1150 committed rows with rank and 20 alternatives 92 us
 // (52 us of bytes). A row's end is a chain of short steps (about 10 us beside
 // three other rows on the SM): it weighs on short rows, 2816 rows of V = 32000
-// bf16 taking 49 us without and 75 with alternatives (27 us of bytes). Four
+// bf16 taking 50 us without and 74 with alternatives (27 us of bytes). Four
 // CTAs an SM with four loads a batch beat 3 and 5 CTAs and 2 to 8 loads.
 #include "../../include/spec_verify.h"
 #include "sv_device.cuh"
-#include "sv_launch.cuh"
 
 #include <cfloat>
 #include <climits>
@@ -330,20 +329,6 @@ struct Smem {
   int n, n2;
 };
 
-// Places for n entries a lane in a list of *count entries: the lane's first.
-__device__ __forceinline__ int warp_place(int n, int* count) {
-  const int lane = threadIdx.x & 31;
-  int x = n;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kFull, x, o);
-    if (lane >= o) x += y;
-  }
-  int first = 0;
-  if (lane == 31 && x) first = atomicAdd(count, x);
-  return __shfl_sync(kFull, first, 31) + x - n;
-}
-
 // n elements of the row reach the least of the warps' floors.
 __device__ __forceinline__ float shared_floor(const Smem& sm) {
   float f = sm.floor_w[0];
@@ -418,8 +403,6 @@ __global__ void __launch_bounds__(kThreads, SV_LP_CTAS) logprobs_kernel(Params P
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = cl > 1 ? (int)cluster_rank() : 0;
   const int r = cl > 1 ? blockIdx.x / cl : blockIdx.x;
-  release_stream();
-  wait_for_stream();
   if (blockIdx.x == 0) check_offsets(P, tid);
   if (P.cu && !row_wanted(P, r, find_request(P.cu, P.B, r))) return;  // all CTAs of the row alike
   const int V = P.V, n_top = P.n_top;
@@ -504,20 +487,17 @@ __global__ void __launch_bounds__(kThreads, SV_LP_CTAS) logprobs_kernel(Params P
           floor = fmaxf(floor, warp_nth_largest(m, n_top));
           hit = hit && bm >= floor;
         }
-        // The warp's vectors that reach it, one addition to the count for all of them.
-        uint32_t mine = 0;
+        if (hit) {  // (one addition a warp, places by a scan over its lanes: 3% slower)
 #pragma unroll
-        for (int u = 0; u < kU; ++u) mine |= (uint32_t)(hit && max_value<DT>(vm[u]) >= floor) << u;
-        int k = warp_place(__popc(mine), &sm.n);
-#pragma unroll
-        for (int u = 0; u < kU; ++u)
-          if (mine >> u & 1u) {
-            if (k < kVecs) {
-              sm.vec[k] = cur[u];
-              sm.vec_at[k] = at + u * kThreads + tid;
+          for (int u = 0; u < kU; ++u)
+            if (max_value<DT>(vm[u]) >= floor) {
+              const int k = atomicAdd(&sm.n, 1);
+              if (k < kVecs) {
+                sm.vec[k] = cur[u];
+                sm.vec_at[k] = at + u * kThreads + tid;
+              }
             }
-            ++k;
-          }
+        }
         __syncwarp();
         if (!first) {
           const float w = warp_nth_largest(m, q);
@@ -570,25 +550,16 @@ __global__ void __launch_bounds__(kThreads, SV_LP_CTAS) logprobs_kernel(Params P
     const int c = sm.n;
     if (c <= kVecs) {
       // What reached the last floor, in any order: the sort below does not depend on it.
-      for (int i0 = warp * 32; i0 < c; i0 += kThreads) {
-        const int i = i0 + lane;
+      for (int i = tid; i < c; i += kThreads) {
         float f[EPV];
-        uint32_t mine = 0;
-        if (i < c) {
-          Elem<DT>::unpack(sm.vec[i], f);
+        Elem<DT>::unpack(sm.vec[i], f);
+        const int x0 = sm.vec_at[i] * EPV - off;
 #pragma unroll
-          for (int j = 0; j < EPV; ++j) mine |= (uint32_t)(f[j] >= floor && f[j] > -INFINITY) << j;
-        }
-        int k = warp_place(__popc(mine), &sm.n2);
-        if (mine) {
-          const int x0 = sm.vec_at[i] * EPV - off;
-#pragma unroll
-          for (int j = 0; j < EPV; ++j)
-            if (mine >> j & 1u) {
-              if (k < kCap - 1) sm.cand[k] = make_key(f[j], x0 + j);
-              ++k;
-            }
-        }
+        for (int j = 0; j < EPV; ++j)
+          if (f[j] >= floor && f[j] > -INFINITY) {
+            const int k = atomicAdd(&sm.n2, 1);
+            if (k < kCap - 1) sm.cand[k] = make_key(f[j], x0 + j);
+          }
       }
       __syncthreads();
     }
@@ -750,8 +721,20 @@ extern "C" sv_status sv_token_logprobs(const void* logits, sv_dtype dtype, int32
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const int cl = lp::cluster_size(R, (long long)V * es);
   if ((long long)R * cl > INT32_MAX) return SV_ERR_INVALID_ARG;
-  const cudaError_t e =
-      dtype == SV_BF16 ? launch_overlapped(lp::logprobs_kernel<1>, dim3((unsigned)(R * cl)), kThreads, 0, (unsigned)cl, st, P, cl)
-                       : launch_overlapped(lp::logprobs_kernel<0>, dim3((unsigned)(R * cl)), kThreads, 0, (unsigned)cl, st, P, cl);
+  // An ordinary launch: the rows are streamed by read-only loads (3% faster than others here), which a launch that overlaps the
+  // kernel before it may not use.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(R * cl));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cl;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cl > 1 ? 1 : 0;
+  cudaError_t e = dtype == SV_BF16 ? cudaLaunchKernelEx(&cfg, lp::logprobs_kernel<1>, P, cl)
+                                   : cudaLaunchKernelEx(&cfg, lp::logprobs_kernel<0>, P, cl);
+  if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }

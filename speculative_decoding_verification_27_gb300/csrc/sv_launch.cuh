@@ -16,6 +16,22 @@ namespace sv {
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void release_stream() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Such a kernel may have started while the one before it still wrote, so its
+// inputs are not read-only for its lifetime: they are read by ordinary loads
+// (not .nc, not __ldg), through a pointer that only exists behind the wait, so
+// that no load moves ahead of it.
+template <typename T>
+__device__ __forceinline__ const T* behind_wait(const T* p) {
+  asm volatile("" : "+l"(p)::"memory");
+  return p;
+}
+// 16 bytes that are read once.
+__device__ __forceinline__ uint4 ld_once16(const void* p) {
+  uint4 v;
+  asm("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 template <typename... K, typename... A>
 cudaError_t launch_overlapped(void (*kernel)(K...), dim3 grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t st,
                               A... args) {
