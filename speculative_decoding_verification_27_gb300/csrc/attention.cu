@@ -979,28 +979,25 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
           auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; };
           see &= hi < -c.u.ctx ? 0ull : below(-at0) | (below(hi + 1 - at0) & ~below(max(lo, 0) - at0));
         }
-        uint32_t s[32];
-        auto load = [&](int h) {
-          tc_ld32(s, s_addr + h * 32);
-          tc_wait_ld();
-          if (masked) {
+        uint32_t s[2][32];
+        tc_ld32(s[0], s_addr);
+        tc_ld32(s[1], s_addr + 32);
+        tc_wait_ld();
+        if (masked) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
             const uint32_t bits = (uint32_t)(see >> (h * 32));
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (!(bits & 1u << j)) s[j] = 0xff800000u;
+              if (!(bits & 1u << j)) s[h][j] = 0xff800000u;
           }
-        };
-        float top = -INFINITY;
-#pragma unroll
-        for (int h = 1; h >= 0; --h) {
-          load(h);
-          float most[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) most[j] = fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 4]));
-#pragma unroll
-          for (int j = 8; j < 32; ++j) most[j & 3] = fmaxf(most[j & 3], __uint_as_float(s[j]));
-          top = fmaxf(top, fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])));
         }
+        float most[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) most[j] = fmaxf(__uint_as_float(s[0][j]), __uint_as_float(s[1][j]));
+#pragma unroll
+        for (int j = 4; j < 32; ++j) most[j & 3] = fmaxf(most[j & 3], fmaxf(__uint_as_float(s[0][j]), __uint_as_float(s[1][j])));
+        const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
         // The reference moves where the maximum is 2^8 above it. Before a row's first token there is nothing to rescale.
         float f = 1.f;
         if (m == -INFINITY) {
@@ -1018,11 +1015,10 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
         f2_t sum = 0ull;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (h) load(h);
           uint32_t p[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const f2_t e = f2_ex2(f2_fma(f2_pack(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), sl, neg));
+            const f2_t e = f2_ex2(f2_fma(f2_pack(__uint_as_float(s[h][2 * j]), __uint_as_float(s[h][2 * j + 1])), sl, neg));
             sum = f2_add(sum, e);
             float a, b;
             f2_unpack(e, a, b);
