@@ -12,13 +12,14 @@
 // by the type and by the windows' mean number of stacked rows (64 requests of
 // 4096 tokens, 8 key-value heads, one token to 32 of them; the copy rate would
 // read heads of 128 in 159 us, of 64 in 79):
-//   bf16, up to 16, 32, 64 rows   window_mma_kernel: 191-200 us for heads of
-//     128 (5.3 - 5.6 TB/s) up to 32 rows, 265 us for 64; heads of 64: 118-128
-//     and 172 us;
-//   bf16, more rows               window_tc_kernel, tiles of 128 rows: 280 us
-//     (heads of 128) and 170 us (of 64) for 128 rows, where the other took
-//     476 and 293 us. At 64 rows its tiles would be half empty and it takes
-//     as long as for 128: no gain;
+//   bf16, up to 16 or 32 rows, and up to 64 with heads of 128
+//     window_mma_kernel: 193-198 us for heads of 128 (5.4 - 5.6 TB/s) up to
+//     32 rows, 256 us for 64; heads of 64: 119-126 us;
+//   bf16, more rows
+//     window_tc_kernel, tiles of 128 rows: 271 us (heads of 128) and 142 us (of
+//     64) for 128 rows, where the other took 476 and 293 us. With 64 rows its
+//     tiles are half empty and it takes as long: heads of 64 140 us against
+//     158, heads of 128 271 against 256;
 //   fp32, up to 4, 8, 16 rows     window_fma_kernel.
 // Sums of a split request are joined by join_kernel.
 #include "sv_cache.cuh"
@@ -266,12 +267,12 @@ constexpr size_t part_bytes() {
 template <int D, int WM>
 struct Shape {
   static constexpr int MT = 16 * WM;            // stacked rows of a unit
-  static constexpr int WK = WM < 4 ? 4 / WM : 1;  // warps that split a key tile
+  static constexpr int WK = 4 / WM;             // warps that split a key tile
   static constexpr int kT = 32 * WM * WK;       // threads
   static constexpr int KW = kTK / WK;           // tokens of a tile for one warp
   static constexpr int KS = KW < 32 ? KW : 32;  // tokens that go through the softmax at once
-  static constexpr int kCtas = D == 64 ? (WM <= 2 ? 4 : WM == 4 ? 3 : 2) : (WM <= 4 ? 2 : 1);  // an SM
-  static constexpr int kStages = D == 64 ? (WM <= 2 ? 3 : WM == 4 ? 4 : 6) : (WM <= 4 ? 3 : 5);
+  static constexpr int kCtas = D == 64 ? 4 : 2;   // an SM
+  static constexpr int kStages = 3;
   static constexpr int kTile = kTK * D * 2;     // bytes of K (or V) of a tile
   static constexpr size_t smem = (size_t)kStages * 2 * kTile + (kStages + 1) * (kTK * 8 + 16);
   static_assert(kCtas * MT <= 256, "the workspace has room for the partial results");
@@ -1369,18 +1370,30 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
 }
 
 // Joins the parts of a unit that several CTAs share. Block c takes the unit
-// that CTA c's share cuts at its end, if it began there; blockIdx.y takes
-// every gridDim.y-th row. Groups of D / 4 threads (a thread holds 4 elements)
-// take every kG-th part, four parts' loads in flight, and the groups' sums
-// are joined in order. The block is launched while the parts are still being
-// computed and waits for them.
+// that CTA c's share cuts at its end, if it began there. A group of D / 4
+// threads holds a row, 4 elements a thread, with four parts' loads in flight.
+// A unit of up to four parts has a row to each group, and no barrier; one of
+// more parts (a long request on an otherwise idle machine) has its parts dealt
+// to the groups of a block, whose sums are joined in order. The block is
+// brought up while the parts are still being computed and waits for them.
 constexpr int kJoinT = 128;
+
+struct RowSum {
+  float m, l;
+  float4 o;
+};
+__device__ __forceinline__ void add_row(RowSum& a, float m, float l, const float4& o, float scale) {
+  const float top = fmaxf(a.m, m), fa = factor(a.m, top, scale), fb = factor(m, top, scale);
+  a.m = top;
+  a.l = fmaf(l, fb, a.l * fa);
+  a.o = make_float4(fmaf(o.x, fb, a.o.x * fa), fmaf(o.y, fb, a.o.y * fa), fmaf(o.z, fb, a.o.z * fa), fmaf(o.w, fb, a.o.w * fa));
+}
+
 template <int DT, int D, int MT>
 __global__ void __launch_bounds__(kJoinT) join_kernel(Params P, Plan L, int grid) {
   const float scale = DT == 1 ? P.scale_log2 : 1.f;  // of the maxima: the fp32 kernel's scores are scaled
   constexpr int TPR = D / 4, kG = kJoinT / TPR;
-  __shared__ float4 s_o[kG][TPR];
-  __shared__ float2 s_ml[kG];
+  __shared__ RowSum s_sum[kG][TPR];
   release_stream();
   wait_for_stream();
   const int c = blockIdx.x;
@@ -1388,68 +1401,60 @@ __global__ void __launch_bounds__(kJoinT) join_kernel(Params P, Plan L, int grid
   if (cut.x < 0 || cut.x >= P.S.n) return;
   const int head = cut.y, mt = cut.z, last = min(cut.w, grid - 1);
   const Window w = find_window(P.W, cut.x);
-  const int rows = w.rows * P.group;
+  const int rows = min(MT, w.rows * P.group - mt * MT);  // of this row tile
   const int g = threadIdx.x / TPR, lane_d = threadIdx.x % TPR;
-  for (int r = blockIdx.y; r < MT; r += gridDim.y) {
-    const int x = mt * MT + r;
-    if (x >= rows) break;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = c + g; k0 <= last; k0 += kG * 4) {
-      float pm[4], pl[4];
-      float4 y[4];
+  // Row r of parts k0, k0 + step, ... (four of them at most).
+  auto add_parts = [&](RowSum& sum, int r, int k0, int step) {
+    float m[4], l[4];
+    float4 o[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = k0 + j * kG;
-        pm[j] = -INFINITY;
-        pl[j] = 0.f;
-        y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k <= last) {
-          const float* part = reinterpret_cast<const float*>(L.part + (size_t)(k * 2 + (k == c)) * part_bytes<D, MT>());
-          pm[j] = part[MT * D + r];
-          pl[j] = part[MT * D + MT + r];
-          y[j] = *reinterpret_cast<const float4*>(part + r * D + lane_d * 4);
-        }
+    for (int j = 0; j < 4; ++j) {
+      const int k = k0 + j * step;
+      m[j] = -INFINITY;
+      l[j] = 0.f;
+      o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k <= last) {
+        const float* part = reinterpret_cast<const float*>(L.part + (size_t)(k * 2 + (k == c)) * part_bytes<D, MT>());
+        m[j] = part[MT * D + r];
+        l[j] = part[MT * D + MT + r];
+        o[j] = *reinterpret_cast<const float4*>(part + r * D + lane_d * 4);
       }
-      float top = m;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) top = fmaxf(top, pm[j]);
-      const float fa = factor(m, top, scale);
-      l *= fa;
-      o = make_float4(o.x * fa, o.y * fa, o.z * fa, o.w * fa);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float f = factor(pm[j], top, scale);
-        l = fmaf(pl[j], f, l);
-        o = make_float4(fmaf(y[j].x, f, o.x), fmaf(y[j].y, f, o.y), fmaf(y[j].z, f, o.z), fmaf(y[j].w, f, o.w));
-      }
-      m = top;
     }
-    s_o[g][lane_d] = o;
-    if (lane_d == 0) s_ml[g] = make_float2(m, l);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) add_row(sum, m[j], l[j], o[j], scale);
+  };
+  auto write = [&](const RowSum& sum, int r) {
+    const int x = mt * MT + r, ww = x / P.group, h = head * P.group + (x - ww * P.group);
+    const float inv = sum.l > 0.f ? 1.f / sum.l : 0.f;
+    const float4 o = make_float4(sum.o.x * inv, sum.o.y * inv, sum.o.z * inv, sum.o.w * inv);
+    char* dst = P.out + (long long)(w.r0 + ww) * P.out_row_b + ((long long)h * D + lane_d * 4) * Elem<DT>::kBytes;
+    if constexpr (DT == 1)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+    else
+      *reinterpret_cast<float4*>(dst) = o;
+    if (P.lse && lane_d == 0) P.lse[(long long)(w.r0 + ww) * (P.C.n_heads * P.group) + h] = lse_of(sum.m, sum.l, scale);
+  };
+  const RowSum none{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (last - c < 4) {
+    for (int r = blockIdx.y * kG + g; r < rows; r += gridDim.y * kG) {
+      RowSum sum = none;
+      add_parts(sum, r, c, 1);
+      write(sum, r);
+    }
+    return;
+  }
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    RowSum sum = none;
+    for (int k0 = c + g; k0 <= last; k0 += kG * 4) add_parts(sum, r, k0, kG);
+    s_sum[g][lane_d] = sum;
     __syncthreads();
     if (g == 0) {
-      float top = m;
 #pragma unroll
-      for (int j = 1; j < kG; ++j) top = fmaxf(top, s_ml[j].x);
-      l = 0.f;
-      o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int j = 0; j < kG; ++j) {
-        const float2 ml = s_ml[j];
-        const float4 y = s_o[j][lane_d];
-        const float f = factor(ml.x, top, scale);
-        l = fmaf(ml.y, f, l);
-        o = make_float4(fmaf(y.x, f, o.x), fmaf(y.y, f, o.y), fmaf(y.z, f, o.z), fmaf(y.w, f, o.w));
+      for (int j = 1; j < kG; ++j) {
+        const RowSum y = s_sum[j][lane_d];
+        add_row(sum, y.m, y.l, y.o, scale);
       }
-      const int ww = x / P.group, h = head * P.group + (x - ww * P.group);
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      char* dst = P.out + (long long)(w.r0 + ww) * P.out_row_b + ((long long)h * D + lane_d * 4) * Elem<DT>::kBytes;
-      if constexpr (DT == 1)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-      else
-        *reinterpret_cast<float4*>(dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-      if (P.lse && lane_d == 0) P.lse[(long long)(w.r0 + ww) * (P.C.n_heads * P.group) + h] = lse_of(top, l, scale);
+      write(sum, r);
     }
     __syncthreads();
   }
@@ -1466,7 +1471,7 @@ cudaError_t launch_shares(void (*kernel)(Params, Plan), const Params& P, const P
   cudaError_t e = allow_smem(kernel, Sh::smem, allowed);
   if (e == cudaSuccess) e = launch_overlapped(kernel, dim3(grid), Sh::kT, Sh::smem, 1, st, P, L);
   if (e == cudaSuccess)
-    e = launch_overlapped(join_kernel<DT, D, Sh::MT>, dim3(grid, Sh::MT < 16 ? Sh::MT : 16), kJoinT, 0, 1, st, P, L, grid);
+    e = launch_overlapped(join_kernel<DT, D, Sh::MT>, dim3(grid, Sh::MT <= 16 ? 4 : Sh::MT <= 64 ? 8 : 16), kJoinT, 0, 1, st, P, L, grid);
   return e;
 }
 template <int D, int WM>
@@ -1552,7 +1557,6 @@ sv_status sv_window_attention(const void* q, int64_t q_stride, int32_t n_q_heads
     else
       e = rows <= 16   ? att::launch_mma<64, 1>(P, L, st)
           : rows <= 32 ? att::launch_mma<64, 2>(P, L, st)
-          : rows <= 64 ? att::launch_mma<64, 4>(P, L, st)
                        : att::launch_tc<64>(P, L, st);
   } else if (D == 128) {
     e = rows <= 4 ? att::launch_fma<128, 4>(P, L, st) : rows <= 8 ? att::launch_fma<128, 8>(P, L, st) : att::launch_fma<128, 16>(P, L, st);
