@@ -1144,42 +1144,65 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
 // ---------------------------------------------------------------------------
 template <int D, int M>
 struct Shape32 {
-  static constexpr int MT = M;
-  static constexpr int kT = 128;
-  static constexpr int kPitch = D * 4 + 16;        // bytes of a row in shared memory: rows of one column lie in different banks
-  static constexpr int kTile = kTK * kPitch;
-  static constexpr int kStages = 2;
-  static constexpr int kCtas = D == 64 ? 3 : 1;    // an SM
-  static constexpr int SP = kTK + 4;               // row pitch of the scores, in floats
-  static constexpr size_t smem = (size_t)kStages * 2 * kTile + (size_t)MT * D * 4 + (size_t)MT * SP * 4 + MT * 16 + kStages * kTK * 8;
+  static constexpr int MT = M;                        // stacked rows of a unit: 4, 8, 16 or 32
+  static constexpr int kT = 128;                      // threads
+  static constexpr int RT = M < 8 ? M : 8;            // rows of a thread's tile, of scores and of the output
+  static constexpr int KT = 4;                        // keys of its tile of scores
+  static constexpr int KG = kTK / KT;                 // groups of threads over the keys
+  static constexpr int DP = kT / KG / (M / RT);       // threads that split the sum of a score
+  static constexpr int WR = M / RT;                   // warps side by side over the rows of the output
+  static constexpr int WK = 4 / WR;                   // and over the tokens
+  static constexpr int LK = 128 / D;                  // parts of a warp that split its tokens
+  static constexpr int kPitch = D * 4 + DP % 8 * 16;  // bytes of a K row: the threads of a quarter warp read different banks
+  static constexpr int SP = kTK + 4;                  // row pitch of the scores, in floats
+  static constexpr int kK = kTK * kPitch, kV = kTK * D * 4;
+  static constexpr int kCtas = D == 64 ? (M <= 8 ? 4 : 3) : (M <= 8 ? 3 : 2);  // an SM
+  static constexpr size_t smem = (size_t)kK + kV + (size_t)M * D * 4 + (size_t)M * SP * 4 + M * 16 + 2 * kTK * 8;
+  static_assert((WK - 1) * M * D * 4 <= kV, "the sums of the other warps fit the tile of V");
 };
 
-// Bound by its instructions and latencies, not by its bytes: 64 requests of
-// 1000 tokens, 8 heads of 64, windows of 4 rows take 70 us (39 us of bytes),
-// 37 ragged windows over 0 - 1000 tokens 33 us a call. Row tiles of 4, 8 or 16.
-// A tile's scores: thread (token, half of the rows) walks d. Its softmax: a
-// warp takes every fourth row. Its product with V: thread (d, share of the
-// tokens) holds every row's sum.
+// N values of each of DP / X threads summed over them: every exchange adds one half of them to the same half of another
+// thread's, and thread i is left with the part that its bits from X on name.
+template <int N, int X, int DP>
+__device__ __forceinline__ void sum_halves(float* s, int i) {
+  if constexpr (X < DP) {
+    const bool up = i & X;
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+      const float give = up ? s[e] : s[e + N / 2], keep = up ? s[e + N / 2] : s[e];
+      s[e] = keep + __shfl_xor_sync(kFull, give, X);
+    }
+    sum_halves<N / 2, X * 2, DP>(s, i);
+  }
+}
+
 template <int D, int MT>
 __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(Params P, Plan L) {
   using Sh = Shape32<D, MT>;
-  constexpr int S = Sh::kStages, SP = Sh::SP, RH = MT / 2, KH = 128 / D, CPR = D / 4;
+  constexpr int SP = Sh::SP, RT = Sh::RT, KT = Sh::KT, KG = Sh::KG, DP = Sh::DP, CPR = D / 4;
+  constexpr int NR = RT >= DP ? RT / DP : 1;   // rows and keys of the scores that a thread is left with
+  constexpr int NK = RT * KT / DP / NR;
+  constexpr int TV = kTK / Sh::WK / Sh::LK;    // tokens of a thread's share of the product with V
   extern __shared__ __align__(1024) char smem[];
-  char* s_kv = smem;
-  float* s_q = reinterpret_cast<float*>(smem + S * 2 * Sh::kTile);  // [MT][D]
-  float* s_p = s_q + MT * D;                                        // [MT][SP]
-  float* s_m = s_p + MT * SP;                                       // [MT] maximum, sum, factor of the tile, free
+  char* s_k = smem;
+  char* s_v = smem + Sh::kK;
+  float* s_q = reinterpret_cast<float*>(s_v + Sh::kV);            // [MT][D]
+  float* s_p = s_q + MT * D;                                      // [MT][SP]
+  float* s_m = s_p + MT * SP;                                     // [MT] maximum, sum, factor of the tile, free
   float* s_l = s_m + MT;
   float* s_f = s_l + MT;
-  long long* s_off = reinterpret_cast<long long*>(s_f + 2 * MT);    // [S][kTK]
+  long long* s_off = reinterpret_cast<long long*>(s_f + 2 * MT);  // [2][kTK]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Share sh;
   Cursor ld;
   if (!take_share<MT, 128>(P, L, sh, ld)) return;
   const int n_tiles = (int)(sh.t1 - sh.t0);
   Cursor cp = ld;
-  const int key = tid % kTK, half = tid / kTK;
-  const int d_own = tid % D, kh = tid / D;
+  // Scores: rows row0 .. row0 + RT - 1, keys key0 + KG j, every DP-th piece of d.
+  const int dp = tid % DP, key0 = tid / DP % KG, row0 = tid / (DP * KG) * RT;
+  // Output: rows orow .. orow + RT - 1, four elements from d0 on, tokens t0 .. t0 + TV - 1.
+  const int d0 = lane % (32 / Sh::LK) * 4, lk = lane / (32 / Sh::LK);
+  const int orow = warp % Sh::WR * RT, wk = warp / Sh::WR, t0 = (wk * Sh::LK + lk) * TV;
 
   // A token of the loading cursor's tile: its page, looked up a tile ahead of the copy.
   int page = -2, place = 0;
@@ -1192,38 +1215,54 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
       page = P.S.table[(long long)ld.u.b * P.S.stride + slot];
     }
   };
-  lookup();
-  // The offsets of the loading cursor's tile, the tile itself, and the next one's lookup.
-  auto load_tile = [&](int n) {
+  // The offsets of tile n, and the next one's lookup.
+  auto resolve = [&](int n) {
     if (tid < kTK) {
       const bool ok = page >= 0 && page < P.C.n_pages;
       if (!ok && page != -2) set_status(P.status, SV_DATA_BAD_PAGE);
-      s_off[n % S * kTK + tid] = ok ? page * P.C.page_b + place * P.C.token_b + ld.u.head * P.C.head_b : -1;
+      s_off[n % 2 * kTK + tid] = ok ? page * P.C.page_b + place * P.C.token_b + ld.u.head * P.C.head_b : -1;
     }
-    __syncthreads();
-    const uint32_t base = smem_addr(s_kv) + (n % S) * 2 * Sh::kTile;
-    for (int x = tid; x < kTK * CPR; x += 128) {
-      const int r = x / CPR, c = x % CPR;
-      const long long off = s_off[n % S * kTK + r];
-      const long long at = (off < 0 ? 0 : off) + c * 16;
-      cp16(base + r * Sh::kPitch + c * 16, P.C.k + at, off >= 0);
-      cp16(base + Sh::kTile + r * Sh::kPitch + c * 16, P.C.v + at, off >= 0);
-    }
-    cp_commit();
     if (n + 1 < n_tiles) {
       if (++ld.tile == ld.u.tiles) next_unit<MT>(P, ld);
       lookup();
     }
   };
-  for (int i = 0; i < S - 1; ++i) {
-    if (i < n_tiles)
-      load_tile(i);
-    else
-      cp_commit();
-  }
+  auto copy = [&](int n, const char* from, char* to, int pitch) {
+    if (n < n_tiles) {
+      const uint32_t base = smem_addr(to) + tid % CPR * 16;
+      const char* src = from + tid % CPR * 16;
+#pragma unroll
+      for (int j = 0; j < kTK * CPR / 128; ++j) {
+        const int r = tid / CPR + j * (128 / CPR);
+        const long long off = s_off[n % 2 * kTK + r];
+        cp16(base + r * pitch, src + (off < 0 ? 0 : off), off >= 0);
+      }
+    }
+    cp_commit();
+  };
+  lookup();
+  resolve(0);
+  __syncthreads();
+  copy(0, P.C.k, s_k, Sh::kPitch);
+  copy(0, P.C.v, s_v, D * 4);
 
-  float o[MT];
-  int lo[RH], hi[RH];
+  float4 o[RT];
+  int lo[NR], hi[NR];
+  // The thread's rows of the scores it is left with: each halving over the DP threads takes a bit of dp, rows first.
+  int my_row = row0, my_key = 0;
+  {
+    int nr = RT, nk = KT;
+#pragma unroll
+    for (int x = 1; x < DP; x <<= 1) {
+      if (nr > 1) {
+        nr /= 2;
+        if (dp & x) my_row += nr;
+      } else {
+        nk /= 2;
+        if (dp & x) my_key += nk;
+      }
+    }
+  }
   bool begun = false, from_start = false;
   for (int i = 0; i < n_tiles; ++i) {
     if (i + 1 == n_tiles) release_stream();
@@ -1250,51 +1289,60 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
         s_l[tid] = 0.f;
       }
 #pragma unroll
-      for (int e = 0; e < RH; ++e) {
-        const int r = cp.u.mt * MT + half * RH + e;
+      for (int e = 0; e < NR; ++e) {
+        const int r = cp.u.mt * MT + my_row + e;
         const int w = r < rows ? r / P.group : 0;
         lo[e] = r < rows ? candidate_start(P, cp.u.w, w) : 0;
         hi[e] = r < rows ? w : -1 - cp.u.ctx;
       }
 #pragma unroll
-      for (int r = 0; r < MT; ++r) o[r] = 0.f;
+      for (int r = 0; r < RT; ++r) o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    cp_wait<S - 2>();
-    __syncthreads();  // the tile has landed; the stage before it is free
-    if (i + S - 1 < n_tiles)
-      load_tile(i + S - 1);
-    else
-      cp_commit();
-    const char* kt = s_kv + (i % S) * 2 * Sh::kTile;
-    const float* vt = reinterpret_cast<const float*>(kt + Sh::kTile);
+    if (i + 1 < n_tiles) resolve(i + 1);
+    cp_wait<1>();
+    __syncthreads();  // K has landed
 
     // Scores.
     {
-      float s[RH];
+      float s[RT * KT];
 #pragma unroll
-      for (int e = 0; e < RH; ++e) s[e] = 0.f;
-      const float4* kr = reinterpret_cast<const float4*>(kt + key * Sh::kPitch);
-      const float4* qr = reinterpret_cast<const float4*>(s_q + half * RH * D);
-#pragma unroll 4
-      for (int d = 0; d < D / 4; ++d) {
-        const float4 k4 = kr[d];
+      for (int e = 0; e < RT * KT; ++e) s[e] = 0.f;
+      const char* kr = s_k + key0 * Sh::kPitch + dp * 16;
+      const float4* qr = reinterpret_cast<const float4*>(s_q + row0 * D) + dp;
+#pragma unroll 2
+      for (int d = 0; d < CPR; d += DP) {
+        float4 k4[KT];
 #pragma unroll
-        for (int e = 0; e < RH; ++e) {
-          const float4 q4 = qr[e * (D / 4) + d];
-          s[e] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[e]))));
+        for (int j = 0; j < KT; ++j) k4[j] = *reinterpret_cast<const float4*>(kr + j * KG * Sh::kPitch + d * 16);
+#pragma unroll
+        for (int e = 0; e < RT; ++e) {
+          const float4 q4 = qr[e * CPR + d];
+#pragma unroll
+          for (int j = 0; j < KT; ++j) {
+            float& x = s[e * KT + j];
+            x = fmaf(q4.x, k4[j].x, fmaf(q4.y, k4[j].y, fmaf(q4.z, k4[j].z, fmaf(q4.w, k4[j].w, x))));
+          }
         }
       }
-      const int at = cp.tile * kTK + key - cp.u.ctx;
-      const bool page_ok = s_off[i % S * kTK + key] >= 0;
+      // The DP threads' sums joined: each exchange leaves a thread half of its scores.
+      sum_halves<RT * KT, 1, DP>(s, dp);
 #pragma unroll
-      for (int e = 0; e < RH; ++e) {
-        const bool see = page_ok && (at < 0 ? hi[e] >= -cp.u.ctx : at >= lo[e] && at <= hi[e]);
-        s_p[(half * RH + e) * SP + key] = see ? s[e] * P.scale_log2 : -INFINITY;
+      for (int j = 0; j < NK; ++j) {
+        const int key = key0 + (my_key + j) * KG, at = cp.tile * kTK + key - cp.u.ctx;
+        const bool page_ok = s_off[i % 2 * kTK + key] >= 0;
+#pragma unroll
+        for (int e = 0; e < NR; ++e) {
+          const bool see = page_ok && (at < 0 ? hi[e] >= -cp.u.ctx : at >= lo[e] && at <= hi[e]);
+          s_p[(my_row + e) * SP + key] = see ? s[e * NK + j] * P.scale_log2 : -INFINITY;
+        }
       }
     }
     __syncthreads();
+    copy(i + 1, P.C.k, s_k, Sh::kPitch);
     // Softmax of the rows, two tokens a lane.
-    for (int r = warp; r < MT; r += 4) {
+#pragma unroll
+    for (int e = 0; e < MT / 4; ++e) {
+      const int r = warp * (MT / 4) + e;
       const float a = s_p[r * SP + lane], b = s_p[r * SP + lane + 32];
       const float m0 = s_m[r], m = fmaxf(m0, warp_max(fmaxf(a, b)));
       const float off_m = m == -INFINITY ? 0.f : m;
@@ -1311,59 +1359,85 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
         s_m[r] = m;
       }
     }
-    __syncthreads();
+    cp_wait<1>();
+    __syncthreads();  // the weights are written and V has landed
     // The product with V.
 #pragma unroll
-    for (int r = 0; r < MT; ++r) o[r] *= s_f[r];
+    for (int r = 0; r < RT; ++r) {
+      const float f = s_f[orow + r];
+      o[r] = make_float4(o[r].x * f, o[r].y * f, o[r].z * f, o[r].w * f);
+    }
 #pragma unroll 2
-    for (int k = kh * (kTK / KH); k < (kh + 1) * (kTK / KH); k += 4) {
-      float v[4];
+    for (int k = t0; k < t0 + TV; k += 4) {
+      float4 v[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = vt[(k + j) * (Sh::kPitch / 4) + d_own];
+      for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float4*>(s_v + (k + j) * (D * 4) + d0 * 4);
 #pragma unroll
-      for (int r = 0; r < MT; ++r) {
-        const float4 p = *reinterpret_cast<const float4*>(s_p + r * SP + k);
-        o[r] = fmaf(p.x, v[0], fmaf(p.y, v[1], fmaf(p.z, v[2], fmaf(p.w, v[3], o[r]))));
+      for (int r = 0; r < RT; ++r) {
+        const float4 p = *reinterpret_cast<const float4*>(s_p + (orow + r) * SP + k);
+        o[r].x = fmaf(p.x, v[0].x, fmaf(p.y, v[1].x, fmaf(p.z, v[2].x, fmaf(p.w, v[3].x, o[r].x))));
+        o[r].y = fmaf(p.x, v[0].y, fmaf(p.y, v[1].y, fmaf(p.z, v[2].y, fmaf(p.w, v[3].y, o[r].y))));
+        o[r].z = fmaf(p.x, v[0].z, fmaf(p.y, v[1].z, fmaf(p.z, v[2].z, fmaf(p.w, v[3].z, o[r].z))));
+        o[r].w = fmaf(p.x, v[0].w, fmaf(p.y, v[1].w, fmaf(p.z, v[2].w, fmaf(p.w, v[3].w, o[r].w))));
       }
     }
+    __syncthreads();  // V is free
 
     const bool unit_end = cp.tile + 1 == cp.u.tiles;
     if (unit_end || i + 1 == n_tiles) {
       begun = false;
-      if constexpr (KH > 1) {  // the halves of the tokens, joined in the place of the scores (MT * D floats fit the tile just used)
-        float* buf = reinterpret_cast<float*>(const_cast<char*>(kt));
-        __syncthreads();
-        if (kh == 1)
+      if constexpr (Sh::LK > 1) {
 #pragma unroll
-          for (int r = 0; r < MT; ++r) buf[r * D + d_own] = o[r];
-        __syncthreads();
-        if (kh == 0)
+        for (int r = 0; r < RT; ++r) {
+          o[r].x += __shfl_xor_sync(kFull, o[r].x, 16);
+          o[r].y += __shfl_xor_sync(kFull, o[r].y, 16);
+          o[r].z += __shfl_xor_sync(kFull, o[r].z, 16);
+          o[r].w += __shfl_xor_sync(kFull, o[r].w, 16);
+        }
+      }
+      if constexpr (Sh::WK > 1) {  // the warps' shares of the tokens, joined in the place of V
+        float4* buf = reinterpret_cast<float4*>(s_v);
+        if (wk > 0 && lk == 0)
 #pragma unroll
-          for (int r = 0; r < MT; ++r) o[r] += buf[r * D + d_own];
+          for (int r = 0; r < RT; ++r) buf[((wk - 1) * MT + orow + r) * CPR + d0 / 4] = o[r];
+        __syncthreads();
+        if (wk == 0)
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int y = 0; y < Sh::WK - 1; ++y) {
+              const float4 z = buf[(y * MT + orow + r) * CPR + d0 / 4];
+              o[r] = make_float4(o[r].x + z.x, o[r].y + z.y, o[r].z + z.z, o[r].w + z.w);
+            }
+        __syncthreads();
       }
       const bool split = !from_start || !unit_end;
       if (tid == 0 && i + 1 == n_tiles) tell_cut(L, sh, cp, !unit_end && from_start);
-      if (kh == 0) {
+      if (wk == 0) {
         float* part = reinterpret_cast<float*>(L.part + (size_t)(blockIdx.x * 2 + (from_start ? 1 : 0)) * part_bytes<D, MT>());
 #pragma unroll
-        for (int r = 0; r < MT; ++r) {
-          const float m = s_m[r], l = s_l[r];
+        for (int r = 0; r < RT; ++r) {
+          if (r % Sh::LK != lk) continue;  // the parts of a warp write a row each
+          const float m = s_m[orow + r], l = s_l[orow + r];
           if (split) {
-            part[r * D + d_own] = o[r];
-            if (d_own == 0) {
-              part[MT * D + r] = m;
-              part[MT * D + MT + r] = l;
+            reinterpret_cast<float4*>(part + (orow + r) * D)[d0 / 4] = o[r];
+            if (d0 == 0) {
+              part[MT * D + orow + r] = m;
+              part[MT * D + MT + orow + r] = l;
             }
             continue;
           }
-          const int x = cp.u.mt * MT + r;
+          const int x = cp.u.mt * MT + orow + r;
           if (x >= rows) break;
           const int w = x / P.group, h = cp.u.head * P.group + (x - w * P.group);
-          reinterpret_cast<float*>(P.out + (long long)(cp.u.w.r0 + w) * P.out_row_b + (long long)h * (D * 4))[d_own] = l > 0.f ? o[r] / l : 0.f;
-          if (P.lse && d_own == 0) P.lse[(long long)(cp.u.w.r0 + w) * (P.C.n_heads * P.group) + h] = lse_of(m, l, 1.f);
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          reinterpret_cast<float4*>(P.out + (long long)(cp.u.w.r0 + w) * P.out_row_b + (long long)h * (D * 4))[d0 / 4] =
+              make_float4(o[r].x * inv, o[r].y * inv, o[r].z * inv, o[r].w * inv);
+          if (P.lse && d0 == 0) P.lse[(long long)(cp.u.w.r0 + w) * (P.C.n_heads * P.group) + h] = lse_of(m, l, 1.f);
         }
       }
     }
+    copy(i + 1, P.C.v, s_v, D * 4);
     if (++cp.tile == cp.u.tiles && i + 1 < n_tiles) next_unit<MT>(P, cp);
   }
   cp_wait<0>();
@@ -1489,6 +1563,13 @@ cudaError_t launch_fma(const Params& P, const Plan& L, cudaStream_t st) {
   static std::atomic<unsigned long long> allowed{0};
   return launch_shares<0, D, Shape32<D, M>>(window_fma_kernel<D, M>, P, L, st, allowed);
 }
+template <int D>
+cudaError_t launch_rows32(long long rows, const Params& P, const Plan& L, cudaStream_t st) {
+  return rows <= 4    ? launch_fma<D, 4>(P, L, st)
+         : rows <= 8  ? launch_fma<D, 8>(P, L, st)
+         : rows <= 16 ? launch_fma<D, 16>(P, L, st)
+                      : launch_fma<D, 32>(P, L, st);
+}
 
 }  // namespace att
 }  // namespace sv
@@ -1559,9 +1640,9 @@ sv_status sv_window_attention(const void* q, int64_t q_stride, int32_t n_q_heads
           : rows <= 32 ? att::launch_mma<64, 2>(P, L, st)
                        : att::launch_tc<64>(P, L, st);
   } else if (D == 128) {
-    e = rows <= 4 ? att::launch_fma<128, 4>(P, L, st) : rows <= 8 ? att::launch_fma<128, 8>(P, L, st) : att::launch_fma<128, 16>(P, L, st);
+    e = att::launch_rows32<128>(rows, P, L, st);
   } else {
-    e = rows <= 4 ? att::launch_fma<64, 4>(P, L, st) : rows <= 8 ? att::launch_fma<64, 8>(P, L, st) : att::launch_fma<64, 16>(P, L, st);
+    e = att::launch_rows32<64>(rows, P, L, st);
   }
   return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
