@@ -20,7 +20,7 @@
 //     64) for 128 rows, where the other took 476 and 293 us. With 64 rows its
 //     tiles are half empty and it takes as long: heads of 64 140 us against
 //     158, heads of 128 271 against 256;
-//   fp32, up to 4, 8, 16 rows     window_fma_kernel.
+//   fp32, row tiles of 4, 8, 16 or 32   window_fma_kernel.
 // Sums of a split request are joined by join_kernel.
 #include "sv_cache.cuh"
 #include "sv_launch.cuh"
@@ -1157,7 +1157,7 @@ struct Shape32 {
   static constexpr int SP = kTK + 4;                  // row pitch of the scores, in floats
   static constexpr int kK = kTK * kPitch, kV = kTK * D * 4;
   static constexpr int kCtas = D == 64 ? (M <= 8 ? 4 : 3) : (M <= 8 ? 3 : 2);  // an SM
-  static constexpr size_t smem = (size_t)kK + kV + (size_t)M * D * 4 + (size_t)M * SP * 4 + M * 16 + 2 * kTK * 8;
+  static constexpr size_t smem = (size_t)kK + kV + (size_t)M * D * 4 + (size_t)M * SP * 4 + M * (WK + 1) * 8 + 2 * kTK * 8 + 16;
   static_assert((WK - 1) * M * D * 4 <= kV, "the sums of the other warps fit the tile of V");
 };
 
@@ -1176,22 +1176,38 @@ __device__ __forceinline__ void sum_halves(float* s, int i) {
   }
 }
 
+// Bound by the bytes up to 8 rows and by the fp32 pipes' instructions and the
+// latencies around them above. A tile's scores: a thread holds 8 rows x 4 keys
+// and every DP-th piece of d, 12 reads of shared memory for 128 multiply-adds
+// sum_halves leaves it DP times fewer
+// scores, whose maxima go over the warp and over the warps that share the rows;
+// sums of weights stay with their keys until the unit ends. The product with
+// V: 8 rows x 4 elements a thread. K is loaded while the weights and the
+// product with V are computed and V behind it, so that a CTA needs one tile of each
+// and two or more CTAs fit an SM. 64 requests of 1000 tokens, 8 heads of 64
+// (32 requests for 128), 262 MB: 4 rows 64 us (64), 8 rows 68 (68), 16 rows 89
+// (84), 32 rows 132 (125), 128 rows 500 (465: 37 TFLOP/s).
+// Packed pairs of multiply-adds were no faster (their sums take twice the
+// registers), nor were four CTAs an SM with heads of 64.
 template <int D, int MT>
 __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(Params P, Plan L) {
   using Sh = Shape32<D, MT>;
   constexpr int SP = Sh::SP, RT = Sh::RT, KT = Sh::KT, KG = Sh::KG, DP = Sh::DP, CPR = D / 4;
   constexpr int NR = RT >= DP ? RT / DP : 1;   // rows and keys of the scores that a thread is left with
   constexpr int NK = RT * KT / DP / NR;
+  static_assert(KT == 4 && (NK == 4 || NK == 2), "a thread sums its weights in pairs");
   constexpr int TV = kTK / Sh::WK / Sh::LK;    // tokens of a thread's share of the product with V
   extern __shared__ __align__(1024) char smem[];
   char* s_k = smem;
   char* s_v = smem + Sh::kK;
   float* s_q = reinterpret_cast<float*>(s_v + Sh::kV);            // [MT][D]
   float* s_p = s_q + MT * D;                                      // [MT][SP]
-  float* s_m = s_p + MT * SP;                                     // [MT] maximum, sum, factor of the tile, free
-  float* s_l = s_m + MT;
-  float* s_f = s_l + MT;
-  long long* s_off = reinterpret_cast<long long*>(s_f + 2 * MT);  // [2][kTK]
+  float* s_m = s_p + MT * SP;                                     // [MT] maxima of a unit's end
+  float* s_f = s_m + MT;                                          // [MT] factors of the tile
+  float* s_top = s_f + MT;                                        // [WK][MT] the warps' maxima of the tile
+  float* s_l = s_top + Sh::WK * MT;                               // [WK][MT] their sums of a unit's end
+  long long* s_off = reinterpret_cast<long long*>(s_l + Sh::WK * MT);  // [2][kTK]
+  uint32_t* s_valid = reinterpret_cast<uint32_t*>(s_off + 2 * kTK);    // [2][2]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Share sh;
   Cursor ld;
@@ -1221,6 +1237,8 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
       const bool ok = page >= 0 && page < P.C.n_pages;
       if (!ok && page != -2) set_status(P.status, SV_DATA_BAD_PAGE);
       s_off[n % 2 * kTK + tid] = ok ? page * P.C.page_b + place * P.C.token_b + ld.u.head * P.C.head_b : -1;
+      const unsigned all = __ballot_sync(kFull, ok);
+      if (lane == 0) s_valid[n % 2 * 2 + warp] = all;
     }
     if (n + 1 < n_tiles) {
       if (++ld.tile == ld.u.tiles) next_unit<MT>(P, ld);
@@ -1231,11 +1249,15 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
     if (n < n_tiles) {
       const uint32_t base = smem_addr(to) + tid % CPR * 16;
       const char* src = from + tid % CPR * 16;
+      constexpr int kRows = 128 / CPR, kAhead = 8;  // rows that the CTA copies at once; offsets read together
 #pragma unroll
-      for (int j = 0; j < kTK * CPR / 128; ++j) {
-        const int r = tid / CPR + j * (128 / CPR);
-        const long long off = s_off[n % 2 * kTK + r];
-        cp16(base + r * pitch, src + (off < 0 ? 0 : off), off >= 0);
+      for (int j = 0; j < kTK / kRows; j += kAhead) {
+        long long off[kAhead];
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) off[e] = s_off[n % 2 * kTK + tid / CPR + (j + e) * kRows];
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+          cp16(base + (tid / CPR + (j + e) * kRows) * pitch, src + (off[e] < 0 ? 0 : off[e]), off[e] >= 0);
       }
     }
     cp_commit();
@@ -1247,6 +1269,7 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
   copy(0, P.C.v, s_v, D * 4);
 
   float4 o[RT];
+  float m[NR], l[NR];  // maxima of the rows so far, and sums over the keys key0 + KG j
   int lo[NR], hi[NR];
   // The thread's rows of the scores it is left with: each halving over the DP threads takes a bit of dp, rows first.
   int my_row = row0, my_key = 0;
@@ -1270,7 +1293,6 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
     if (!begun) {
       begun = true;
       from_start = cp.tile == 0;
-      __syncthreads();
       float4 qv[(MT * D / 4 + 127) / 128];
 #pragma unroll
       for (int j = 0; j < (MT * D / 4 + 127) / 128; ++j) {
@@ -1284,12 +1306,10 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
 #pragma unroll
       for (int j = 0; j < (MT * D / 4 + 127) / 128; ++j)
         if (tid + j * 128 < MT * D / 4) reinterpret_cast<float4*>(s_q)[tid + j * 128] = qv[j];
-      if (tid < MT) {
-        s_m[tid] = -INFINITY;
-        s_l[tid] = 0.f;
-      }
 #pragma unroll
       for (int e = 0; e < NR; ++e) {
+        m[e] = -INFINITY;
+        l[e] = 0.f;
         const int r = cp.u.mt * MT + my_row + e;
         const int w = r < rows ? r / P.group : 0;
         lo[e] = r < rows ? candidate_start(P, cp.u.w, w) : 0;
@@ -1303,10 +1323,10 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
     __syncthreads();  // K has landed
 
     // Scores.
-    {
-      float s[RT * KT];
+    float s[RT * KT];
 #pragma unroll
-      for (int e = 0; e < RT * KT; ++e) s[e] = 0.f;
+    for (int e = 0; e < RT * KT; ++e) s[e] = 0.f;
+    {
       const char* kr = s_k + key0 * Sh::kPitch + dp * 16;
       const float4* qr = reinterpret_cast<const float4*>(s_q + row0 * D) + dp;
 #pragma unroll 2
@@ -1324,40 +1344,61 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
           }
         }
       }
-      // The DP threads' sums joined: each exchange leaves a thread half of its scores.
-      sum_halves<RT * KT, 1, DP>(s, dp);
+    }
+    // The DP threads' sums joined: each exchange leaves a thread half of its scores.
+    sum_halves<RT * KT, 1, DP>(s, dp);
+#pragma unroll
+    for (int e = 0; e < NR * NK; ++e) s[e] *= P.scale_log2;
+    if ((cp.tile + 1) * kTK > cp.u.ctx || (s_valid[i % 2 * 2] & s_valid[i % 2 * 2 + 1]) != kFull) {
 #pragma unroll
       for (int j = 0; j < NK; ++j) {
         const int key = key0 + (my_key + j) * KG, at = cp.tile * kTK + key - cp.u.ctx;
-        const bool page_ok = s_off[i % 2 * kTK + key] >= 0;
+        const bool page_ok = s_valid[i % 2 * 2 + key / 32] >> key % 32 & 1;
 #pragma unroll
         for (int e = 0; e < NR; ++e) {
           const bool see = page_ok && (at < 0 ? hi[e] >= -cp.u.ctx : at >= lo[e] && at <= hi[e]);
-          s_p[(my_row + e) * SP + key] = see ? s[e * NK + j] * P.scale_log2 : -INFINITY;
+          if (!see) s[e * NK + j] = -INFINITY;
         }
       }
     }
-    __syncthreads();
+    // Softmax: the rows' maxima over the warp, then over the warps that share them; the sums stay apart until the unit's end.
+    float top[NR];
+#pragma unroll
+    for (int e = 0; e < NR; ++e) {
+      top[e] = s[e * NK];
+#pragma unroll
+      for (int j = 1; j < NK; ++j) top[e] = fmaxf(top[e], s[e * NK + j]);
+    }
+#pragma unroll
+    for (int x = RT / NR; x < 32; x <<= 1)
+#pragma unroll
+      for (int e = 0; e < NR; ++e) top[e] = fmaxf(top[e], __shfl_xor_sync(kFull, top[e], x));
+    if (Sh::WK > 1 && lane < RT / NR)
+#pragma unroll
+      for (int e = 0; e < NR; ++e) s_top[warp % Sh::WK * MT + my_row + e] = top[e];
+    __syncthreads();  // K is free
     copy(i + 1, P.C.k, s_k, Sh::kPitch);
-    // Softmax of the rows, two tokens a lane.
 #pragma unroll
-    for (int e = 0; e < MT / 4; ++e) {
-      const int r = warp * (MT / 4) + e;
-      const float a = s_p[r * SP + lane], b = s_p[r * SP + lane + 32];
-      const float m0 = s_m[r], m = fmaxf(m0, warp_max(fmaxf(a, b)));
-      const float off_m = m == -INFINITY ? 0.f : m;
-      const float pa = ex2(a - off_m), pb = ex2(b - off_m);
-      float sum = pa + pb;
+    for (int e = 0; e < NR; ++e) {
+      if constexpr (Sh::WK > 1)
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
-      s_p[r * SP + lane] = pa;
-      s_p[r * SP + lane + 32] = pb;
-      if (lane == 0) {
-        const float f = m0 == -INFINITY ? 0.f : ex2(m0 - m);
-        s_f[r] = f;
-        s_l[r] = s_l[r] * f + sum;
-        s_m[r] = m;
+        for (int y = 0; y < Sh::WK; ++y) top[e] = fmaxf(top[e], s_top[y * MT + my_row + e]);
+      top[e] = fmaxf(top[e], m[e]);
+      const float off_m = top[e] == -INFINITY ? 0.f : top[e], f = m[e] == -INFINITY ? 0.f : ex2(m[e] - top[e]);
+      m[e] = top[e];
+      if (warp % Sh::WK == 0 && lane < RT / NR) s_f[my_row + e] = f;
+      float p[NK];
+#pragma unroll
+      for (int j = 0; j < NK; ++j) {
+        p[j] = ex2(s[e * NK + j] - off_m);
+        s_p[(my_row + e) * SP + key0 + (my_key + j) * KG] = p[j];
       }
+      float sum = p[0] + p[1];
+      if constexpr (NK == KT)
+        sum += p[2] + p[3];
+      else
+        sum += __shfl_xor_sync(kFull, sum, RT / NR);
+      l[e] = fmaf(l[e], f, sum);
     }
     cp_wait<1>();
     __syncthreads();  // the weights are written and V has landed
@@ -1386,6 +1427,16 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
     const bool unit_end = cp.tile + 1 == cp.u.tiles;
     if (unit_end || i + 1 == n_tiles) {
       begun = false;
+#pragma unroll
+      for (int x = DP; x < 32; x <<= 1)
+#pragma unroll
+        for (int e = 0; e < NR; ++e) l[e] += __shfl_xor_sync(kFull, l[e], x);
+      if (lane < RT / NR)
+#pragma unroll
+        for (int e = 0; e < NR; ++e) {
+          s_l[warp % Sh::WK * MT + my_row + e] = l[e];
+          if (warp % Sh::WK == 0) s_m[my_row + e] = m[e];
+        }
       if constexpr (Sh::LK > 1) {
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -1400,7 +1451,10 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
         if (wk > 0 && lk == 0)
 #pragma unroll
           for (int r = 0; r < RT; ++r) buf[((wk - 1) * MT + orow + r) * CPR + d0 / 4] = o[r];
-        __syncthreads();
+      }
+      __syncthreads();
+      if constexpr (Sh::WK > 1) {
+        const float4* buf = reinterpret_cast<const float4*>(s_v);
         if (wk == 0)
 #pragma unroll
           for (int r = 0; r < RT; ++r)
@@ -1418,22 +1472,24 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           if (r % Sh::LK != lk) continue;  // the parts of a warp write a row each
-          const float m = s_m[orow + r], l = s_l[orow + r];
+          float sum = s_l[orow + r];
+#pragma unroll
+          for (int y = 1; y < Sh::WK; ++y) sum += s_l[y * MT + orow + r];
           if (split) {
             reinterpret_cast<float4*>(part + (orow + r) * D)[d0 / 4] = o[r];
             if (d0 == 0) {
-              part[MT * D + orow + r] = m;
-              part[MT * D + MT + orow + r] = l;
+              part[MT * D + orow + r] = s_m[orow + r];
+              part[MT * D + MT + orow + r] = sum;
             }
             continue;
           }
           const int x = cp.u.mt * MT + orow + r;
           if (x >= rows) break;
           const int w = x / P.group, h = cp.u.head * P.group + (x - w * P.group);
-          const float inv = l > 0.f ? 1.f / l : 0.f;
+          const float inv = sum > 0.f ? 1.f / sum : 0.f;
           reinterpret_cast<float4*>(P.out + (long long)(cp.u.w.r0 + w) * P.out_row_b + (long long)h * (D * 4))[d0 / 4] =
               make_float4(o[r].x * inv, o[r].y * inv, o[r].z * inv, o[r].w * inv);
-          if (P.lse && d0 == 0) P.lse[(long long)(cp.u.w.r0 + w) * (P.C.n_heads * P.group) + h] = lse_of(m, l, 1.f);
+          if (P.lse && d0 == 0) P.lse[(long long)(cp.u.w.r0 + w) * (P.C.n_heads * P.group) + h] = lse_of(s_m[orow + r], sum, 1.f);
         }
       }
     }
