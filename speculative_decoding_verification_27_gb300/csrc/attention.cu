@@ -14,12 +14,12 @@
 // read heads of 128 in 159 us, of 64 in 79):
 //   bf16, up to 16 or 32 rows, and up to 64 with heads of 128
 //     window_mma_kernel: 193-198 us for heads of 128 (5.4 - 5.6 TB/s) up to
-//     32 rows, 256 us for 64; heads of 64: 119-126 us;
+//     32 rows, 240 us for 64; heads of 64: 119-126 us;
 //   bf16, more rows
-//     window_tc_kernel, tiles of 128 rows: 271 us (heads of 128) and 142 us (of
+//     window_tc_kernel, tiles of 128 rows: 244 us (heads of 128) and 141 us (of
 //     64) for 128 rows, where the other took 476 and 293 us. With 64 rows its
-//     tiles are half empty and it takes as long: heads of 64 140 us against
-//     158, heads of 128 271 against 256;
+//     tiles are half empty and it takes as long: heads of 64 138 us against
+//     158, heads of 128 244 against 240;
 //   fp32, row tiles of 4, 8, 16 or 32   window_fma_kernel.
 // Sums of a split request are joined by join_kernel.
 #include "sv_cache.cuh"
@@ -334,13 +334,18 @@ __global__ void __launch_bounds__(Shape<D, WM>::kT, Shape<D, WM>::kCtas) window_
     const uint32_t base = smem_addr(s_kv) + stage * 2 * Sh::kTile;
     const int c = tid % CPR;
 #pragma unroll
-    for (int i = 0; i < kTK / RPP; ++i) {
-      const int r = tid / CPR + i * RPP;
-      const long long off = s_off[ring * kTK + r];
-      const bool ok = off >= 0;
-      const long long at = (ok ? off : 0) + c * 16;
-      cp16(base + swz<D>(r, c), P.C.k + at, ok);
-      cp16(base + Sh::kTile + swz<D>(r, c), P.C.v + at, ok);
+    for (int i = 0; i < kTK / RPP; i += 4) {
+      long long off[4];  // read together: 254 -> 242 us for windows of 64 rows
+#pragma unroll
+      for (int e = 0; e < 4; ++e) off[e] = s_off[ring * kTK + tid / CPR + (i + e) * RPP];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = tid / CPR + (i + e) * RPP;
+        const bool ok = off[e] >= 0;
+        const long long at = (ok ? off[e] : 0) + c * 16;
+        cp16(base + swz<D>(r, c), P.C.k + at, ok);
+        cp16(base + Sh::kTile + swz<D>(r, c), P.C.v + at, ok);
+      }
     }
   };
 
@@ -861,12 +866,17 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
         __syncwarp();
         const uint32_t base = kv_base + (i % S) * 2 * Sh::kTile + to;
         if ((valid[0] & valid[1]) == 0xffffffffu) {
-#pragma unroll 8
-          for (int n = 0; n < kTK / RPP; ++n) {
-            const char* src = k_ch + s_off[j][n * RPP + r0];
-            const uint32_t dst = base + n * RPP * 128 + (x0 ^ ((n * RPP & 7) << 4));
-            cp16(dst, src, true);
-            cp16(dst + Sh::kTile, src + v_k, true);
+#pragma unroll 1
+          for (int n0 = 0; n0 < kTK / RPP; n0 += 8) {
+            long long off[8];  // read together: 271 -> 244 us for heads of 128
+#pragma unroll
+            for (int e = 0; e < 8; ++e) off[e] = s_off[j][(n0 + e) * RPP + r0];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t dst = base + (n0 + e) * RPP * 128 + (x0 ^ ((e * RPP & 7) << 4));
+              cp16(dst, k_ch + off[e], true);
+              cp16(dst + Sh::kTile, k_ch + off[e] + v_k, true);
+            }
           }
         } else {  // zeros where there is no page, and behind the sequence
 #pragma unroll 1
