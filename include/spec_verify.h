@@ -587,7 +587,7 @@ sv_status sv_cache_commit(const sv_kv_cache* cache, const sv_sequences* seqs, in
  *               heads contiguous), 16-byte aligned. Rows of no window are
  *               neither read nor written.
  *   out_lse     [R, n_q_heads] float32, or NULL.
- *   scale       finite; usually 1 / sqrt(head_dim).
+ *   scale       below 2^127 in magnitude; usually 1 / sqrt(head_dim).
  *   head_dim    64 or 128; n_q_heads a multiple of n_kv_heads, at most 64
  *               query heads to a key-value head.
  *   workspace   sv_window_attention_workspace_size(cache, n_q_heads, R)

@@ -1659,7 +1659,7 @@ sv_status sv_window_attention(const void* q, int64_t q_stride, int32_t n_q_heads
   const int es = elem_size(cache->dtype), D = cache->head_dim;
   if (D != 64 && D != 128) return SV_ERR_INVALID_ARG;
   if (n_q_heads < 1 || n_q_heads % P.C.n_heads || n_q_heads / P.C.n_heads > 64) return SV_ERR_INVALID_ARG;
-  if (layer < 0 || layer >= P.C.n_layers || !std::isfinite(scale)) return SV_ERR_INVALID_ARG;
+  if (layer < 0 || layer >= P.C.n_layers || !(std::fabs(scale) < 0x1p127f)) return SV_ERR_INVALID_ARG;
   const int64_t strides[2] = {q_stride, out_stride};
   for (int64_t s : strides)
     if (s < (int64_t)n_q_heads * D || s > INT64_MAX / 4 || s * es % 16) return SV_ERR_INVALID_ARG;

@@ -41,6 +41,12 @@ def test_host_validation(lib):
     assert lib.sv_window_attention_workspace_size(_cache(), 4, -1) == 0
 
 
+def test_scale_that_leaves_fp32_in_base_two(lib):
+    """The scores are taken to base two: a scale has to stay finite times log2(e)."""
+    assert _call(lib, scale=2.0 ** 127) == _call(lib, scale=-3e38) == api.SV_ERR_INVALID_ARG
+    assert _call(lib, scale=2.0 ** 127, R=0) == api.SV_ERR_INVALID_ARG and _call(lib, scale=1.7e38, R=0) == api.SV_OK
+
+
 # ---------------------------------------------------------------------------
 # Against 64 bits
 # ---------------------------------------------------------------------------
@@ -259,6 +265,37 @@ def test_high_tiles_split_repeats_and_bad_pages(cuda_lib, D):
     k = c.k[0][c.table[1].long()[keep // 16], keep % 16].double().repeat_interleave(32, 1)
     s = torch.einsum("hd,thd->ht", c.q[5].double(), k) * D ** -0.5
     assert (torch.logsumexp(s, 1) - got[1][5].cpu().double()).abs().max() < 1e-4
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("group,rows", [(1, 3), (2, 4), (5, 3), (8, 4), (3, 40)])
+def test_fp32_row_tiles(cuda_lib, D, group, rows):
+    """Each height of the fp32 row tiles: maxima that move at every tile, units split over CTAs, pages that hide a part of a tile."""
+    c = Case([900, 0, 64, 130], [[rows], [1, rows], [rows], [rows]], 3 * group, 3, D, 7, F32, seed=50 + D + rows, layout="both", q_pad=4)
+    rise = torch.linspace(0.2, 4.0, 64)
+    for t in range(900 + rows):
+        p, i = int(c.table[0, t // 7]), t % 7
+        c.k[0, p, i] *= rise[min(63, t // 14)]
+    c.check()
+    q, cache, layer, table, ctx, cu, cand = c.args
+    want = api.sv_window_attention(*c.args, want_lse=True)
+    broken = table.clone()
+    broken[0, 3:60] = 1 << 20  # tokens 21 .. 419
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = api.sv_window_attention(q, cache, layer, broken, ctx, cu, cand, want_lse=True, status=status)
+    assert int(status) == api.SV_DATA_BAD_PAGE
+    assert torch.equal(got[0][rows:c.R - 3], want[0][rows:c.R - 3]) and torch.equal(got[1][rows:c.R - 3], want[1][rows:c.R - 3])
+    at = torch.tensor([t for t in range(900 + rows) if not 21 <= t < 420])
+    page = c.table[0].long()[at // 7]
+    k, v = (x[0][page, at % 7].double().repeat_interleave(group, 1) for x in (c.k, c.v))
+    s = torch.einsum("hd,thd->ht", c.q[rows - 1].double(), k) * D ** -0.5
+    o = torch.einsum("ht,thd->hd", torch.softmax(s, 1), v)
+    # A score is off by (D + 8) 2^-24 of its sum of magnitudes; a weight by twice that and the sums' (n + 64) 2^-22.
+    d = (D + 8) * 2.0 ** -24 * D ** -0.5 * torch.einsum("hd,thd->ht", c.q[rows - 1].double().abs(), k.abs()).amax(1, keepdim=True)
+    bound = 2 * d + (len(at) + 64) * 2.0 ** -22
+    assert ((torch.logsumexp(s, 1) - got[1][rows - 1].cpu().double()).abs() <= bound[:, 0] + 1e-6).all()
+    assert ((o - got[0][rows - 1].cpu().double()).abs() <= 2 * bound * v.abs().amax()).all()
 
 
 @pytest.mark.gpu
