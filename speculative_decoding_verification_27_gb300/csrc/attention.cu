@@ -13,19 +13,20 @@
 // 4096 tokens, 8 key-value heads, one token to 32 of them; the copy rate would
 // read heads of 128 in 159 us, of 64 in 79):
 //   bf16, up to 16 or 32 rows, and up to 64 with heads of 128
-//     window_mma_kernel: 193-198 us for heads of 128 (5.4 - 5.6 TB/s) up to
-//     32 rows, 240 us for 64; heads of 64: 119-126 us;
+//     window_mma_kernel: 187-195 us for heads of 128 (5.5 - 5.7 TB/s) up to
+//     32 rows, 240 us for 64; heads of 64: 118-123 us;
 //   bf16, more rows
-//     window_tc_kernel, tiles of 128 rows: 244 us (heads of 128) and 141 us (of
+//     window_tc_kernel, tiles of 128 rows: 240 us (heads of 128) and 140 us (of
 //     64) for 128 rows, where the other took 476 and 293 us. With 64 rows its
 //     tiles are half empty and it takes as long: heads of 64 138 us against
-//     158, heads of 128 244 against 240;
+//     158, heads of 128 240 against 240;
 //   fp32, row tiles of 4, 8, 16 or 32   window_fma_kernel.
 // Sums of a split request are joined by join_kernel.
 #include "sv_cache.cuh"
 #include "sv_launch.cuh"
 
 #include <cmath>
+#include <type_traits>
 #include <cuda_bf16.h>
 
 namespace sv {
@@ -60,7 +61,8 @@ constexpr int kTK = 64;    // tokens of a key tile
 // join_kernel.
 struct Plan {
   char* part;          // partial results: two slots a CTA
-  int* cut;            // [grid][4]: the unit that a CTA's share cuts at its end: b, head, row tile, its last CTA (b = -1: none)
+  int* cut;            // [grid][8]: the unit that a CTA's share cuts at its end: its first stacked row's window row and rows
+                       // (0: none), head, row tile, its last CTA
 };
 
 struct Unit {
@@ -147,7 +149,7 @@ __device__ __forceinline__ bool take_share(const Params& P, const Plan& L, Share
   }
   const int grid = (int)min((long long)gridDim.x, total), id = blockIdx.x;  // shares of a tile at least
   if (id >= grid) {
-    if (tid == 0) L.cut[id * 4] = -1;
+    if (tid == 0) L.cut[id * 8 + 1] = 0;
     return false;
   }
   sh.size = div_small(total, grid, sh.more);
@@ -165,7 +167,7 @@ __device__ __forceinline__ bool take_share(const Params& P, const Plan& L, Share
     s_unit = c.u;
     s_first = sh.t0 - at;  // first tile of the share within its request
   }
-  if (tid == 0) L.cut[id * 4] = -1;  // until the share's end is reached
+  if (tid == 0) L.cut[id * 8 + 1] = 0;  // until the share's end is reached
   __syncthreads();
   c.u = s_unit;
   const long long unit = div_small(s_first, c.u.tiles, c.tile);
@@ -193,7 +195,9 @@ __device__ __forceinline__ void tell_cut(const Plan& L, const Share& sh, const C
   const long long last = sh.t1 - 1 + (c.u.tiles - 1 - c.tile);  // the unit's last tile in the list
   const long long front = (sh.size + 1) * sh.more;               // tiles of the larger shares
   const long long k = last < front ? last / (sh.size + 1) : sh.more + (last - front) / sh.size;
-  *reinterpret_cast<int4*>(L.cut + blockIdx.x * 4) = make_int4(cuts ? c.u.b : -1, c.u.head, c.u.mt, (int)k);
+  int4* cut = reinterpret_cast<int4*>(L.cut + blockIdx.x * 8);
+  cut[0] = make_int4(c.u.w.r0, cuts ? c.u.w.rows : 0, c.u.head, c.u.mt);
+  cut[1] = make_int4((int)k, 0, 0, 0);
 }
 
 // The first row of the candidate that window row w lies in.
@@ -416,7 +420,7 @@ __global__ void __launch_bounds__(Shape<D, WM>::kT, Shape<D, WM>::kCtas) window_
       store_lookup((i + S) % (S + 1), ld.u.head, page, place);  // for the next round's copy
       if (i + S + 1 < n_tiles) {
         if (++ld.tile == ld.u.tiles) next_unit<MT>(P, ld);
-        lookup(ld, page, place);  // has this round's arithmetic to arrive
+        lookup(ld, page, place);  // has this pass's arithmetic to arrive
       }
     }
 
@@ -1511,11 +1515,14 @@ __global__ void __launch_bounds__(128, Shape32<D, MT>::kCtas) window_fma_kernel(
 
 // Joins the parts of a unit that several CTAs share. Block c takes the unit
 // that CTA c's share cuts at its end, if it began there. A group of D / 4
-// threads holds a row, 4 elements a thread, with four parts' loads in flight.
-// A unit of up to four parts has a row to each group, and no barrier; one of
-// more parts (a long request on an otherwise idle machine) has its parts dealt
-// to the groups of a block, whose sums are joined in order. The block is
-// brought up while the parts are still being computed and waits for them.
+// threads holds a row, 4 elements a thread, with four or eight parts' loads in
+// flight. A unit of up to eight parts has a row to each group, and no barrier
+// (64 requests of 2000 tokens and one head: 31 us a call; with the parts dealt
+// out from five on, 35); one of more parts (a long request on an otherwise idle
+// machine) has them dealt to the groups of a block, whose sums are joined in
+// order (38 parts of one token's unit: eight in flight 15.1 us a call, four
+// 16.4). The block is brought up while the parts are still being computed and
+// waits for them.
 constexpr int kJoinT = 128;
 
 struct RowSum {
@@ -1537,18 +1544,19 @@ __global__ void __launch_bounds__(kJoinT) join_kernel(Params P, Plan L, int grid
   release_stream();
   wait_for_stream();
   const int c = blockIdx.x;
-  const int4 cut = *reinterpret_cast<const int4*>(L.cut + c * 4);
-  if (cut.x < 0 || cut.x >= P.S.n) return;
-  const int head = cut.y, mt = cut.z, last = min(cut.w, grid - 1);
-  const Window w = find_window(P.W, cut.x);
-  const int rows = min(MT, w.rows * P.group - mt * MT);  // of this row tile
+  const int4 cut = *reinterpret_cast<const int4*>(L.cut + c * 8);
+  const int last = min(L.cut[c * 8 + 4], grid - 1);
+  if (cut.y <= 0) return;
+  const int head = cut.z, mt = cut.w;
+  const int rows = min(MT, cut.y * P.group - mt * MT);  // of this row tile
   const int g = threadIdx.x / TPR, lane_d = threadIdx.x % TPR;
-  // Row r of parts k0, k0 + step, ... (four of them at most).
-  auto add_parts = [&](RowSum& sum, int r, int k0, int step) {
-    float m[4], l[4];
-    float4 o[4];
+  // Row r of N parts k0, k0 + step, ..., their loads in flight together.
+  auto add_parts = [&](auto n, RowSum& sum, int r, int k0, int step) {
+    constexpr int N = decltype(n)::value;
+    float m[N], l[N];
+    float4 o[N];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < N; ++j) {
       const int k = k0 + j * step;
       m[j] = -INFINITY;
       l[j] = 0.f;
@@ -1561,31 +1569,37 @@ __global__ void __launch_bounds__(kJoinT) join_kernel(Params P, Plan L, int grid
       }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) add_row(sum, m[j], l[j], o[j], scale);
+    for (int j = 0; j < N; ++j) add_row(sum, m[j], l[j], o[j], scale);
   };
   auto write = [&](const RowSum& sum, int r) {
     const int x = mt * MT + r, ww = x / P.group, h = head * P.group + (x - ww * P.group);
     const float inv = sum.l > 0.f ? 1.f / sum.l : 0.f;
     const float4 o = make_float4(sum.o.x * inv, sum.o.y * inv, sum.o.z * inv, sum.o.w * inv);
-    char* dst = P.out + (long long)(w.r0 + ww) * P.out_row_b + ((long long)h * D + lane_d * 4) * Elem<DT>::kBytes;
+    char* dst = P.out + (long long)(cut.x + ww) * P.out_row_b + ((long long)h * D + lane_d * 4) * Elem<DT>::kBytes;
     if constexpr (DT == 1)
       *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
     else
       *reinterpret_cast<float4*>(dst) = o;
-    if (P.lse && lane_d == 0) P.lse[(long long)(w.r0 + ww) * (P.C.n_heads * P.group) + h] = lse_of(sum.m, sum.l, scale);
+    if (P.lse && lane_d == 0) P.lse[(long long)(cut.x + ww) * (P.C.n_heads * P.group) + h] = lse_of(sum.m, sum.l, scale);
   };
   const RowSum none{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  if (last - c < 4) {
+  auto row_a_group = [&](auto n) {
     for (int r = blockIdx.y * kG + g; r < rows; r += gridDim.y * kG) {
       RowSum sum = none;
-      add_parts(sum, r, c, 1);
+      add_parts(n, sum, r, c, 1);
       write(sum, r);
     }
-    return;
-  }
+  };
+  constexpr std::integral_constant<int, 4> four;
+  constexpr std::integral_constant<int, 8> eight;
+  if (last - c < 4) return row_a_group(four);
+  if (last - c < 8) return row_a_group(eight);
   for (int r = blockIdx.y; r < rows; r += gridDim.y) {
     RowSum sum = none;
-    for (int k0 = c + g; k0 <= last; k0 += kG * 4) add_parts(sum, r, k0, kG);
+    if (last - c < kG * 4)
+      add_parts(four, sum, r, c + g, kG);
+    else
+      for (int k0 = c + g; k0 <= last; k0 += kG * 8) add_parts(eight, sum, r, k0, kG);
     s_sum[g][lane_d] = sum;
     __syncthreads();
     if (g == 0) {
@@ -1645,7 +1659,7 @@ extern "C" {
 size_t sv_window_attention_workspace_size(const sv_kv_cache* cache, int32_t n_q_heads, int32_t R) {
   if (!cache || (cache->head_dim != 64 && cache->head_dim != 128) || n_q_heads < 1 || R < 0) return 0;
   // The cuts, then two partial results a CTA: of any kernel, 256 rows an SM at most.
-  return (size_t)sv::att::kGrid * 16 + 2 * (size_t)152 * 256 * ((size_t)cache->head_dim + 2) * 4;
+  return (size_t)sv::att::kGrid * 32 + 2 * (size_t)152 * 256 * ((size_t)cache->head_dim + 2) * 4;
 }
 
 sv_status sv_window_attention(const void* q, int64_t q_stride, int32_t n_q_heads, int32_t R, const sv_kv_cache* cache,
@@ -1682,7 +1696,7 @@ sv_status sv_window_attention(const void* q, int64_t q_stride, int32_t n_q_heads
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   att::Plan L{};
   L.cut = static_cast<int*>(workspace);
-  L.part = static_cast<char*>(workspace) + att::kGrid * 16;
+  L.part = static_cast<char*>(workspace) + att::kGrid * 32;
   // Row tiles as high as the windows' mean number of stacked rows.
   const long long rows = ((long long)R * P.group + P.S.n - 1) / P.S.n;
   cudaError_t e;
