@@ -31,7 +31,6 @@
 #include "../../include/spec_verify.h"
 #include "sv_device.cuh"
 
-#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -49,6 +48,9 @@ struct Params {
   const int32_t* out_len;
   float c_hi, c_lo;          // log2(e) / T in two parts
   float inv_T_hi, inv_T_lo;  // 1 / T
+  // How far below a maximum terms are zero. Up to `large` a step of the type is less than that, and what lies between two maxima and
+  // the first one's cut-off stays finite in the exponent: the cut-off is then found once.
+  float far, large;
   float* logprob;
   int32_t* rank;
   float* entropy;
@@ -163,34 +165,37 @@ __device__ __forceinline__ float value_below(float f) {
   return key_value(k);
 }
 
-// Where logits are cut off below a maximum m: kFar in the exponent, rounded
-// down, and below m itself where that is less than a step. -inf where m is
-// the type's lowest value (then the terms are counted, add_lowest).
+constexpr uint32_t kAlone = 0xffffffffu;  // no value of the type, nor a NaN that arithmetic gives
+
+// Where logits are cut off below a maximum m whose next lower value is less
+// than kFar away in the exponent: kFar below it, rounded down to the type.
 template <int DT>
 __device__ __forceinline__ uint32_t cut_off(float m, float far) {
   if constexpr (DT == 1) {
-    const int k = min(order_key(m - far) >> 16, (order_key(m) >> 16) - 1);
+    const int k = order_key(m - far) >> 16;
     const uint32_t b = __float_as_uint(key_value((int)((uint32_t)k << 16 | (k < 0 ? 0xffffu : 0u)))) & 0xffff0000u;
     return b | b >> 16;
   } else {
-    return __float_as_uint(key_value(min(order_key(m - far), order_key(m) - 1)));
+    return __float_as_uint(m - far);
   }
 }
 
-// A maximum that is the type's lowest value: what is not -inf counts one.
+// A maximum that no other value of the type comes near (the type's lowest
+// one, or a step of the type is more than any exponent reaches): what equals
+// it counts one, all else nothing.
 template <int DT>
-__device__ __forceinline__ void add_lowest(const uint4& v, f2_t& S) {
+__device__ __forceinline__ void add_equal(const uint4& v, float m, f2_t& S) {
   float f[Elem<DT>::kEPV], n = 0.f;
   Elem<DT>::unpack(v, f);
 #pragma unroll
-  for (int j = 0; j < Elem<DT>::kEPV; ++j) n += f[j] > -INFINITY ? 1.f : 0.f;
+  for (int j = 0; j < Elem<DT>::kEPV; ++j) n += f[j] == m ? 1.f : 0.f;
   S = f2_add(S, f2_pack(n, 0.f));
 }
 
 // Adds one vector's terms 2^((z - m) c) and their first moments, in pairs.
 // The reference's negative and the two parts of c come as pairs; `lowest`
-// cuts off logits so far below m that their term is zero (-inf among them,
-// whose product 0 * inf would not be a number).
+// cuts off logits so far below m that their term is zero: their exponent
+// could leave fp32, and its product with a term of zero not be a number.
 template <int DT>
 __device__ __forceinline__ void add_terms(const uint4& v, uint32_t lowest, f2_t neg_m, f2_t c_hi, f2_t c_lo, f2_t& S, f2_t& S1) {
   const uint32_t* w = &v.x;
@@ -440,11 +445,9 @@ __global__ void __launch_bounds__(kThreads, SV_LP_CTAS) logprobs_kernel(Params P
   __syncthreads();
 
   const int q = (n_top + kWarps - 1) / kWarps;
-  const float far = kFar / P.c_hi;
   const f2_t c_hi = f2_splat(P.c_hi), c_lo = f2_splat(P.c_lo);
-  const float lowest_value = DT == 1 ? __uint_as_float(0xff7f0000u) : -FLT_MAX;
   float m = -INFINITY;  // this thread's maximum
-  uint32_t lowest = 0;
+  uint32_t lowest = 0;  // its cut-off, or kAlone: nothing below m has a term
   f2_t neg_m = 0ull;
   f2_t S = 0ull, S1 = 0ull;
   int above = 0;
@@ -466,7 +469,10 @@ __global__ void __launch_bounds__(kThreads, SV_LP_CTAS) logprobs_kernel(Params P
         S1 = f2_mul(f, f2_fma(f2_splat(d), S, S1));
         S = f2_mul(f, S);
       }
-      if (!(m > lowest_value)) lowest = cut_off<DT>(bm, far);  // then it stays: a higher maximum only makes its term smaller
+      if (!(fmaxf(fabsf(m), fabsf(bm)) < P.large)) {
+        const bool alone = (bm - value_below<DT>(bm)) * P.c_hi >= kFar && bm < INFINITY;
+        lowest = alone ? kAlone : cut_off<DT>(bm, P.far);
+      }
       m = bm;
       neg_m = f2_splat(-m);
     }
@@ -511,9 +517,9 @@ __global__ void __launch_bounds__(kThreads, SV_LP_CTAS) logprobs_kernel(Params P
       const bool near = zt == -INFINITY || (tok_v >= at && tok_v < at + kThreads * kU);
       above += near ? count_above_near<DT>(cur, at + tid, v1, off, tok, zt) : count_above<DT>(cur, at < tok_v ? zt_below : zt);
     }
-    if (m == lowest_value) {
+    if (lowest == kAlone) {
 #pragma unroll
-      for (int u = 0; u < kU; ++u) add_lowest<DT>(cur[u], S);
+      for (int u = 0; u < kU; ++u) add_equal<DT>(cur[u], m, S);
     } else if (bm != -INFINITY) {
 #pragma unroll
       for (int u = 0; u < kU; ++u) add_terms<DT>(cur[u], lowest, neg_m, c_hi, c_lo, S, S1);
@@ -712,6 +718,8 @@ extern "C" sv_status sv_token_logprobs(const void* logits, sv_dtype dtype, int32
   P.c_lo = std::isinf(P.c_hi) ? 0.f : (float)(c - (double)P.c_hi);
   P.inv_T_hi = (float)inv_T;
   P.inv_T_lo = std::isinf(P.inv_T_hi) ? 0.f : (float)(inv_T - (double)P.inv_T_hi);
+  P.far = lp::kFar / P.c_hi;
+  P.large = P.far * (dtype == SV_BF16 ? 0x1p7f : 0x1p23f);
   P.logprob = out_logprob;
   P.rank = out_rank;
   P.entropy = out_entropy;

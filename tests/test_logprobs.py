@@ -285,3 +285,48 @@ def test_of_a_verify_call(cuda_lib):
             assert abs(math.exp(float(got.logprob[r0 + j])) - p) <= 1e-5 * p + 1e-7
             seen += 1
     assert seen > 10
+
+
+def _masked(V, dtype, value):
+    """Rows of which all but a few tokens hold one large negative value; the allowed ones lie first, last, in the middle, anywhere."""
+    gen = torch.Generator().manual_seed(V)
+    z = torch.full((6, V), value)
+    at = [range(4), range(V - 4, V), range(V // 2, V // 2 + 4), torch.randperm(V, generator=gen)[:40].tolist(),
+          [V // 3, V // 2, V - 2, V - 1], list(range(0, V, max(1, V // 9)))]
+    for r, x in enumerate(at):
+        z[r, list(x)] = 3.0 * torch.randn(len(x), generator=gen)
+    z[4, : V // 4] = -INF  # a mask of another kind beside it
+    return z.to(dtype), torch.tensor([x[3] for x in at], dtype=torch.int32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,copies", [(5000, 1), (70001, 1), (151936, 1), (32000, 60)])
+@pytest.mark.parametrize("value,T", [(torch.finfo(torch.bfloat16).min, 1.0), (torch.finfo(torch.float32).min / 2, 0.7), (-3.0e38, 1.0),
+                                     (-1.0e38, 0.3), (-1.0e30, 1.0e-9), (-1.0e9, 1.0), (-1.0e4, 0.5)])
+def test_masks_of_finite_values(cuda_lib, dtype, V, copies, value, T):
+    """A masked token's term is nothing in the entropy, whatever finite value the mask has and whatever was seen before it."""
+    z, tok = (x.repeat((copies,) + (1,) * (x.dim() - 1)) for x in _masked(V, dtype, value))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = api.sv_token_logprobs(z.cuda(), tok.cuda(), temperature=T, n_top=3, status=status)
+    assert int(status) == 0
+    _check(z, tok, T, 3, got)
+    assert torch.equal(api.sv_token_logprobs(z.cuda(), tok.cuda(), temperature=T).entropy, got.entropy)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size,T", [(2.0 ** 60, 2.0 ** -100), (1.0e37, 1.0e-3), (1.0e30, 1.0e-20), (2.0 ** 90, 2.0 ** 80), (5.0e37, 2.0 ** 96)])
+@pytest.mark.parametrize("V", [64, 9001, 128000])
+def test_temperatures_beside_the_step_of_the_type(cuda_lib, dtype, size, T, V):
+    """Logits whose neighbouring values lie further apart than any exponent reaches, and rows where they just do not."""
+    gen = torch.Generator().manual_seed(V)
+    z = (torch.randn(5, V, generator=gen) * size).to(dtype)
+    z[1, : V // 2] = -INF
+    z[2] = -z[2].float().abs().to(dtype)
+    top = z.max(1, keepdim=True).values
+    at = torch.stack([torch.randperm(V, generator=gen)[:3] for _ in range(5)])
+    z.scatter_(1, at, top.expand(5, 3))  # three or four equal largest values
+    z[3, at[3, 0]] = torch.nextafter(top[3], torch.full_like(top[3], -INF))[0]
+    tok = at[:, 2].to(torch.int32)
+    _check(z, tok, T, 2, api.sv_token_logprobs(z.cuda(), tok.cuda(), temperature=T, n_top=2))
