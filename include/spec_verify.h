@@ -420,7 +420,7 @@ sv_status sv_vshard_finish(const void* jobs, int32_t B, int32_t R_t, const int32
  *                (the tokens being out_tokens) are read; the other rows'
  *                outputs, and those past cu_draft[B] + B, are left as they
  *                were. out_len[b] = 0 takes no row of request b.
- *   temperature  2^-100 <= T <= 2^100.
+ *   temperature  2^-100 <= T <= 2^96.
  *   n_top        0 .. SV_LOGPROBS_MAX_TOP; out_top_* are [R, n_top] (may be
  *                NULL when n_top is 0, or each by itself when not wanted).
  *   out_*        each may be NULL. float32 and int32.

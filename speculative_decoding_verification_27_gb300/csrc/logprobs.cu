@@ -694,7 +694,8 @@ extern "C" sv_status sv_token_logprobs(const void* logits, sv_dtype dtype, int32
   if ((dtype != SV_FP32 && dtype != SV_BF16) || V < 1 || V > (1 << 30) || ld < V || R < 0 || B < 0) return SV_ERR_INVALID_ARG;
   const int es = dtype == SV_BF16 ? 2 : 4;
   if (ld > INT64_MAX / 4) return SV_ERR_INVALID_ARG;
-  if (!(temperature >= 0x1p-100f && temperature <= 0x1p100f)) return SV_ERR_INVALID_ARG;
+  // Up to 2^96 a cut-off kFar below the maximum is finite: 139 T < 2^104, the step of fp32 at its largest values.
+  if (!(temperature >= 0x1p-100f && temperature <= 0x1p96f)) return SV_ERR_INVALID_ARG;
   if (n_top < 0 || n_top > SV_LOGPROBS_MAX_TOP) return SV_ERR_INVALID_ARG;
   if (!tokens && (out_logprob || out_rank)) return SV_ERR_INVALID_ARG;
   if ((cu_draft == nullptr) != (out_len == nullptr) || (!cu_draft && B != 0)) return SV_ERR_INVALID_ARG;

@@ -330,3 +330,9 @@ def test_temperatures_beside_the_step_of_the_type(cuda_lib, dtype, size, T, V):
     z[3, at[3, 0]] = torch.nextafter(top[3], torch.full_like(top[3], -INF))[0]
     tok = at[:, 2].to(torch.int32)
     _check(z, tok, T, 2, api.sv_token_logprobs(z.cuda(), tok.cuda(), temperature=T, n_top=2))
+
+
+def test_temperature_range(lib):
+    """Above 2^96 what is zero beside a maximum near fp32's lowest value lies below that, and -inf could not be told from it."""
+    assert _call(lib, T=2.0 ** 96, R=0) == _call(lib, T=2.0 ** -100, R=0) == api.SV_OK
+    assert _call(lib, T=2.0 ** 96 * 1.001, R=0) == _call(lib, T=2.0 ** -101, R=0) == api.SV_ERR_INVALID_ARG
