@@ -11,6 +11,7 @@ import functools
 import os
 import re
 import struct
+import threading
 from typing import NamedTuple, Optional
 
 import torch
@@ -604,6 +605,18 @@ class _Sequences(ctypes.Structure):
 _pack_sequences = struct.Struct("@PqiiP").pack  # _Sequences as bytes: the library reads it during the call only
 
 
+class _Scratch:
+    """Scratch of the calls on one stream, whose kernels run in order. A call
+    of two launches hands its results over in the block, so no other thread's
+    launch on the stream may come between them: the lock is held over the
+    whole call (and may be taken again by a handler that interrupts it)."""
+    __slots__ = ("lock", "block")
+
+    def __init__(self):
+        self.lock = threading.RLock()
+        self.block = None
+
+
 class KVCache:
     """The pages of a key-value cache: `k` and `v` are [n_layers, n_pages,
     page_size, n_kv_heads, head_dim] views with equal strides (any order of
@@ -632,12 +645,11 @@ class KVCache:
                          _vec(page_ref, "page_ref", torch.int32, (n,)), _vec(free_bits, "free_bits", torch.int32, (words,)))
         self._ref = ctypes.byref(self._c)
         self._attention_bytes = load().sv_window_attention_workspace_size(self._ref, self.n_kv_heads, 0)
-        self._workspaces: dict = {}
+        self._scratches: dict = {}
 
-    def _workspace(self, nbytes: int, stream) -> torch.Tensor:
-        """Scratch of at least nbytes for a call on `stream`: one block a
-        stream, whose calls run in order. A call that is being captured gets
-        a block of its graph's own."""
+    def _scratch(self, stream) -> _Scratch:
+        """What calls on `stream` share. A call that is being captured gets
+        scratch of its graph's own."""
         if stream is None:
             key = _raw_stream(self.k.get_device())
             capturing = torch.cuda.is_current_stream_capturing()
@@ -646,11 +658,16 @@ class KVCache:
             with torch.cuda.stream(stream):
                 capturing = torch.cuda.is_current_stream_capturing()
         if capturing:
-            return _new(torch.empty, nbytes, torch.uint8, self.k, stream)
-        ws = self._workspaces.get(key)
-        if ws is None or ws.numel() < nbytes:
-            ws = self._workspaces[key] = _new(torch.empty, max(nbytes, self._attention_bytes), torch.uint8, self.k, stream)
-        return ws
+            return _Scratch()
+        return self._scratches.get(key) or self._scratches.setdefault(key, _Scratch())
+
+    def _launch_with_scratch(self, nbytes: int, stream, call):
+        """call(workspace) with at least nbytes of the stream's scratch."""
+        scratch = self._scratch(stream)
+        with scratch.lock:
+            if scratch.block is None or scratch.block.numel() < nbytes:
+                scratch.block = _new(torch.empty, max(nbytes, self._attention_bytes), torch.uint8, self.k, stream)
+            call(scratch.block)
 
 
 def _seqs(page_table: torch.Tensor, ctx_len: torch.Tensor) -> bytes:
@@ -702,11 +719,15 @@ def sv_cache_reserve(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Te
     n = page_table.shape[0]
     if granted is None:
         granted = _new(torch.empty, n, torch.int32, page_table, stream)
+
+    def call(ws):
+        _launch("sv_cache_reserve", cache.k, stream, cache._ref, _seqs(page_table, ctx_len), *_windows(n, cu_draft, cu_cand),
+                _vec(granted, "granted", torch.int32, (n,)), _ptr(ws), ws.numel(), _vec(status, "status", torch.int32, (1,)))
+
     if workspace is None:
-        workspace = cache._workspace(_reserve_bytes(n), stream)
-    _launch("sv_cache_reserve", cache.k, stream, cache._ref, _seqs(page_table, ctx_len), *_windows(n, cu_draft, cu_cand),
-            _vec(granted, "granted", torch.int32, (n,)), _ptr(workspace), workspace.numel(),
-            _vec(status, "status", torch.int32, (1,)))
+        cache._launch_with_scratch(_reserve_bytes(n), stream, call)
+    else:
+        call(workspace)
     return granted
 
 
@@ -759,11 +780,16 @@ def sv_window_attention(q: torch.Tensor, cache: KVCache, layer: int, page_table:
         raise ValueError("q and out must be [R, q_heads, head_dim] with contiguous heads")
     if out_lse is None and want_lse:
         out_lse = _new(torch.zeros, (R, heads), torch.float32, q, stream)
+
+    def call(ws):
+        _launch("sv_window_attention", q, stream, q.data_ptr(), q.stride(0) if R > 1 else heads * D, heads, R, cache._ref,
+                int(layer), _seqs(page_table, ctx_len), *_windows(page_table.shape[0], cu_draft, cu_cand),
+                D ** -0.5 if scale is None else float(scale), out.data_ptr(), out.stride(0) if R > 1 else heads * D,
+                _vec(out_lse, "out_lse", torch.float32, (R, heads)), _ptr(ws), ws.numel(),
+                _vec(status, "status", torch.int32, (1,)))
+
     if workspace is None:
-        workspace = cache._workspace(cache._attention_bytes, stream)
-    _launch("sv_window_attention", q, stream, q.data_ptr(), q.stride(0) if R > 1 else heads * D, heads, R, cache._ref,
-            int(layer), _seqs(page_table, ctx_len), *_windows(page_table.shape[0], cu_draft, cu_cand),
-            D ** -0.5 if scale is None else float(scale), out.data_ptr(), out.stride(0) if R > 1 else heads * D,
-            _vec(out_lse, "out_lse", torch.float32, (R, heads)), _ptr(workspace), workspace.numel(),
-            _vec(status, "status", torch.int32, (1,)))
+        cache._launch_with_scratch(cache._attention_bytes, stream, call)
+    else:
+        call(workspace)
     return out, out_lse

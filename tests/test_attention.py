@@ -478,3 +478,32 @@ def test_a_step_of_all_calls(cuda_lib):
                 p = int(table[b, t // page])
                 assert torch.equal(cache.k[:, p, t % page], x) and torch.equal(cache.v[:, p, t % page], -x)
             assert int((table[b] >= 0).sum()) == -(-len(held[b]) // page)
+
+
+@pytest.mark.gpu
+def test_two_threads_on_one_stream(cuda_lib):
+    """Calls of two host threads on the same stream and cache, each with its own windows, all of them split and joined."""
+    import threading
+    c = Case([9000, 700, 3000], [[3], [2], [1]], 8, 2, 64, 16, BF, seed=21)
+    c.run()
+    q, cache, layer, table, ctx, cu, cand = c.args
+    short = torch.tensor([100, 650, 3000], dtype=torch.int32, device="cuda")
+    args = [c.args, (-q, cache, layer, table, short, cu, cand)]
+    want = [api.sv_window_attention(*a, want_lse=True) for a in args]
+    torch.cuda.synchronize()
+    got, start = [[], []], threading.Barrier(2)
+
+    def work(i):
+        start.wait()
+        for _ in range(200):
+            got[i].append(api.sv_window_attention(*args[i], want_lse=True))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 200
+        assert all(torch.equal(g[0], want[i][0]) and torch.equal(g[1], want[i][1]) for g in got[i])

@@ -1,0 +1,81 @@
+"""The Python binding of the cache and attention calls by itself: which
+scratch a call gets, what tensors it takes. On the CPU, with tensors that say
+they are on a GPU and a library that only notes its calls."""
+import threading
+import time
+
+import pytest
+import torch
+
+from speculative_decoding_verification_27_gb300 import api, build
+
+
+class OnGpu(torch.Tensor):
+    """A tensor that claims to lie on a GPU."""
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return 0
+
+
+def gpu(*shape, dtype=torch.int32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+
+
+class Noted:
+    """The library's calls as (name, arguments)."""
+
+    def __init__(self, real):
+        self.real, self.calls, self.during = real, [], lambda name, args: None
+
+    def __getattr__(self, name):
+        if name.endswith("_size"):
+            return getattr(self.real, name)
+
+        def call(*args):
+            self.calls.append((name, args))
+            self.during(name, args)
+            return 0
+        return call
+
+    def blocks(self):
+        """The workspaces of the calls so far."""
+        at = {"sv_cache_reserve": 6, "sv_window_attention": 14}
+        return [args[at[name]].value for name, args in self.calls]
+
+
+@pytest.fixture
+def rig(monkeypatch):
+    """(library, cache, page table, lengths, q) with two sequences."""
+    build.build_library()
+    lib = Noted(api.load())
+    monkeypatch.setattr(api, "_new", lambda make, shape, dtype, like, stream: make(shape, dtype=dtype).as_subclass(OnGpu))
+    monkeypatch.setattr(api, "_raw_stream", lambda device: 7 + device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    k = gpu(1, 4, 2, 1, 64, dtype=torch.bfloat16)
+    cache = api.KVCache(k, k.clone(), gpu(4), gpu(1))
+    monkeypatch.setattr(api, "_lib", lib)
+    return lib, cache, gpu(2, 3), gpu(2), gpu(2, 1, 64, dtype=torch.bfloat16)
+
+
+def test_threads_on_one_stream_take_turns(rig):
+    """A call of two launches hands its results over in the stream's scratch: no other thread's may come between them."""
+    lib, cache, table, ctx, q = rig
+    busy, clashes = set(), []
+
+    def during(name, args):
+        ws = lib.blocks()[-1]
+        clashes.append(ws in busy)
+        busy.add(ws)
+        time.sleep(0.02)
+        busy.discard(ws)
+
+    lib.during = during
+    calls = [lambda: api.sv_window_attention(q, cache, 0, table, ctx), lambda: api.sv_cache_reserve(cache, table, ctx)]
+    threads = [threading.Thread(target=lambda i=i: [calls[i % 2]() for _ in range(4)]) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(clashes) == 16 and not any(clashes)
