@@ -650,13 +650,18 @@ class KVCache:
     def _scratch(self, stream) -> _Scratch:
         """What calls on `stream` share. A call that is being captured gets
         scratch of its graph's own."""
-        if stream is None:
-            key = _raw_stream(self.k.get_device())
-            capturing = torch.cuda.is_current_stream_capturing()
-        else:
+        device = self.k.get_device()
+        if stream is not None:
             key = stream.cuda_stream
             with torch.cuda.stream(stream):
                 capturing = torch.cuda.is_current_stream_capturing()
+        else:
+            key = _raw_stream(device)
+            if device == torch.cuda.current_device():
+                capturing = torch.cuda.is_current_stream_capturing()
+            else:
+                with torch.cuda.device(device):
+                    capturing = torch.cuda.is_current_stream_capturing()
         if capturing:
             return _Scratch()
         return self._scratches.get(key) or self._scratches.setdefault(key, _Scratch())

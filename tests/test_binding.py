@@ -79,3 +79,31 @@ def test_threads_on_one_stream_take_turns(rig):
     for t in threads:
         t.join()
     assert len(clashes) == 16 and not any(clashes)
+
+
+def test_capture_is_asked_of_the_caches_device(rig, monkeypatch):
+    """The current stream of another device may be capturing, or not be, when the cache's is (not)."""
+    lib, cache, table, ctx, q = rig
+    current = [1]
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            self.was, current[0] = current[0], self.device
+
+        def __exit__(self, *e):
+            current[0] = self.was
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    blocks = []
+    for capturing in (None, 0, 1):  # the device whose current stream captures
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: current[0] == capturing)
+        api.sv_window_attention(q, cache, 0, table, ctx)
+        blocks.append(lib.blocks()[-1])
+        kept = [s.block.data_ptr() for s in cache._scratches.values()]
+        assert kept == blocks[:1]
+    assert current == [1]
+    assert blocks[2] == blocks[0] != blocks[1]
