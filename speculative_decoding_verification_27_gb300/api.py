@@ -671,7 +671,7 @@ class KVCache:
         scratch = self._scratch(stream)
         with scratch.lock:
             if scratch.block is None or scratch.block.numel() < nbytes:
-                scratch.block = _new(torch.empty, max(nbytes, self._attention_bytes), torch.uint8, self.k, stream)
+                scratch.block = _new(torch.empty, nbytes, torch.uint8, self.k, stream)
             call(scratch.block)
 
 

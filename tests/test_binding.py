@@ -107,3 +107,16 @@ def test_capture_is_asked_of_the_caches_device(rig, monkeypatch):
         assert kept == blocks[:1]
     assert current == [1]
     assert blocks[2] == blocks[0] != blocks[1]
+
+
+def test_scratch_is_as_large_as_the_calls_need(rig):
+    """A stream that only reserves pages holds a few bytes a sequence; the attention's partial results come with its first call."""
+    lib, cache, table, ctx, q = rig
+    api.sv_cache_reserve(cache, table, ctx)
+    scratch, = cache._scratches.values()
+    assert scratch.block.numel() == lib.real.sv_cache_reserve_workspace_size(2)
+    api.sv_window_attention(q, cache, 0, table, ctx)
+    size = lib.real.sv_window_attention_workspace_size(cache._ref, 1, 2)
+    assert scratch.block.numel() == size > 1 << 20
+    api.sv_cache_reserve(cache, table, ctx)
+    assert scratch.block.numel() == size
