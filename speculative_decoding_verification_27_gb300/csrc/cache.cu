@@ -621,9 +621,7 @@ sv_status sv_cache_reserve(const sv_kv_cache* cache, const sv_sequences* seqs, i
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const int smem = 3 * ((S.n + 4) & ~3) * 4;
   static std::atomic<unsigned long long> allowed{0};
-  if (smem > 48 * 1024 &&
-      allow_smem(cache::reserve_kernel, 3 * 4 * (SV_CACHE_MAX_SEQS + 4), allowed) != cudaSuccess)
-    return SV_ERR_CUDA;
+  if (allow_smem(cache::reserve_kernel, 3 * 4 * (SV_CACHE_MAX_SEQS + 4), allowed) != cudaSuccess) return SV_ERR_CUDA;
   cache::ReserveWs* ws = static_cast<cache::ReserveWs*>(workspace);
   if (launch_overlapped(cache::reserve_kernel, dim3(1), cache::kR, smem, 1, st, C, S, W, granted, ws, status) != cudaSuccess)
     return SV_ERR_CUDA;

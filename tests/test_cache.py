@@ -1,7 +1,10 @@
 """The page operations (sv_cache_*) against the same operations on host
 lists, their refusals (CPU) and their data errors."""
 import ctypes
+import os
 import random
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -517,3 +520,25 @@ def test_a_captured_step(cuda_lib):
         r.m.append(names, granted)
         r.m.commit([(0, x) for x in keep])
         r.check()
+
+
+_BATCHES = """
+import torch
+from speculative_decoding_verification_27_gb300 import api
+k = torch.zeros(1, 4096, 2, 1, 8, device="cuda")
+for n in (3399, 3400, 4095, 4096):
+    cache = api.KVCache(k, k.clone())
+    table = torch.full((n, 1), -1, dtype=torch.int32, device="cuda")
+    got = api.sv_cache_reserve(cache, table, torch.zeros(n, dtype=torch.int32, device="cuda"))
+    assert bool((got == 1).all()) and table[:, 0].tolist() == list(range(n)), n
+print("all granted")
+"""
+
+
+@pytest.mark.gpu
+def test_batches_around_the_default_shared_memory(cuda_lib):
+    """The largest batches that fit the shared memory a kernel has without asking, and the next ones, in a process of their own: a
+    larger batch before them would ask for all."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", _BATCHES], cwd=root, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0 and "all granted" in p.stdout, p.stderr[-2000:]
