@@ -30,6 +30,7 @@
 // CTAs an SM with four loads a batch beat 3 and 5 CTAs and 2 to 8 loads.
 #include "../../include/spec_verify.h"
 #include "sv_device.cuh"
+#include "sv_launch.cuh"
 
 #include <climits>
 #include <cmath>
@@ -742,8 +743,7 @@ extern "C" sv_status sv_token_logprobs(const void* logits, sv_dtype dtype, int32
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = cl > 1 ? 1 : 0;
-  cudaError_t e = dtype == SV_BF16 ? cudaLaunchKernelEx(&cfg, lp::logprobs_kernel<1>, P, cl)
-                                   : cudaLaunchKernelEx(&cfg, lp::logprobs_kernel<0>, P, cl);
-  if (e == cudaSuccess) e = cudaGetLastError();
+  const cudaError_t e = own_error(dtype == SV_BF16 ? cudaLaunchKernelEx(&cfg, lp::logprobs_kernel<1>, P, cl)
+                                                   : cudaLaunchKernelEx(&cfg, lp::logprobs_kernel<0>, P, cl));
   return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }

@@ -32,6 +32,13 @@ __device__ __forceinline__ uint4 ld_once16(const void* p) {
   return v;
 }
 
+// A call's own status, which is returned; the runtime keeps it too, for the
+// next one who asks about errors, unless it is taken back.
+inline cudaError_t own_error(cudaError_t e) {
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e;
+}
+
 template <typename... K, typename... A>
 cudaError_t launch_overlapped(void (*kernel)(K...), dim3 grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t st,
                               A... args) {
@@ -51,8 +58,7 @@ cudaError_t launch_overlapped(void (*kernel)(K...), dim3 grid, unsigned threads,
     cfg.numAttrs = 2;
   }
   cfg.attrs = at;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<K>(args)...);
-  return e == cudaSuccess ? cudaGetLastError() : e;
+  return own_error(cudaLaunchKernelEx(&cfg, kernel, static_cast<K>(args)...));
 }
 
 // Allows the kernel that much dynamic shared memory, once per device (`done`
@@ -60,11 +66,11 @@ cudaError_t launch_overlapped(void (*kernel)(K...), dim3 grid, unsigned threads,
 template <typename F>
 cudaError_t allow_smem(F* kernel, size_t bytes, std::atomic<unsigned long long>& done) {
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = own_error(cudaGetDevice(&dev));
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
   if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  e = own_error(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }

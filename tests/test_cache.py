@@ -542,3 +542,53 @@ def test_batches_around_the_default_shared_memory(cuda_lib):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     p = subprocess.run([sys.executable, "-c", _BATCHES], cwd=root, capture_output=True, text=True, timeout=300)
     assert p.returncode == 0 and "all granted" in p.stdout, p.stderr[-2000:]
+
+
+@pytest.mark.gpu
+def test_a_launch_that_fails_leaves_no_error(cuda_lib):
+    """Calls on a stream whose capture has become invalid report it, and leave nothing for the next one to find."""
+    from test_logprobs import _logits
+    rt = ctypes.CDLL("libcudart.so.13")
+    stream = ctypes.c_void_p()
+    r = Rig(n=2, page=4, n_pages=9)
+    new = torch.zeros(r.L, 2, r.H, r.D, dtype=r.dtype, device="cuda")
+    z, tok = (x.cuda() for x in _logits(2, 100, torch.float32, 1))
+    one = r.i32([0])
+    torch.cuda.synchronize()
+
+    class S:  # what the binding takes of a stream
+        cuda_stream = 0
+
+    assert rt.cudaStreamCreateWithFlags(ctypes.byref(stream), 1) == 0
+    S.cuda_stream = stream.value
+    q = torch.zeros(2, r.H, r.D, dtype=r.dtype, device="cuda")
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    granted = r.i32([0, 0])
+    outs = api.sv_token_logprobs(z, tok)
+    torch.cuda.synchronize()
+    calls = [lambda: api.sv_cache_free(*r.args(), one, stream=S), lambda: api.sv_cache_fork(*r.args(), one, r.i32([1]), stream=S),
+             lambda: api.sv_cache_reserve(*r.args(), granted=granted, workspace=ws, stream=S),
+             lambda: api.sv_cache_append(r.cache, 0, new, new, r.table, r.ctx, stream=S),
+             lambda: api.sv_cache_commit(*r.args(), None, granted, stream=S),
+             lambda: api.sv_window_attention(q, r.cache, 0, r.table, r.ctx, out=q, workspace=ws, stream=S),
+             lambda: api.sv_token_logprobs(z, tok, out_logprob=outs.logprob, out_rank=outs.rank, out_entropy=outs.entropy, stream=S)]
+    rt.cudaStreamBeginCapture.argtypes = [ctypes.c_void_p, ctypes.c_int]
+    rt.cudaStreamSynchronize.argtypes = [ctypes.c_void_p]
+    rt.cudaStreamEndCapture.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+    rt.cudaStreamDestroy.argtypes = [ctypes.c_void_p]
+    left = []
+    try:
+        for call in calls:
+            graph = ctypes.c_void_p()
+            assert rt.cudaStreamBeginCapture(stream, 2) == 0  # relaxed: nothing else is affected
+            assert rt.cudaStreamSynchronize(stream) != 0      # not allowed meanwhile: the capture is invalid from here on
+            rt.cudaGetLastError()
+            with pytest.raises(api.SpecVerifyError):
+                call()
+            left.append(rt.cudaGetLastError())
+            rt.cudaStreamEndCapture(stream, ctypes.byref(graph))
+            rt.cudaGetLastError()
+    finally:
+        rt.cudaStreamDestroy(stream)
+    assert left == [0] * len(calls)
+    assert api.sv_cache_reserve(*r.args()).tolist() == [1, 1]
