@@ -73,10 +73,10 @@ struct Unit {
 };
 
 // Request b's window, tokens and key tiles, and its number of row tiles (0 tiles where there is nothing to do).
-template <int MT>
+template <int MT, bool kWarp>
 __device__ __forceinline__ void load_request(const Params& P, int b, Unit& u, bool tell) {
   u.b = b;
-  u.w = find_window(P.W, b);
+  u.w = find_window<kWarp>(P.W, b);
   u.ctx = P.S.ctx[b];
   const bool len = length_ok(P.C, P.S, u.ctx), fits = len && length_ok(P.C, P.S, (long long)u.ctx + max(u.w.rows, 0));
   if (u.w.rows <= 0 || !fits) {
@@ -85,9 +85,6 @@ __device__ __forceinline__ void load_request(const Params& P, int b, Unit& u, bo
     u.keys = u.tiles = u.n_mt = 0;
     return;
   }
-  if (tell && P.W.cand)
-    for (int c = u.w.c0; c < u.w.c1; ++c)
-      if (P.W.cu[c + 1] < P.W.cu[c]) set_status(P.status, SV_DATA_BAD_OFFSETS);
   u.keys = u.ctx + u.w.rows;
   u.tiles = (u.keys + kTK - 1) / kTK;
   u.n_mt = (int)(((long long)u.w.rows * P.group + MT - 1) / MT);
@@ -130,7 +127,7 @@ __device__ __forceinline__ bool take_share(const Params& P, const Plan& L, Share
   const int per = (P.S.n + kThr - 1) / kThr;
   long long mine = 0;
   for (int b = tid * per; b < min((tid + 1) * per, P.S.n); ++b) {
-    load_request<MT>(P, b, c.u, blockIdx.x == 0);
+    load_request<MT, false>(P, b, c.u, blockIdx.x == 0);
     mine += (long long)c.u.tiles * c.u.n_mt * P.C.n_heads;
   }
   long long incl = mine;
@@ -159,7 +156,7 @@ __device__ __forceinline__ bool take_share(const Params& P, const Plan& L, Share
     long long at = incl - mine;
     if (per > 1)
       for (int b = tid * per;; ++b) {
-        load_request<MT>(P, b, c.u, false);
+        load_request<MT, false>(P, b, c.u, false);
         const long long n = (long long)c.u.tiles * c.u.n_mt * P.C.n_heads;
         if (sh.t0 < at + n) break;
         at += n;
@@ -175,7 +172,7 @@ __device__ __forceinline__ bool take_share(const Params& P, const Plan& L, Share
   return true;
 }
 
-// On to the next unit's first tile (the share holds one).
+// On to the next unit's first tile (the share holds one), by a whole warp.
 template <int MT>
 __device__ __forceinline__ void next_unit(const Params& P, Cursor& c) {
   c.tile = 0;
@@ -184,7 +181,7 @@ __device__ __forceinline__ void next_unit(const Params& P, Cursor& c) {
   if (++c.u.head < P.C.n_heads) return;
   c.u.head = 0;
   for (int b = c.u.b + 1; b < P.S.n; ++b) {
-    load_request<MT>(P, b, c.u, false);
+    load_request<MT, true>(P, b, c.u, false);
     if (c.u.tiles) return;
   }
 }

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kR) reserve_kernel(CacheView C, SeqView S, Win
   __syncthreads();
   for (int b = tid; b < S.n; b += kR) {
     const int len = S.ctx[b];
-    const Window w = find_window(W, b);
+    const Window w = find_window<false>(W, b);
     const int32_t* row = S.table + (long long)b * S.stride;
     int have = -1, need = 0, part = -1;
     uint32_t bad = 0;
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kR) reserve_kernel(CacheView C, SeqView S, Win
   for (int b = tid; b < S.n; b += kR) {
     const bool late = b >= end && (s_first[b + 1] > s_first[b] || s_part[b] >= 0);
     if (late) s_have[b] = -1;
-    if (granted) granted[b] = s_have[b] >= 0 ? find_window(W, b).rows : 0;
+    if (granted) granted[b] = s_have[b] >= 0 ? find_window<false>(W, b).rows : 0;
   }
   int taken = 0;
   for (int w0 = 0; w0 < n_words && taken < total; w0 += kR) {
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kT) append_kernel(CacheView C, SeqView S, Wind
   const bool whole = C.head_b == C.head_bytes;  // a token's heads lie together
   for (int b = blockIdx.y; b < S.n; b += gridDim.y) {
     const int len = S.ctx[b];
-    const Window w = find_window(W, b);
+    const Window w = find_window<true>(W, b);
     if (w.rows < 0 || !length_ok(C, S, len)) {
       if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0)
         set_status(status, w.rows < 0 ? SV_DATA_BAD_OFFSETS : SV_DATA_BAD_SEQ);
@@ -479,7 +479,7 @@ __device__ __forceinline__ Kept kept_rows(const CacheView& C, const SeqView& S, 
   const bool c_ok = c >= 0 && c < W.n_cand;
   const int n = c_ok ? out_len[c] : 0;
   const int cu0 = c_ok && W.cu ? W.cu[c] : 0, cu1 = c_ok && W.cu ? W.cu[c + 1] : 0;
-  const Window w = find_window(W, b);
+  const Window w = find_window<true>(W, b);
   if (w.rows < 0) return Kept{0, 0, SV_DATA_BAD_OFFSETS};
   if (!length_ok(C, S, len)) return Kept{0, 0, SV_DATA_BAD_SEQ};
   if (best && c == -1) return Kept{0, 0, 0};

@@ -87,15 +87,29 @@ __device__ __forceinline__ void set_status(uint32_t* status, uint32_t bit) {
 
 // Request b's candidates [c0, c1) and window rows [r0, r0 + rows); rows = -1
 // where the offsets are out of order or out of range (R < 0: no row limit).
+// A request's candidates are looked over by the whole warp (all lanes with
+// the same b) or, with kWarp false, by the thread.
 struct Window {
   int c0, c1, r0, rows;
 };
+template <bool kWarp>
 __device__ __forceinline__ Window find_window(const WindowView& W, int b) {
   if (!W.cu) return W.R < 0 || b < W.R ? Window{b, b + 1, b, 1} : Window{b, b, 0, -1};
   const int c0 = W.cand ? W.cand[b] : b, c1 = W.cand ? W.cand[b + 1] : b + 1;
   if (c0 < 0 || c1 < c0 || c1 > W.n_cand) return Window{0, 0, 0, -1};
-  const long long r0 = (long long)W.cu[c0] + c0, r1 = (long long)W.cu[c1] + c1;
-  if (W.cu[c0] < 0 || r1 < r0 + (c1 - c0) || r1 > 0x7fffffffll || (W.R >= 0 && r1 > W.R)) return Window{0, 0, 0, -1};
+  const int first = W.cu[c0], end = W.cu[c1];
+  bool bad = false;
+  if (W.cand) {  // (looked at beside the two above: behind their test it is one more round trip to memory)
+    if constexpr (kWarp) {
+      for (int c = c0 + (int)(threadIdx.x & 31); c < c1; c += 32) bad |= W.cu[c + 1] < W.cu[c];
+      bad = __any_sync(kFull, bad);
+    } else {
+#pragma unroll 4
+      for (int c = c0; c < c1; ++c) bad |= W.cu[c + 1] < W.cu[c];
+    }
+  }
+  const long long r0 = (long long)first + c0, r1 = (long long)end + c1;
+  if (bad || first < 0 || r1 < r0 + (c1 - c0) || r1 > 0x7fffffffll || (W.R >= 0 && r1 > W.R)) return Window{0, 0, 0, -1};
   return Window{c0, c1, (int)r0, (int)(r1 - r0)};
 }
 

@@ -592,3 +592,41 @@ def test_a_launch_that_fails_leaves_no_error(cuda_lib):
         rt.cudaStreamDestroy(stream)
     assert left == [0] * len(calls)
     assert api.sv_cache_reserve(*r.args()).tolist() == [1, 1]
+
+
+@pytest.mark.gpu
+def test_candidates_whose_offsets_decrease(cuda_lib):
+    """Offsets that decrease inside a request are found by every call, which leaves that request alone and serves the others."""
+    r = Rig(n=3, page=4, n_pages=30, width=6)
+    r.ctx.copy_(r.i32([3, 2, 0]))
+    r.table[:, 0] = r.i32([0, 1, -1])
+    r.cache.page_ref[:2] = 1
+    r.cache.free_bits[0] &= ~3
+    cand, good, bad = r.i32([0, 1, 4, 5]), r.i32([0, 1, 4, 5, 6, 8]), r.i32([0, 1, 4, 3, 6, 8])
+    R = 13
+    state = lambda: [x.clone() for x in (r.table, r.ctx, r.cache.page_ref)]  # noqa: E731
+    before = state()
+    granted = api.sv_cache_reserve(*r.args(), bad, cand, status=r.status)
+    assert granted.tolist() == [2, 0, 3] and r.bits() == api.SV_DATA_BAD_OFFSETS
+    assert all(torch.equal(a[1:2], b[1:2]) for a, b in zip(before[:2], state()[:2]))
+    assert api.sv_cache_reserve(*r.args(), good, cand, status=r.status).tolist() == [2, 8, 3] and r.bits() == 0
+    r.cache.k.zero_()
+    r.cache.v.zero_()
+    new = torch.ones(r.L, R, r.H, r.D, dtype=r.dtype, device="cuda")
+    api.sv_cache_append(r.cache, 0, new, new, r.table, r.ctx, bad, cand, status=r.status)
+    assert r.bits() == api.SV_DATA_BAD_OFFSETS
+    row = r.table[1, :3].long()
+    assert bool((r.cache.k[:, row] == 0).all()) and bool((r.cache.v[:, row] == 0).all())
+    assert int((r.cache.k[0, :, :, 0, 0] == 1).sum()) == 5  # the rows of the other two
+    q = torch.ones(R, 2 * r.H, r.D, dtype=r.dtype, device="cuda")
+    out = torch.full_like(q, 7.0)
+    api.sv_window_attention(q, r.cache, 0, r.table, r.ctx, bad, cand, out=out, status=r.status)
+    assert r.bits() == api.SV_DATA_BAD_OFFSETS
+    assert bool((out[2:10] == 7).all()) and not bool((out[:2] == 7).any()) and not bool((out[10:13] == 7).any())
+    before = state()
+    api.sv_cache_commit(*r.args(), bad, r.i32([1, 2, 0, 2, 1]), cand, r.i32([0, 3, 4]), status=r.status)
+    assert r.bits() == api.SV_DATA_BAD_OFFSETS
+    after = state()
+    assert after[1].tolist() == [4, 2, 1] and torch.equal(before[0][1], after[0][1])
+    api.sv_cache_commit(*r.args(), good, r.i32([0, 3, 0, 0, 0]), cand, r.i32([0, 1, 4]), status=r.status)
+    assert r.bits() == 0 and r.ctx.tolist() == [4, 5, 1]
