@@ -88,7 +88,8 @@ __global__ void __launch_bounds__(kT) fork_kernel(CacheView C, SeqView S, int N,
   const int32_t* from = S.table + (long long)s * S.stride;
   int32_t* to = S.table + (long long)d * S.stride;
   bool good = true;
-  for (int k = lane; k < n; k += 32) good &= from[k] >= 0 && from[k] < C.n_pages;
+  // A page that the counts call free is not the source's. (Forks beside this one only raise the counts of pages that have a holder.)
+  for (int k = lane; k < n; k += 32) good &= from[k] >= 0 && from[k] < C.n_pages && C.ref[from[k]] >= 1;
   if (!__all_sync(kFull, good)) {
     if (lane == 0) set_status(status, SV_DATA_BAD_PAGE);
     return;
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(kT) fork_kernel(CacheView C, SeqView S, int N,
   for (int k = lane; k < n; k += 32) {
     const int page = from[k];
     to[k] = page;
-    if (atomicAdd(&C.ref[page], 1) < 1) set_status(status, SV_DATA_BAD_PAGE);
+    atomicAdd(&C.ref[page], 1);
   }
   if (lane == 0) S.ctx[d] = len;
 }

@@ -630,3 +630,28 @@ def test_candidates_whose_offsets_decrease(cuda_lib):
     assert after[1].tolist() == [4, 2, 1] and torch.equal(before[0][1], after[0][1])
     api.sv_cache_commit(*r.args(), good, r.i32([0, 3, 0, 0, 0]), cand, r.i32([0, 1, 4]), status=r.status)
     assert r.bits() == 0 and r.ctx.tolist() == [4, 5, 1]
+
+
+@pytest.mark.gpu
+def test_fork_of_a_page_without_holders(cuda_lib):
+    """A table whose page the counts call free is not forked: nothing of it is written, and the page stays what it was."""
+    rng = random.Random(8)
+    r = Rig(page=4, n=4, n_pages=30)
+    r.step(rng)
+    r.step(rng)
+    r.m.free([2, 3])
+    api.sv_cache_free(*r.args(), r.i32([2, 3]))
+    r.check()
+    b = max((0, 1), key=lambda x: r.m.ctx[x])
+    assert r.m.ctx[b] > 0
+    page = r.m.table[b][r.m.pages(r.m.ctx[b]) - 1]
+    for count in (0, -1):
+        r.cache.page_ref[page] = count
+        before = [x.clone() for x in (r.table, r.ctx, r.cache.page_ref, r.cache.free_bits)]
+        api.sv_cache_fork(*r.args(), r.i32([b, b]), r.i32([2, 3]), status=r.status)
+        assert r.bits() == api.SV_DATA_BAD_PAGE
+        assert all(torch.equal(x, y) for x, y in zip(before, (r.table, r.ctx, r.cache.page_ref, r.cache.free_bits)))
+    r.cache.page_ref[page] = 1
+    api.sv_cache_fork(*r.args(), r.i32([b, b]), r.i32([2, 3]), status=r.status)
+    assert not r.m.fork([b, b], [2, 3]) and r.bits() == 0
+    r.check()
