@@ -651,7 +651,7 @@ sv_status sv_cache_append(const sv_kv_cache* cache, int32_t layer, int32_t n_lay
   if (!k_new || !v_new || (uintptr_t)k_new % 16 || (uintptr_t)v_new % 16) return SV_ERR_INVALID_ARG;
   // A warp a row of the mean window, up to eight CTAs an SM.
   const int gy = cache::y_grid(S.n), gz = n_layers < 64 ? n_layers : 64;
-  const long long gx = ((R + gy - 1) / gy + cache::kT / 32 - 1) / (cache::kT / 32);
+  const long long gx = (((long long)R + gy - 1) / gy + cache::kT / 32 - 1) / (cache::kT / 32);
   const long long most = (152 * 8 + (long long)gy * gz - 1) / ((long long)gy * gz);
   return cache::launch(cache::append_kernel, dim3((unsigned)(gx < most ? gx : most), gy, gz), static_cast<cudaStream_t>(cuda_stream),
       C, S, W, layer, n_layers, static_cast<const char*>(k_new), static_cast<const char*>(v_new), new_layer_stride * es,

@@ -655,3 +655,17 @@ def test_fork_of_a_page_without_holders(cuda_lib):
     api.sv_cache_fork(*r.args(), r.i32([b, b]), r.i32([2, 3]), status=r.status)
     assert not r.m.fork([b, b], [2, 3]) and r.bits() == 0
     r.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 3])
+def test_append_of_the_longest_list_of_rows(cuda_lib, n):
+    """R may be any int32: here one row that stands for all of them, of which the windows take a few."""
+    r = Rig(n=n, page=4, n_pages=9)
+    cu = r.i32([2 * b for b in range(n + 1)])
+    api.sv_cache_reserve(*r.args(), cu)
+    new = torch.randn(1, 1, r.H, r.D, device="cuda").to(r.dtype).expand(1, 2 ** 31 - 1, r.H, r.D)
+    api.sv_cache_append(r.cache, 1, new, new, r.table, r.ctx, cu, status=r.status)
+    assert r.bits() == 0
+    for b in range(n):
+        assert torch.equal(r.cache.k[1, int(r.table[b, 0]), :3], new[0, :3]) and torch.equal(r.cache.v[1, int(r.table[b, 0]), :3], new[0, :3])
