@@ -605,6 +605,18 @@ class _Sequences(ctypes.Structure):
 _pack_sequences = struct.Struct("@PqiiP").pack  # _Sequences as bytes: the library reads it during the call only
 
 
+def _steps(t: torch.Tensor) -> list:
+    """The strides that are taken: a dimension of one element takes no step, and its stride may be anything."""
+    return [s if m > 1 else 0 for s, m in zip(t.stride(), t.shape)]
+
+
+def _heads_contiguous(t: torch.Tensor) -> bool:
+    """Whether the last two dimensions, heads and their elements, lie together."""
+    heads, D = t.shape[-2:]
+    step, one = t.stride()[-2:]
+    return one == 1 and (step == D or heads == 1)
+
+
 class _Scratch:
     """Scratch of the calls on one stream, whose kernels run in order. A call
     of two launches hands its results over in the block, so no other thread's
@@ -625,7 +637,7 @@ class KVCache:
     int32 has a bit set per free page; without them the cache starts empty."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, page_ref=None, free_bits=None):
-        if k.dim() != 5 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.device != v.device:
+        if k.dim() != 5 or k.shape != v.shape or _steps(k) != _steps(v) or k.dtype != v.dtype or k.device != v.device:
             raise ValueError("k and v must be [layers, pages, page_size, kv_heads, head_dim] with equal strides")
         if not k.is_cuda or (k.shape[4] > 1 and k.stride(4) != 1):
             raise ValueError("k and v must be CUDA tensors with a contiguous last dimension")
@@ -639,9 +651,7 @@ class KVCache:
                 free_bits[-1] = (1 << n % 32) - 1
         self.k, self.v, self.page_ref, self.free_bits = k, v, page_ref, free_bits
         self.n_layers, self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = k.shape
-        # A dimension of one element takes no step; its stride may be anything.
-        steps = [s if m > 1 else 0 for s, m in zip(k.stride(), k.shape)]
-        self._c = _Cache(k.data_ptr(), v.data_ptr(), _dtype(k), *k.shape, *steps[:4],
+        self._c = _Cache(k.data_ptr(), v.data_ptr(), _dtype(k), *k.shape, *_steps(k)[:4],
                          _vec(page_ref, "page_ref", torch.int32, (n,)), _vec(free_bits, "free_bits", torch.int32, (words,)))
         self._ref = ctypes.byref(self._c)
         self._attention_bytes = load().sv_window_attention_workspace_size(self._ref, self.n_kv_heads, 0)
@@ -746,7 +756,8 @@ def sv_cache_append(cache: KVCache, layer: int, k_new: torch.Tensor, v_new: torc
     L, R = k_new.shape[:2]
     want = (L, R, cache.n_kv_heads, cache.head_dim)
     strides = k_new.stride()
-    if k_new.shape != want or v_new.shape != want or v_new.stride() != strides or strides[2:] != (cache.head_dim, 1) or \
+    if k_new.shape != want or v_new.shape != want or (v_new.stride() != strides and _steps(v_new) != _steps(k_new)) or \
+            not _heads_contiguous(k_new) or \
             k_new.dtype != cache.k.dtype or v_new.dtype != cache.k.dtype or not k_new.is_cuda or not v_new.is_cuda:
         raise ValueError("k_new and v_new must be CUDA tensors [n_layers, R, kv_heads, head_dim] of the cache's dtype, alike "
                          "in strides, with contiguous heads")
@@ -781,7 +792,7 @@ def sv_window_attention(q: torch.Tensor, cache: KVCache, layer: int, page_table:
     R, heads, D = q.shape
     if out is None:
         out = _new(torch.zeros, (R, heads, D), q.dtype, q, stream)
-    if out.shape != q.shape or out.dtype != q.dtype or not out.is_cuda or q.stride()[1:] != (D, 1) or out.stride()[1:] != (D, 1):
+    if out.shape != q.shape or out.dtype != q.dtype or not out.is_cuda or not _heads_contiguous(q) or not _heads_contiguous(out):
         raise ValueError("q and out must be [R, q_heads, head_dim] with contiguous heads")
     if out_lse is None and want_lse:
         out_lse = _new(torch.zeros, (R, heads), torch.float32, q, stream)

@@ -507,3 +507,36 @@ def test_two_threads_on_one_stream(cuda_lib):
     for i in range(2):
         assert len(got[i]) == 200
         assert all(torch.equal(g[0], want[i][0]) and torch.equal(g[1], want[i][1]) for g in got[i])
+
+
+@pytest.mark.gpu
+def test_dimensions_of_one_take_no_step(cuda_lib):
+    """One head, one row, one layer: their strides may be anything, as torch leaves them behind a transpose or a slice."""
+    c = Case([30, 7], [[2], [1]], 1, 1, 64, 16, BF, seed=4, cands=False)
+    c.check()
+    q, cache, layer, table, ctx, cu = c.args[:6]
+    want = api.sv_window_attention(q, cache, 0, table, ctx, cu)[0]
+    odd, out = (torch.empty(1, c.R, 64, dtype=BF, device="cuda").transpose(0, 1) for _ in range(2))  # [R, 1, D] of [1, R, D]
+    odd.copy_(q)
+    assert odd.stride(1) != 64 and odd.is_contiguous()
+    assert torch.equal(api.sv_window_attention(odd, cache, 0, table, ctx, cu)[0], want)
+    api.sv_window_attention(odd, cache, 0, table, ctx, cu, out=out)
+    assert torch.equal(out[:3], want[:3])
+    # Keys of one head, and a single row whose keys and values come from buffers of other widths.
+    k = torch.zeros(1, 6, 4, 1, 64, dtype=BF, device="cuda")
+    cache = api.KVCache(k, k.clone())
+    table = torch.full((1, 4), -1, dtype=torch.int32, device="cuda")
+    ctx = torch.zeros(1, dtype=torch.int32, device="cuda")
+    api.sv_cache_reserve(cache, table, ctx)
+    wide_k, wide_v = torch.randn(1, 1, 128, device="cuda").to(BF), torch.randn(1, 1, 192, device="cuda").to(BF)
+    api.sv_cache_append(cache, 0, wide_k[..., :64], wide_v[..., 64:128], table, ctx)
+    assert torch.equal(cache.k[0, 0, 0], wide_k[0, :, :64]) and torch.equal(cache.v[0, 0, 0], wide_v[0, :, 64:128])
+    # A cache of one layer whose K and V lie in buffers of different depth.
+    a, b = (torch.zeros(*s, 4, 1, 64, dtype=BF, device="cuda") for s in ((2, 6), (6, 1)))
+    b = b.transpose(0, 1)
+    assert a[:1].stride() != b.stride()
+    cache = api.KVCache(a[:1], b, cache.page_ref, cache.free_bits)  # the page is held
+    api.sv_cache_append(cache, 0, wide_k[..., :64], wide_v[..., 64:128], table, ctx)
+    assert torch.equal(a[0, 0, 0], wide_k[0, :, :64]) and torch.equal(b[0, 0, 0], wide_v[0, :, 64:128])
+    with pytest.raises(ValueError):
+        api.sv_window_attention(q.expand(-1, 2, -1), cache, 0, table, ctx, cu)
