@@ -544,6 +544,14 @@ def _vec(t: Optional[torch.Tensor], name: str, dtype, shape: tuple):
     return t.data_ptr()
 
 
+def _on_one_device(t: torch.Tensor, *others: Optional[torch.Tensor]):
+    """The kernels run on t's device and read the addresses of all."""
+    device = t.get_device()
+    for x in others:
+        if x is not None and x.get_device() != device:
+            raise ValueError("the tensors of a call must lie on one CUDA device")
+
+
 def sv_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *, cu_draft=None, out_len=None,
                       temperature: float = 1.0, n_top: int = 0, out_logprob=None, out_rank=None, out_entropy=None,
                       out_top_ids=None, out_top_logprobs=None, status=None, stream=None) -> TokenLogprobs:
@@ -574,6 +582,7 @@ def sv_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = Non
     if n_top > 0 and out_top_logprobs is None:
         out_top_logprobs = _new(make, (R, n_top), f32, logits, stream)
     rows, tops = (R,), (R, n_top)
+    _on_one_device(logits, tokens, cu_draft, out_len, out_logprob, out_rank, out_entropy, out_top_ids, out_top_logprobs, status)
     _launch("sv_token_logprobs", logits, stream, logits.data_ptr(), _dtype(logits), V, ld, R,
             _vec(tokens, "tokens", i32, rows), B, _vec(cu_draft, "cu_draft", i32, (B + 1,)),
             _vec(out_len, "out_len", i32, (B,)), temperature, n_top, _vec(out_logprob, "out_logprob", f32, rows),
@@ -649,6 +658,7 @@ class KVCache:
             free_bits = torch.full((words,), -1, dtype=torch.int32, device=k.device)
             if n % 32:
                 free_bits[-1] = (1 << n % 32) - 1
+        _on_one_device(k, page_ref, free_bits)
         self.k, self.v, self.page_ref, self.free_bits = k, v, page_ref, free_bits
         self.n_layers, self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = k.shape
         self._c = _Cache(k.data_ptr(), v.data_ptr(), _dtype(k), *k.shape, *_steps(k)[:4],
@@ -710,6 +720,7 @@ def sv_cache_fork(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Tenso
                   status=None, stream=None) -> None:
     """Sequences dst[i] (empty) become copies of src[i] that share its pages."""
     N = src.shape[0]
+    _on_one_device(cache.k, page_table, ctx_len, src, dst, status)
     _launch("sv_cache_fork", cache.k, stream, cache._ref, _seqs(page_table, ctx_len), N, _vec(src, "src", torch.int32, (N,)),
             _vec(dst, "dst", torch.int32, (N,)), _vec(status, "status", torch.int32, (1,)))
 
@@ -718,6 +729,7 @@ def sv_cache_free(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Tenso
                   stream=None) -> None:
     """Ends the sequences `which`: their pages are released."""
     N = which.shape[0]
+    _on_one_device(cache.k, page_table, ctx_len, which, status)
     _launch("sv_cache_free", cache.k, stream, cache._ref, _seqs(page_table, ctx_len), N,
             _vec(which, "which", torch.int32, (N,)), _vec(status, "status", torch.int32, (1,)))
 
@@ -734,6 +746,7 @@ def sv_cache_reserve(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Te
     n = page_table.shape[0]
     if granted is None:
         granted = _new(torch.empty, n, torch.int32, page_table, stream)
+    _on_one_device(cache.k, page_table, ctx_len, cu_draft, cu_cand, granted, workspace, status)
 
     def call(ws):
         _launch("sv_cache_reserve", cache.k, stream, cache._ref, _seqs(page_table, ctx_len), *_windows(n, cu_draft, cu_cand),
@@ -761,6 +774,7 @@ def sv_cache_append(cache: KVCache, layer: int, k_new: torch.Tensor, v_new: torc
             k_new.dtype != cache.k.dtype or v_new.dtype != cache.k.dtype or not k_new.is_cuda or not v_new.is_cuda:
         raise ValueError("k_new and v_new must be CUDA tensors [n_layers, R, kv_heads, head_dim] of the cache's dtype, alike "
                          "in strides, with contiguous heads")
+    _on_one_device(cache.k, k_new, v_new, page_table, ctx_len, cu_draft, cu_cand, status)
     _launch("sv_cache_append", cache.k, stream, cache._ref, int(layer), L, k_new.data_ptr(), v_new.data_ptr(),
             strides[0] if L > 1 else 0, strides[1] if R > 1 else 0, R, _seqs(page_table, ctx_len),
             *_windows(page_table.shape[0], cu_draft, cu_cand), _vec(status, "status", torch.int32, (1,)))
@@ -775,6 +789,7 @@ def sv_cache_commit(cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Ten
     if (cu_cand is None) != (best is None):
         raise ValueError("cu_cand and best come together")
     win = _windows(n, cu_draft, cu_cand)
+    _on_one_device(cache.k, page_table, ctx_len, cu_draft, out_len, cu_cand, best, status)
     _launch("sv_cache_commit", cache.k, stream, cache._ref, _seqs(page_table, ctx_len), *win,
             _vec(best, "best", torch.int32, (n,)), _vec(out_len, "out_len", torch.int32, (win[0],)),
             _vec(status, "status", torch.int32, (1,)))
@@ -796,6 +811,7 @@ def sv_window_attention(q: torch.Tensor, cache: KVCache, layer: int, page_table:
         raise ValueError("q and out must be [R, q_heads, head_dim] with contiguous heads")
     if out_lse is None and want_lse:
         out_lse = _new(torch.zeros, (R, heads), torch.float32, q, stream)
+    _on_one_device(cache.k, q, page_table, ctx_len, cu_draft, cu_cand, out, out_lse, workspace, status)
 
     def call(ws):
         _launch("sv_window_attention", q, stream, q.data_ptr(), q.stride(0) if R > 1 else heads * D, heads, R, cache._ref,

@@ -15,7 +15,7 @@ class OnGpu(torch.Tensor):
     is_cuda = property(lambda self: True)
 
     def get_device(self):
-        return 0
+        return getattr(self, "gpu_index", 0)
 
 
 def gpu(*shape, dtype=torch.int32):
@@ -120,3 +120,40 @@ def test_scratch_is_as_large_as_the_calls_need(rig):
     assert scratch.block.numel() == size > 1 << 20
     api.sv_cache_reserve(cache, table, ctx)
     assert scratch.block.numel() == size
+
+
+def test_tensors_of_another_device_are_refused(rig):
+    """Every tensor of a call lies on the cache's (or the logits') device: the kernel reads its address there."""
+    lib, cache, table, ctx, q = rig
+    i1, i2, i3, i4 = (gpu(n) for n in (1, 2, 3, 4))
+    f2, out, ws = gpu(2, dtype=torch.float32), gpu(2, 1, 64, dtype=torch.bfloat16), gpu(1 << 26, dtype=torch.uint8)
+    new, z, status = gpu(1, 2, 1, 64, dtype=torch.bfloat16), gpu(2, 8, dtype=torch.float32), gpu(1)
+    top_i, top_f = gpu(2, 2), gpu(2, 2, dtype=torch.float32)
+    seqs = dict(page_table=table, ctx_len=ctx, status=status)
+    win = dict(cu_draft=i3, cu_cand=i3.clone())
+    calls = [(api.sv_cache_fork, dict(cache=cache, src=i1, dst=i1.clone(), **seqs)),
+             (api.sv_cache_free, dict(cache=cache, which=i1, **seqs)),
+             (api.sv_cache_reserve, dict(cache=cache, granted=i2, workspace=ws, **seqs, **win)),
+             (api.sv_cache_append, dict(cache=cache, layer=0, k_new=new, v_new=new.clone(), **seqs, **win)),
+             (api.sv_cache_commit, dict(cache=cache, out_len=i2, best=i2.clone(), **seqs, **win)),
+             (api.sv_window_attention, dict(cache=cache, q=q, layer=0, out=out, out_lse=f2.view(2, 1), workspace=ws, **seqs, **win)),
+             (api.sv_token_logprobs, dict(logits=z, tokens=i2, cu_draft=i3, out_len=i2.clone(), n_top=2, out_logprob=f2, out_rank=i2,
+                                          out_entropy=f2.clone(), out_top_ids=top_i, out_top_logprobs=top_f, status=status))]
+    checked = 0
+    for call, args in calls:
+        call(**args)
+        n = len(lib.calls)
+        for name, t in args.items():
+            if isinstance(t, torch.Tensor):
+                elsewhere = t.clone()
+                elsewhere.gpu_index = 1
+                with pytest.raises(ValueError):
+                    call(**dict(args, **{name: elsewhere}))
+                checked += 1
+        assert len(lib.calls) == n
+    assert checked == 49
+    for page_ref, free_bits in ((0, 1), (1, 0)):
+        counts = [gpu(4), gpu(1)]
+        counts[0].gpu_index, counts[1].gpu_index = page_ref, free_bits
+        with pytest.raises(ValueError):
+            api.KVCache(cache.k, cache.v, *counts)
