@@ -669,3 +669,38 @@ def test_append_of_the_longest_list_of_rows(cuda_lib, n):
     assert r.bits() == 0
     for b in range(n):
         assert torch.equal(r.cache.k[1, int(r.table[b, 0]), :3], new[0, :3]) and torch.equal(r.cache.v[1, int(r.table[b, 0]), :3], new[0, :3])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page,n_pages,cands", [(7, 20, None), (1, 60, [0, 1, 2, 4]), (16, 12, [1, 3]), (4, 30, [1, 2])])
+def test_random_steps_that_run_short(cuda_lib, page, n_pages, cands):
+    """Random steps, forks and ends on a pool that has too few pages for many of them; requests that share a partly filled page are
+    refused among them."""
+    rng = random.Random(page)
+    r = Rig(page=page, n_pages=n_pages, width=max(3, 60 // page), L=2)
+    n, plain, seen = len(r.m.ctx), r.m.reserve, []
+
+    def reserve(rows):
+        held = [r.m.table[b][r.m.ctx[b] // page] for b in range(n) if rows[b] and r.m.ctx[b] % page]
+        shared = {p for p in held if r.m.ref[p] > 1}
+        parts = [r.m.table[b][r.m.ctx[b] // page] if r.m.ctx[b] % page else -1 for b in range(n)]
+        granted, short, wide = plain(rows)
+        seen.append((short, any(rows[b] and not granted[b] and parts[b] in shared for b in range(n))))
+        return granted, short, wide
+
+    r.m.reserve = reserve
+    for _ in range(30):
+        r.step(rng, cands)
+        if rng.random() < 0.5:
+            which = rng.sample(range(n), rng.randint(1, 4))
+            api.sv_cache_free(*r.args(), r.i32(which), status=r.status)
+            r.m.free(which)
+            assert r.bits() == 0
+        empty, live = [b for b in range(n) if not r.m.ctx[b]], [b for b in range(n) if r.m.ctx[b]]
+        if empty and live:
+            dst = rng.sample(empty, rng.randint(1, len(empty)))
+            src = [rng.choice(live) for _ in dst]
+            api.sv_cache_fork(*r.args(), r.i32(src), r.i32(dst), status=r.status)
+            assert not r.m.fork(src, dst) and r.bits() == 0
+        r.check()
+    assert sum(s for s, _ in seen) >= 5 and (page == 1 or any(x for _, x in seen))
