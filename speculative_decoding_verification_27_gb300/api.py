@@ -534,13 +534,13 @@ def _new(make, shape, dtype, like: torch.Tensor, stream):
 
 
 def _vec(t: Optional[torch.Tensor], name: str, dtype, shape: tuple):
-    """Address of a contiguous CUDA tensor of that type and shape; None stays None."""
+    """Address of a contiguous tensor of that type and shape (whose device _on_one_device looks at); None stays None."""
     if t is None:
         return None
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {list(shape)}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on a CUDA device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
@@ -698,8 +698,8 @@ class KVCache:
 def _seqs(page_table: torch.Tensor, ctx_len: torch.Tensor) -> bytes:
     n, width = page_table.shape
     stride, step = page_table.stride()
-    if page_table.dtype != torch.int32 or not page_table.is_cuda or (step != 1 and width > 1):
-        raise ValueError("page_table must be an int32 CUDA matrix with contiguous rows")
+    if page_table.dtype != torch.int32 or (step != 1 and width > 1):
+        raise ValueError("page_table must be an int32 matrix with contiguous rows")
     return _pack_sequences(page_table.data_ptr(), stride if n > 1 else max(width, 1), width, n,
                            _vec(ctx_len, "ctx_len", torch.int32, (n,)))
 
@@ -770,9 +770,9 @@ def sv_cache_append(cache: KVCache, layer: int, k_new: torch.Tensor, v_new: torc
     want = (L, R, cache.n_kv_heads, cache.head_dim)
     strides = k_new.stride()
     if k_new.shape != want or v_new.shape != want or (v_new.stride() != strides and _steps(v_new) != _steps(k_new)) or \
-            not _heads_contiguous(k_new) or \
-            k_new.dtype != cache.k.dtype or v_new.dtype != cache.k.dtype or not k_new.is_cuda or not v_new.is_cuda:
-        raise ValueError("k_new and v_new must be CUDA tensors [n_layers, R, kv_heads, head_dim] of the cache's dtype, alike "
+            (strides[2:] != (cache.head_dim, 1) and not _heads_contiguous(k_new)) or \
+            k_new.dtype != cache.k.dtype or v_new.dtype != cache.k.dtype:
+        raise ValueError("k_new and v_new must be [n_layers, R, kv_heads, head_dim] of the cache's dtype, alike "
                          "in strides, with contiguous heads")
     _on_one_device(cache.k, k_new, v_new, page_table, ctx_len, cu_draft, cu_cand, status)
     _launch("sv_cache_append", cache.k, stream, cache._ref, int(layer), L, k_new.data_ptr(), v_new.data_ptr(),
@@ -802,12 +802,13 @@ def sv_window_attention(q: torch.Tensor, cache: KVCache, layer: int, page_table:
     and itself, whose keys and values are in their pages. Returns (out, lse);
     rows of no window keep the values of a given `out`, and are zero in one
     made here. scale: 1 / sqrt(head_dim) if None."""
-    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.dtype != cache.k.dtype or not q.is_cuda:
-        raise ValueError("q must be a CUDA tensor [R, q_heads, head_dim] of the cache's dtype")
+    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.dtype != cache.k.dtype:
+        raise ValueError("q must be [R, q_heads, head_dim] of the cache's dtype")
     R, heads, D = q.shape
     if out is None:
         out = _new(torch.zeros, (R, heads, D), q.dtype, q, stream)
-    if out.shape != q.shape or out.dtype != q.dtype or not out.is_cuda or not _heads_contiguous(q) or not _heads_contiguous(out):
+    if out.shape != q.shape or out.dtype != q.dtype or (q.stride()[1:] != (D, 1) and not _heads_contiguous(q)) or \
+            (out.stride()[1:] != (D, 1) and not _heads_contiguous(out)):
         raise ValueError("q and out must be [R, q_heads, head_dim] with contiguous heads")
     if out_lse is None and want_lse:
         out_lse = _new(torch.zeros, (R, heads), torch.float32, q, stream)
