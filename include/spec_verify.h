@@ -408,8 +408,9 @@ sv_status sv_vshard_finish(const void* jobs, int32_t B, int32_t R_t, const int32
  *                 logits: the lowest index first) and their ln p. Tokens at
  *                 -inf are no alternatives: where fewer are left the rest
  *                 is -1 and -inf.
- * One pass reads each row once; the sums are fp32 per thread, joined in
- * double.
+ * One pass reads each row once, but for rows with so many equal values among
+ * the largest that their buffer overflows (a pass more per alternative). The
+ * sums are fp32 per thread, joined in pairs of fp32.
  *
  *   logits       [R, V] dtype with row stride ld >= V elements; R >= 0. Finite
  *                or -inf; 1 <= V <= 2^30.
@@ -480,11 +481,13 @@ sv_status sv_token_logprobs(const void* logits, sv_dtype dtype, int32_t V, int64
  * Every call checks each index that it reads from the device and stays in
  * bounds: sequences it cannot serve are left as they were and set a bit in
  * `status` (a device uint32 that the caller clears, or NULL): offsets out of
- * order SV_DATA_BAD_OFFSETS, pages out of range SV_DATA_BAD_PAGE, sequence
+ * order, between a request's candidates too, SV_DATA_BAD_OFFSETS, pages out of range SV_DATA_BAD_PAGE, sequence
  * indices and lengths SV_DATA_BAD_SEQ. Calls that change a cache or its
- * sequences must not overlap others on the same cache. Results do not depend
- * on timing: pages are taken lowest index first, in the order of the
- * sequences.
+ * sequences must not overlap others on the same cache. A workspace holds what
+ * the launches of a call hand on: two calls may share it when they are
+ * enqueued one after the other on one stream, not from two host threads at
+ * once. Results do not depend on timing: pages are taken lowest index first,
+ * in the order of the sequences.
  */
 typedef struct {
   void* k;
@@ -510,7 +513,8 @@ typedef struct {
  * writes (sv_cache_reserve). dst[i] must hold nothing (ctx_len 0). The same
  * src may stand more than once. A dst that stands more than once is taken
  * by its first entry; an entry whose src is also a dst is refused. Both set
- * SV_DATA_BAD_SEQ, as do lengths or indices out of range.
+ * SV_DATA_BAD_SEQ, as do lengths or indices out of range. A source with a page
+ * out of range or without a holder is refused (SV_DATA_BAD_PAGE).
  */
 sv_status sv_cache_fork(const sv_kv_cache* cache, const sv_sequences* seqs, int32_t N,
                         const int32_t* src, const int32_t* dst, uint32_t* status, void* cuda_stream);
@@ -592,6 +596,7 @@ sv_status sv_cache_commit(const sv_kv_cache* cache, const sv_sequences* seqs, in
  *               query heads to a key-value head.
  *   workspace   sv_window_attention_workspace_size(cache, n_q_heads, R)
  *               bytes, 16-byte aligned, of any contents.
+ * q, and the scores q . k with and without the scale, must be finite in fp32.
  * Scores, the softmax statistics and the sums are fp32. With a bf16 cache the
  * weights are rounded to bf16 for the product with V (as V is), their sum is
  * not. Keys and values of the tokens a window holds must be finite; what lies

@@ -13,12 +13,12 @@
 // 4096 tokens, 8 key-value heads, one token to 32 of them; the copy rate would
 // read heads of 128 in 159 us, of 64 in 79):
 //   bf16, up to 16 or 32 rows, and up to 64 with heads of 128
-//     window_mma_kernel: 187-195 us for heads of 128 (5.5 - 5.7 TB/s) up to
-//     32 rows, 240 us for 64; heads of 64: 118-123 us;
+//     window_mma_kernel: 184-190 us for heads of 128 (5.7 - 5.9 TB/s) up to
+//     32 rows, 240-244 us for 64; heads of 64: 111-117 us;
 //   bf16, more rows
-//     window_tc_kernel, tiles of 128 rows: 240 us (heads of 128) and 140 us (of
+//     window_tc_kernel, tiles of 128 rows: 242 us (heads of 128) and 138 us (of
 //     64) for 128 rows, where the other took 476 and 293 us. With 64 rows its
-//     tiles are half empty and it takes as long: heads of 64 138 us against
+//     tiles are half empty and it takes as long: heads of 64 136 us against
 //     158, heads of 128 240 against 240;
 //   fp32, row tiles of 4, 8, 16 or 32   window_fma_kernel.
 // Sums of a split request are joined by join_kernel.
@@ -481,6 +481,8 @@ __global__ void __launch_bounds__(Shape<D, WM>::kT, Shape<D, WM>::kCtas) window_
         m_run[1] = m_new[1];
       }
       // A row that has seen nothing yet keeps -inf scores: with an offset of 0 their weights are 0.
+      // The product takes the weights in V's type; their sum keeps 32 bits. Against 64 bits the output is 0.0018 off, where
+      // rounding the exact one to bf16 gives 0.0017 (weights kept in 32 bits would need a product of two parts, twice the work).
       const float off0 = m_run[0] == -INFINITY ? 0.f : __fmul_rn(m_run[0], P.scale_log2);
       const float off1 = m_run[1] == -INFINITY ? 0.f : __fmul_rn(m_run[1], P.scale_log2);
       uint32_t pa[KS / 16][4];
@@ -1010,7 +1012,9 @@ __global__ void __launch_bounds__(TcShape<D>::kT, TcShape<D>::kCtas) window_tc_k
 #pragma unroll
         for (int j = 4; j < 32; ++j) most[j & 3] = fmaxf(most[j & 3], fmaxf(__uint_as_float(s[0][j]), __uint_as_float(s[1][j])));
         const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-        // The reference moves where the maximum is 2^8 above it. Before a row's first token there is nothing to rescale.
+        // The reference moves where the maximum is 2^8 above it: the weights, rounded to bf16 as in the kernel above, then reach
+        // 2^8 instead of one (that rounding is relative; 0.0022 off 64 bits in all). Before a row's first token there is nothing
+        // to rescale.
         float f = 1.f;
         if (m == -INFINITY) {
           m = top;
@@ -1189,15 +1193,15 @@ __device__ __forceinline__ void sum_halves(float* s, int i) {
 
 // Bound by the bytes up to 8 rows and by the fp32 pipes' instructions and the
 // latencies around them above. A tile's scores: a thread holds 8 rows x 4 keys
-// and every DP-th piece of d, 12 reads of shared memory for 128 multiply-adds
-// sum_halves leaves it DP times fewer
-// scores, whose maxima go over the warp and over the warps that share the rows;
-// sums of weights stay with their keys until the unit ends. The product with
-// V: 8 rows x 4 elements a thread. K is loaded while the weights and the
-// product with V are computed and V behind it, so that a CTA needs one tile of each
-// and two or more CTAs fit an SM. 64 requests of 1000 tokens, 8 heads of 64
-// (32 requests for 128), 262 MB: 4 rows 64 us (64), 8 rows 68 (68), 16 rows 89
-// (84), 32 rows 132 (125), 128 rows 500 (465: 37 TFLOP/s).
+// and every DP-th piece of d, 12 reads of shared memory for 128 multiply-adds;
+// sum_halves leaves it DP times fewer scores, whose maxima go over the warp
+// and over the warps that share the rows; sums of weights stay with their keys
+// until the unit ends. The product with V: 8 rows x 4 elements a thread. K is
+// loaded while the weights and the product with V are computed and V behind
+// it, so that a CTA needs one tile of each and two or more CTAs fit an SM. 64
+// requests of 1000 tokens, 8 heads of 64 (32 requests for 128), 262 MB: 4 rows
+// 64 us (64), 8 rows 68 (68), 16 rows 89 (84), 32 rows 132 (125), 128 rows 500
+// (465: 37 TFLOP/s).
 // Packed pairs of multiply-adds were no faster (their sums take twice the
 // registers), nor were four CTAs an SM with heads of 64.
 template <int D, int MT>

@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kR) reserve_kernel(CacheView C, SeqView S, Win
     const int w = w0 + tid;
     const uint32_t bits = w0 == 0 ? bits0 : free_word(w);
     const int mine = __popc(bits);
-    int sum = min(avail, INT_MAX), first = word_first;
+    int sum = avail, first = word_first;
     if (n_words > kR) first = block_excl_scan(mine, s_warp, sum);
     s_word_first[tid] = first;
     s_bits[tid] = bits;

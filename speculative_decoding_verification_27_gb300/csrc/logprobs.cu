@@ -22,11 +22,11 @@
 // the hits and cost more than they did, and raising it less often did too.
 //
 // Bound by the bytes for long rows: 2048 rows of V = 151936 bf16 without
-// alternatives take 113 us (81% of the copy rate), with 20 of them 140; the
-// benchmark batch's 1150 committed rows with rank and 20 alternatives 92 us
+// alternatives take 113 us (81% of the copy rate), with 20 of them 141; the
+// benchmark batch's 1150 committed rows with rank and 20 alternatives 93 us
 // (52 us of bytes). A row's end is a chain of short steps (about 10 us beside
 // three other rows on the SM): it weighs on short rows, 2816 rows of V = 32000
-// bf16 taking 50 us without and 74 with alternatives (27 us of bytes). Four
+// bf16 taking 49 us without and 75 with alternatives (27 us of bytes). Four
 // CTAs an SM with four loads a batch beat 3 and 5 CTAs and 2 to 8 loads.
 #include "../../include/spec_verify.h"
 #include "sv_device.cuh"
