@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(Shape8<D, N>::kT, Shape8<D, N>::kCtas) window_
             ref = fmaxf(fmaxf(fmaxf(s_red[0][g][0][lane], s_red[0][g][1][lane]), fmaxf(s_red[0][g][2][lane], s_red[0][g][3][lane])) -
                             my_off[lane],
                         old);
-            my_off[lane] = ref == -INFINITY ? kHead : kHead - ref;
+            my_off[lane] = kHead - ref;  // (inf for a row that has seen nothing: whatever it sees next moves the reference)
             my_f[lane] = factor(old, ref, 1.f);
           }
           __syncwarp();
@@ -606,6 +606,8 @@ __global__ void __launch_bounds__(Shape8<D, N>::kT, Shape8<D, N>::kCtas) window_
         __syncwarp();
         move = *(volatile int*)&s_over[g][i & 3] != 0;
         if (!move) break;
+        if (lane < RG && ref == -INFINITY) my_off[lane] = 0.f;
+        __syncwarp();
         load_scores();
       }
 #pragma unroll

@@ -7,7 +7,7 @@ import torch
 
 from speculative_decoding_verification_27_gb300 import api, build
 from test_attention import BF, F32, INF, Case
-from test_attention8 import E8, Case8
+from test_attention8 import E8, Case8, late_candidates
 from test_cache import FAKE, ODD, _cache, _seqs
 
 
@@ -149,6 +149,14 @@ def test_peaked_rows_and_scales(cuda_lib, dtype, Hq, scale, heavy):
     if dtype == E8:
         c.dequantise()
     check(c, **({} if scale is None else {"scale": scale}))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("low", [False, True])
+@pytest.mark.parametrize("Hq,D", [(2, 64), (4, 128)])
+def test_rows_that_see_nothing_of_the_first_tiles(cuda_lib, Hq, D, low):
+    """Behind the prefix, rows whose own tokens begin a tile or more into their windows."""
+    check(share(late_candidates(Hq, D, low, prefix=200), [(0, 40, 200)]), **({"scale": 0.5} if low else {}))
 
 
 @pytest.mark.gpu
