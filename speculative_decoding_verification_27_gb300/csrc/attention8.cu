@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(Shape8<D, N>::kT, Shape8<D, N>::kCtas) window_
         if (group_any(g, dead)) goto out;
         const bool from_start = T.flags & 4, split = (T.flags & 6) != 6;
         const int rows = min(N, T.rows) - row0;                 // of the group
-        const bool based = T.first > 0 && from_start;           // goes on from what the first pass found
+        const bool based = T.first > 0 && from_start && rows > 0;  // goes on from what the first pass found (a group without a row has none)
         const bool wide = split || P.groups;                    // fp32 sums, or the output itself
         if (lane < RG) {
           float* part = reinterpret_cast<float*>(L.part + (size_t)(blockIdx.x * 2 + (from_start ? 1 : 0)) * part_bytes<D, N>());

@@ -161,6 +161,29 @@ def test_rows_that_see_nothing_of_the_first_tiles(cuda_lib, Hq, D, low):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,last", [(8, [[3], [1]]), (24, [[1]]), (4, [[5, 4], [2]])])
+def test_last_windows_of_few_rows(cuda_lib, dtype, D, Hq, last):
+    """Windows that leave half of a row tile empty, the batch's last ones, with no row behind them and a workspace of just the size
+    that is asked for: the half without a row has nothing in it."""
+    rows = 64 // Hq
+    c = make(dtype, [150, 140, 201, 170, 141, 139, 144][: 5 + len(last)], [[rows + b % 2] for b in range(5)] + last, Hq, 1, D, 16,
+             [(0, 5 + len(last), 139)], seed=D + Hq, spare=0)
+    c.run()
+    nbytes = api.load().sv_prefix_attention_workspace_size(c.args[1]._ref, Hq, c.R, len(c.ctx), 1)
+    check(c, workspace=torch.empty(nbytes, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("low", [False, True])
+@pytest.mark.parametrize("Hq,D", [(8, 64), (8, 128)])
+def test_rows_that_see_nothing_in_two_halves(cuda_lib, Hq, D, low):
+    """Row tiles of 64, whose halves move their references by themselves."""
+    check(share(late_candidates(Hq, D, low, prefix=200), [(0, 40, 200)]), **({"scale": 0.5} if low else {}))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("layout,q_pad", [("hnd", 0), ("both", 64)])
 def test_layouts_and_strides(cuda_lib, dtype, layout, q_pad):
     check(make(dtype, [140, 203, 150, 141], [[4], [2, 3], [1], [6]], 8, 4, 64, 16, [(0, 2, 140), (2, 4, 141)], seed=3, layout=layout, q_pad=q_pad))
