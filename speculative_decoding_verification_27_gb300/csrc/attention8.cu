@@ -102,18 +102,6 @@ __device__ __forceinline__ float join_lanes(const float (&v)[N], char* buf, int 
   return x;
 }
 
-// Whether any thread of a softmax group says so; a barrier of its 128 threads.
-template <int kId>
-__device__ __forceinline__ bool barrier_any(bool x) {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.cta.red.or.pred p, %2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(r) : "r"((uint32_t)x), "n"(kId) : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ bool group_any(int g, bool x) {  // (barriers by number: by a register a CTA would take all sixteen)
-  return g == 0 ? barrier_any<1>(x) : barrier_any<2>(x);
-}
-
 constexpr int kTK8 = 128;     // tokens of a key tile: the rows of S^T
 constexpr float kHead = 2.f;  // weights are 2^2 at the reference
 
@@ -147,6 +135,7 @@ struct Bars8 {
   uint64_t q_full[2], q_empty[2];
   uint64_t o_free;                 // a unit's O^T has been read
   uint64_t checked[2];             // a softmax group's threads have looked at their scores
+  uint64_t met[2];                 // a softmax group's threads have come to a unit's end, or to a move of the reference
   uint64_t looked[S + 2];          // a tile's byte offsets are written
   uint64_t end;                    // every product has ended
 };
@@ -175,8 +164,9 @@ static __device__ __noinline__ bool wait_asleep(uint32_t bar, uint32_t parity, v
 //   1 warp       the tiles of V;
 //   the last     issues the products, S^T of a tile, then O^T of the one
 //                before it. K's place is free a softmax earlier than V's.
-// Every wait is bounded, as in window_tc_kernel. A softmax group's threads
-// agree at a barrier on whether to go on, so that none waits for one that left.
+// Every wait is bounded, as in window_tc_kernel, a softmax group's for one
+// another too: a warp whose wait gave up leaves, and the others' waits give up
+// behind it.
 //
 // Only the warps of K walk over the units: what the others need to know of a
 // tile lies in a ring beside its offsets. (With a cursor in every role the
@@ -230,6 +220,7 @@ __global__ void __launch_bounds__(Shape8<D, N>::kT, Shape8<D, N>::kCtas) window_
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&bars.checked[i]), 128);
+      mbar_init(smem_addr(&bars.met[i]), 128);
       mbar_init(smem_addr(&bars.s_full[i]), 1);
       mbar_init(smem_addr(&bars.p_ready[i]), G * 128);
       mbar_init(smem_addr(&bars.o_done[i]), 1);
@@ -465,8 +456,8 @@ __global__ void __launch_bounds__(Shape8<D, N>::kT, Shape8<D, N>::kCtas) window_
     const int g = G == 1 ? 0 : warp >> 2, wq = warp & 3, tok = tid & 127, row0 = g * RG;  // the group, the token, the group's first row
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     const uint32_t o_addr = tmem + lanes + row0;
-    bool fresh = true, dead = false;
-    int unit = 0, phase = 0;
+    bool fresh = true;
+    int unit = 0, phase = 0, met_phase = 0;
     float top_v = 0.f, ref = -INFINITY;  // M, and the reference of the group's row `lane`
     f2_t l[RG / 2];                      // the rows' sums over the thread's tokens
 #pragma unroll
@@ -475,6 +466,13 @@ __global__ void __launch_bounds__(Shape8<D, N>::kT, Shape8<D, N>::kCtas) window_
     // To join lanes: in the place of P^T, where no product reads and no thread of the group writes it, or beside the other group's.
     char* my_buf = smem + 4 * Sh::kQ + (G == 1 ? 0 : 4 * Sh::kP + S * 2 * Sh::kTile + R * 2 * TK * 4) + warp * (128 * RG);
     static_assert(G > 1 || 4 * 128 * RG <= 4 * Sh::kP, "P^T has room for every warp");
+    // A barrier of the group's threads; false, for the whole warp, where it gave up.
+    auto meet = [&]() {
+      mbar_arrive(smem_addr(&bars.met[g]));
+      const bool ok = wait(bars.met[g], met_phase);
+      met_phase ^= 1;
+      return __all_sync(kFull, ok) != 0;
+    };
     if (lane < RG) my_off[lane] = 0.f;
     __syncwarp();
     for (int i = 0; i < n_tiles; ++i) {
@@ -482,8 +480,8 @@ __global__ void __launch_bounds__(Shape8<D, N>::kT, Shape8<D, N>::kCtas) window_
       const int b = i & 1, ring = i % R;
       // (The scales and what was written beside a unit's rows are there too: S^T waited for them. Their own barriers may have gone
       // on to a later phase.)
-      if (!wait(bars.s_full[b], (i >> 1) & 1) || (i >= 2 && !wait(bars.o_done[b], ((i >> 1) - 1) & 1))) dead = true;  // and P^T is free
-      __syncwarp();
+      const bool ok = wait(bars.s_full[b], (i >> 1) & 1) && (i < 2 || wait(bars.o_done[b], ((i >> 1) - 1) & 1));  // and P^T is free
+      if (!__all_sync(kFull, ok)) goto out;
       tc_fence_after();
       uint32_t a[RG];
       auto load_scores = [&]() {
@@ -533,14 +531,14 @@ __global__ void __launch_bounds__(Shape8<D, N>::kT, Shape8<D, N>::kCtas) window_
           // The reference moves to the rows' maxima so far, M to the largest scale; each warp finds the same.
           move = false;
           if (!fresh) {
-            if (!wait(bars.o_done[b ^ 1], ((i - 1) >> 1) & 1)) dead = true;  // O^T is at rest, and both P^T are free
-            if (group_any(g, dead)) goto out;                               // once all are through with weights that do not count
+            if (!__all_sync(kFull, wait(bars.o_done[b ^ 1], ((i - 1) >> 1) & 1))) goto out;  // O^T is at rest, and both P^T are free
+            if (!meet()) goto out;                                                           // once all are through with weights that do not count
           }
           const float mine = join_lanes<RG, true>(t, my_buf, lane);
           if (lane < RG) s_red[0][g][wq][lane] = mine;
           const uint32_t most_v = __reduce_max_sync(kFull, here ? __float_as_uint(vs) : 0u);
           if (lane == 0) s_top[g][wq] = __uint_as_float(most_v);
-          if (group_any(g, dead)) goto out;
+          if (!meet()) goto out;
           const float top =
               pow2_above(fmaxf(fmaxf(fmaxf(s_top[g][0], s_top[g][1]), fmaxf(s_top[g][2], s_top[g][3])), fmaxf(top_v, 0x1p-120f)));
           const float fv = top_v > 0.f ? top_v * pow2_inverse(top) : 1.f;
@@ -601,9 +599,8 @@ __global__ void __launch_bounds__(Shape8<D, N>::kT, Shape8<D, N>::kCtas) window_
         }
         if (checked) break;
         checked = true;
-        if (!wait(bars.checked[g], phase)) dead = true;
+        if (!__all_sync(kFull, wait(bars.checked[g], phase))) goto out;
         phase ^= 1;
-        __syncwarp();
         move = *(volatile int*)&s_over[g][i & 3] != 0;
         if (!move) break;
         if (lane < RG && ref == -INFINITY) my_off[lane] = 0.f;
@@ -621,11 +618,10 @@ __global__ void __launch_bounds__(Shape8<D, N>::kT, Shape8<D, N>::kCtas) window_
         float sums[RG];
 #pragma unroll
         for (int r = 0; r < RG / 2; ++r) f2_unpack(l[r], sums[2 * r], sums[2 * r + 1]);
-        if (!wait(bars.o_done[b], (i >> 1) & 1)) dead = true;
-        __syncwarp();
+        if (!__all_sync(kFull, wait(bars.o_done[b], (i >> 1) & 1))) goto out;
         const float mine = join_lanes<RG, false>(sums, my_buf, lane);
         if (lane < RG) s_red[1][g][wq][lane] = mine;
-        if (group_any(g, dead)) goto out;
+        if (!meet()) goto out;
         const bool from_start = T.flags & 4, split = (T.flags & 6) != 6;
         const int rows = min(N, T.rows) - row0;                 // of the group
         const bool based = T.first > 0 && from_start && rows > 0;  // goes on from what the first pass found (a group without a row has none)

@@ -320,6 +320,39 @@ def test_rope_positions_and_in_place(cuda_lib, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,rot,pairs", [(64, 32, False), (64, 16, True), (80, 48, False), (128, 64, True), (256, 32, False)])
+def test_rope_keeps_what_is_not_turned(cuda_lib, dtype, D, rot, pairs):
+    """Without norms an infinity or a NaN behind the turned elements is its element's own: every other one keeps its bits."""
+    got = []
+    for special in (False, True):
+        c = RopeCase([33, 4], [[3, 2], [6]], 6, 2, D, 8, dtype, rot, pairs, (False, False), seed=D)
+        x = c.both.view(c.R, -1, D)
+        put = torch.zeros_like(x, dtype=torch.bool)
+        for r in range(c.R):
+            put[r, r % 8, rot + r % (D - rot)] = put[r, (r + 3) % 8, rot + 5 * r % (D - rot)] = True
+        if special:
+            x[put] = torch.tensor([math.inf, -math.inf, math.nan], dtype=x.dtype).repeat(c.R)[: int(put.sum())]
+        out, status = c.run()
+        assert status == 0
+        got.append((c, out, put, x))
+    (a, out_a, put, _), (b, out_b, _, x) = got
+    q, k, v = (y.transpose(0, 1) for y in x.transpose(0, 1).split([6, 2, 2]))
+    rows = slice(0, 11)
+    assert torch.equal(out_a[rows][~put[rows, :6]], out_b[rows][~put[rows, :6]])
+    assert torch.equal(out_b[rows][put[rows, :6]].nan_to_num(3.5), q[rows][put[rows, :6]].nan_to_num(3.5))
+    table, r0 = b.table.cpu().long(), 0
+    for s, n in ((0, 5), (1, 6)):
+        t = b.ctx[s] + torch.arange(n)
+        at, now = (1, table[s, t // 8], t % 8), slice(r0, r0 + n)
+        for pool, rows, h in (("k", k, 6), ("v", v, 8)):
+            x0, x1, special = getattr(a.cache, pool).cpu()[at], getattr(b.cache, pool).cpu()[at], put[now, h: h + 2]
+            assert torch.equal(x0[~special], x1[~special])
+            assert torch.equal(x1[special].nan_to_num(3.5), rows[now][special].nan_to_num(3.5))
+        r0 += n
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF, F32, E8])
 def test_rope_single_rows_and_many_sequences(cuda_lib, dtype):
     """cu_draft of None, a row a sequence, and more rows than warps."""
