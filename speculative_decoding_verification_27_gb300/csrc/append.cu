@@ -121,8 +121,11 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
 // With each head's angles and weights applied one after another instructions
 // bound it (496 us), as with eight elements a lane, whose partners lie in
 // another lane (367 us); neighbouring parts in one lane make half sectors of
-// every access (101 us for the second).
-template <int DT, bool Q8, bool ROPE, int L, bool kPairs>
+// every access (101 us for the second). kPartly: some elements are not turned,
+// and y has no part in them, as it may be an infinity or a NaN (the same rows
+// packed side by side, half of a head turned: 282 us, and 315 by pairs, where
+// the others take 275 and 285).
+template <int DT, bool Q8, bool ROPE, int L, bool kPairs, bool kPartly>
 __global__ void __launch_bounds__(kT, ROPE ? 2 : 3) append_rows_kernel(const __grid_constant__ Params P) {
   release_stream();
   wait_for_stream();
@@ -334,7 +337,9 @@ __global__ void __launch_bounds__(kT, ROPE ? 2 : 3) append_rows_kernel(const __g
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const f2_t y = kPairs ? f2_pack(f[i / 4][i % 4 * 2 + 1], f[i / 4][i % 4 * 2]) : x[i ^ 4];
-                out2[i] = f2_fma(x[i], A[i], f2_mul(y, B[i]));
+                f2_t of_y = f2_mul(y, B[i]);
+                if (kPartly) of_y = (i < 4 ? turned0 : turned1) ? of_y : 0ull;
+                out2[i] = f2_fma(x[i], A[i], of_y);
               }
             } else {
 #pragma unroll
@@ -397,10 +402,14 @@ sv_status launch_rows(const Params& P, cudaStream_t st) {
     if (e == cudaSuccess) e = launch_overlapped(kernel, grid, kT, bytes, 1, st, P);
     return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
   };
-  static std::atomic<unsigned long long> allowed{0}, allowed_pairs{0};
-  if constexpr (ROPE)
-    if (P.pairs) return launch(append_rows_kernel<DT, Q8, true, L, true>, allowed_pairs);
-  return launch(append_rows_kernel<DT, Q8, ROPE, L, false>, allowed);
+  static std::atomic<unsigned long long> allowed[4]{};
+  if constexpr (ROPE) {
+    if (P.half && 2 * P.half < P.D)
+      return P.pairs ? launch(append_rows_kernel<DT, Q8, true, L, true, true>, allowed[3])
+                     : launch(append_rows_kernel<DT, Q8, true, L, false, true>, allowed[2]);
+    if (P.pairs) return launch(append_rows_kernel<DT, Q8, true, L, true, false>, allowed[1]);
+  }
+  return launch(append_rows_kernel<DT, Q8, ROPE, L, false, false>, allowed[0]);
 }
 template <int DT, bool Q8, bool ROPE>
 sv_status launch_lanes(const Params& P, cudaStream_t st) {
