@@ -20,6 +20,8 @@ namespace app {
 
 constexpr int kT = 256;
 constexpr int kU = 2;  // groups of heads of a warp
+template <bool ROPE>
+constexpr int kCtas = ROPE ? 2 : 3;  // an SM
 
 struct Params {
   CacheView C;
@@ -112,8 +114,8 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
 // are queries, norms and angles. L: lanes of a head.
 //
 // A warp takes up to kU groups of heads, all queries, all keys or all values,
-// of a row, and goes on to the same of other rows, two of which are on their
-// way while one is worked on. Pages are looked up for 32 rows at once. Norm
+// of a row, and goes on to the same of other rows, of which two (in fp32 one)
+// are on their way while one is worked on. Pages are looked up for 32 rows at once. Norm
 // and rotation are out = (x A + y B) / sqrt(mean x^2 + eps) with y the element
 // that x is turned with, A = g cos and B = (y's g) (+-sin): worked out once
 // for the row's heads. 64 prompts of 1000 rows, 48 heads of 128, in bf16: 262
@@ -126,7 +128,7 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
 // packed side by side, half of a head turned: 282 us, and 315 by pairs, where
 // the others take 275 and 285).
 template <int DT, bool Q8, bool ROPE, int L, bool kPairs, bool kPartly>
-__global__ void __launch_bounds__(kT, ROPE ? 2 : 3) append_rows_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(kT, kCtas<ROPE>) append_rows_kernel(const __grid_constant__ Params P) {
   release_stream();
   wait_for_stream();
   using Rg = Ring<DT, ROPE, L>;
@@ -384,14 +386,14 @@ __global__ void __launch_bounds__(kT, ROPE ? 2 : 3) append_rows_kernel(const __g
 }
 
 // Some CTAs a sequence, up to eight an SM: a warp a row's chunk of the mean window, or, where that is more CTAs than run at once,
-// four rows' (256 windows of 8 rows of 48 heads: 20 us, a row each 24; with long windows eight CTAs an SM even out their lengths:
-// 262 us, with four 322).
+// four rows' (256 windows of 8 rows of 48 heads, turned: 20 us, a row each 24; 200 windows of 6 rows of 8 heads into 8 bits, which run
+// at once: a row each 4.0 us, four 4.8; with long windows eight CTAs an SM even out their lengths: 262 us, with four 322).
 template <int DT, bool Q8, bool ROPE, int L>
 sv_status launch_rows(const Params& P, cudaStream_t st) {
   const int gy = P.S.n > 32768 ? 32768 : P.S.n, gz = P.n_layers < 64 ? P.n_layers : 64;
   const long long per = kU * (32 / L), chunks = ((ROPE ? P.n_q : 0) + per - 1) / per + 2 * ((P.C.n_heads + per - 1) / per);
   const long long items = ((long long)P.W.R + gy - 1) / gy * chunks;
-  const long long at_once = 152 * 2, each = (items + kT / 32 - 1) / (kT / 32), four = (items + kT / 8 - 1) / (kT / 8);
+  const long long at_once = 152 * kCtas<ROPE>, each = (items + kT / 32 - 1) / (kT / 32), four = (items + kT / 8 - 1) / (kT / 8);
   const long long gx = each * gy * gz > at_once ? four : each, most = (152 * 8 + (long long)gy * gz - 1) / ((long long)gy * gz);
   const long long least = (chunks + kT / 32 - 1) / (kT / 32);  // a warp for every chunk
   const long long x = gx < most ? gx : most;
