@@ -458,6 +458,15 @@ sv_status sv_token_logprobs(const void* logits, sv_dtype dtype, int32_t V, int64
  * counts the sequences that hold a page; bit p % 32 of free_bits[p / 32] is
  * set exactly where page_ref[p] is 0 (bits past n_pages are 0). A new cache
  * has page_ref 0 everywhere and those bits set.
+ * The rows that go with a cache (queries, outputs, new keys and values) have
+ * its row type: the cache's own, or bf16 with a cache of SV_E4M3. There a
+ * (layer, page, token, head) has a scale in k_scale and v_scale (strides in
+ * elements), and an element stands for its e4m3 value times its scale:
+ * sv_cache_append and sv_rope_append write the scale s = a / 448, a the
+ * largest magnitude of the head's row or 2^-100, and the values
+ * rn_e4m3(x * (448 / a)). head_dim is at most 256. Scales that a caller writes
+ * must be finite and not negative; attention takes k_scale up to 2^64 and
+ * v_scale up to 2^119. The scales of other caches are not looked at.
  *
  * sv_sequences: n sequences, sequence b with ctx_len[b] tokens in the cache.
  * Token t is in page table[b * table_stride + t / page_size], place
@@ -587,7 +596,9 @@ sv_status sv_cache_append(const sv_kv_cache* cache, int32_t layer, int32_t n_lay
  *              is left out altogether (SV_DATA_BAD_POSITION).
  *   rot_dim    a multiple of 16 up to head_dim; 0: no rotation, cos_sin may
  *              be NULL. cos_sin and its row stride: multiples of 16 bytes.
- *   eps        positive where a norm is given. Squares must stay finite.
+ *   eps        positive where a norm is given; there squares must stay
+ *              finite. Without norms an infinity or a NaN stays in its element
+ *              (and the one that is turned with it).
  *   head_dim   a multiple of 8, at most 256.
  *   q, q_out   [R, n_q_heads, head_dim] as for sv_window_attention; q_out may
  *              be q itself (with its stride), but not overlap it otherwise. k_new, v_new,
@@ -647,8 +658,10 @@ sv_status sv_cache_commit(const sv_kv_cache* cache, const sv_sequences* seqs, in
  * q, and the scores q . k with and without the scale, must be finite in fp32.
  * Scores, the softmax statistics and the sums are fp32. With a bf16 cache the
  * weights are rounded to bf16 for the product with V (as V is), their sum is
- * not; with a cache of SV_E4M3 the weights times V's scales are off by 2^-8 of
- * themselves, or by 2^-16 relative to the largest weight and scale. Keys and values of the tokens a window holds must be finite; what lies
+ * not; with a cache of SV_E4M3 the weights times V's scales are off by 2^-8 + 2^-11
+ * of themselves, or by 2^-16 relative to the row's largest weight and twice
+ * the largest of V's scales (of all tokens with a page, seen by the row or
+ * not), and scale * q must be finite too. Keys and values of the tokens a window holds must be finite; what lies
  * in the pages behind it may be anything. A page out of range in a
  * sequence's table hides its tokens (SV_DATA_BAD_PAGE); a row that sees no
  * token gives out = 0 and lse = -inf. SV_DEV_COPY_TIMEOUT in status: a bounded

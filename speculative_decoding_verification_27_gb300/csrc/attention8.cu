@@ -24,9 +24,12 @@
 // cores' 128 rows are full however few rows a window has. With mma.sync (e4m3
 // is taken apart into f16 there, two instructions and the conversions for one
 // product) the benchmark batch's windows over 1024 - 4096 tokens took 527 us;
-// this way 378, of which the bytes at the copy rate are 212. What bounds it is
+// this way 389, of which the bytes at the copy rate are 212. What bounds it is
 // the chain of a tile in a CTA (S^T, its 128 maxima and weights a thread, their
-// two terms, O^T): about 3500 cycles, two CTAs an SM.
+// two terms, O^T), about 3500 cycles, two CTAs an SM, and what a unit takes to
+// begin and to end, 7 - 9 us of a CTA: the same keys as 32 windows over 20480
+// tokens, 256 over 2560 and 1024 over 640 take 257, 312 and 457 us (135 tiles a
+// CTA in 0.8, 6.7 and 27 units).
 //
 // Windows of more than 64 rows go to window_tc_kernel, which takes a tile as
 // f16 under 128 rows at once.

@@ -491,8 +491,9 @@ cudaError_t launch_shares(void (*kernel)(Params, Plan), const Params& P, const P
   const int grid = 152 * Sh::kCtas;
   cudaError_t e = allow_smem(kernel, Sh::smem, allowed);
   if (e == cudaSuccess) e = launch_overlapped(kernel, dim3(grid), Sh::kT, Sh::smem, 1, st, P, L);
-  // Blocks side by side for a unit's rows: some, or, where there are so few units that each is cut into many parts, more (16
-  // forks of 4096 tokens, 64 stacked rows in 38 parts a head: 37 us with eight, 24 with 64, whose blocks cost more than they help).
+  // Blocks side by side for a unit's rows: some, or, where the units are so few that a share holds an eighth of one at most, up to
+  // sixteen. 16 forks of 4096 tokens (64 stacked rows, 38 parts a head), a whole call of sv_prefix_attention: 8 blocks 52 us, 16 43,
+  // 32 42, 64 48; 5 groups of 3 in fp32, where a block has less to do: 38, 39, 46, 55.
   const int some = Sh::MT <= 16 ? 4 : Sh::MT <= 64 ? 8 : 16, all = (int)(L.rows < 16 ? L.rows : 16);
   const int rows = (long long)P.n_req * P.C.n_heads * 8 <= grid && all > some ? all : some;
   if (e == cudaSuccess)
