@@ -465,8 +465,10 @@ sv_status sv_token_logprobs(const void* logits, sv_dtype dtype, int32_t V, int64
  * sv_cache_append and sv_rope_append write the scale s = a / 448, a the
  * largest magnitude of the head's row or 2^-100, and the values
  * rn_e4m3(x * (448 / a)). head_dim is at most 256. Scales that a caller writes
- * must be finite and not negative; attention takes k_scale up to 2^64 and
- * v_scale up to 2^119. The scales of other caches are not looked at.
+ * must be finite and not negative; for attention all are at most 2^64. The
+ * calls that append need strides that tell the scales apart (not 0 over more
+ * than one layer, page, token or head). The scales of other caches are not
+ * looked at.
  *
  * sv_sequences: n sequences, sequence b with ctx_len[b] tokens in the cache.
  * Token t is in page table[b * table_stride + t / page_size], place

@@ -661,8 +661,7 @@ class KVCache:
     With k and v of float8_e4m3fn, k_scale and v_scale are float32 views
     [n_layers, n_pages, page_size, n_kv_heads] with equal strides in any order
     (fastest where a head's scales of a page lie together; made here in that
-    order if None), finite, not negative, and for attention at most 2^64 of
-    K and 2^119 of V. The rows that go with such a cache are bfloat16:
+    order if None), finite, not negative, and for attention at most 2^64. The rows that go with such a cache are bfloat16:
     `row_dtype`, for the other caches their own type."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, page_ref=None, free_bits=None, *, k_scale=None, v_scale=None):

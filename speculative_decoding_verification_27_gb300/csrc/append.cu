@@ -442,7 +442,8 @@ extern "C" sv_status sv_rope_append(const sv_kv_cache* cache, int32_t layer, con
   app::Params P{};
   if (!cache_view(cache, &P.C) || !seq_view(seqs, &P.S) || !window_view(P.S.n, n_cand, cu_draft, cu_cand, R, &P.W))
     return SV_ERR_INVALID_ARG;
-  if (!rope || layer < 0 || layer >= P.C.n_layers || n_q_heads < 1 || n_q_heads > (1 << 16) || (uintptr_t)status % 4)
+  if (!rope || layer < 0 || layer >= P.C.n_layers || n_q_heads < 1 || n_q_heads > (1 << 16) || (uintptr_t)status % 4 ||
+      !scales_apart(P.C))
     return SV_ERR_INVALID_ARG;
   const int es = row_elem_size(cache->dtype), D = cache->head_dim;
   if (D % 8 || D > 256) return SV_ERR_INVALID_ARG;

@@ -666,7 +666,7 @@ sv_status sv_cache_append(const sv_kv_cache* cache, int32_t layer, int32_t n_lay
   if (!cache_view(cache, &C) || !seq_view(seqs, &S) || !window_view(S.n, n_cand, cu_draft, cu_cand, R, &W) ||
       !cache::aligned4(status))
     return SV_ERR_INVALID_ARG;
-  if (layer < 0 || n_layers < 0 || layer > C.n_layers - n_layers) return SV_ERR_INVALID_ARG;
+  if (layer < 0 || n_layers < 0 || layer > C.n_layers - n_layers || !scales_apart(C)) return SV_ERR_INVALID_ARG;
   const int es = row_elem_size(cache->dtype);
   if (new_layer_stride < 0 || new_row_stride < 0 || new_layer_stride > INT64_MAX / 4 || new_row_stride > INT64_MAX / 4 ||
       new_layer_stride * es % 16 || new_row_stride * es % 16)

@@ -81,6 +81,12 @@ inline bool cache_view(const sv_kv_cache* c, CacheView* out) {
   return true;
 }
 
+// Whether a call may write the scales: each (layer, page, token, head) has one of its own, as far as strides of zero tell.
+inline bool scales_apart(const CacheView& C) {
+  return !C.ks || !((C.n_layers > 1 && !C.s_layer) || (C.n_pages > 1 && !C.s_page) || (C.page_size > 1 && !C.s_token) ||
+                    (C.n_heads > 1 && !C.s_head));
+}
+
 inline bool seq_view(const sv_sequences* s, SeqView* out) {
   if (!s || s->n < 0 || s->table_pages < 1 || s->table_stride < s->table_pages) return false;
   if (s->n > 0 && (!s->table || !s->ctx_len || (uintptr_t)s->table % 4 || (uintptr_t)s->ctx_len % 4)) return false;

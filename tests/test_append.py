@@ -75,6 +75,18 @@ def test_rope_in_place_has_one_stride(lib):
     assert _rope(lib, qs=256, os=264, R=0) == OK
 
 
+def test_appends_write_no_common_scales(lib):
+    """Scales that several places share (strides of zero) may be read by attention, not written row by row."""
+    E, OK = api.SV_ERR_INVALID_ARG, api.SV_OK
+    calls = test_cache._calls(lib)
+    one = dict(n_layers=1, n_pages=1, page_size=1, n_kv_heads=1)
+    for c, size in ((dict(sl=0), "n_layers"), (dict(sp=0), "n_pages"), (dict(st=0), "page_size"), (dict(sh=0), "n_kv_heads")):
+        assert calls[3](cache=_cache(**c), R=0) == E and _rope(lib, cache=_cache(**c), R=0) == E
+        alone = _cache(**{**one, **c})
+        assert calls[3](cache=alone, n_layers=1, R=0) == OK and _rope(lib, cache=alone, R=0) == OK, size
+        assert lib.sv_window_attention(FAKE, 256, 4, 0, _cache(**c), 0, _seqs(), 3, FAKE, None, 0.1, FAKE, 256, None, FAKE, 1 << 30, None, None) == OK
+
+
 def test_rope_as_bytes():
     """The binding packs the description as the library reads it."""
     want = bytes(api._Rope(0x1230, 64, 100, 48, 1, 1e-5, 0x4560, 0x7890, 0xabc0))
